@@ -21,14 +21,20 @@ DS4HC_ERR_UNSUPPORTED = 2
 DS4HC_ERR_HIP = 3
 DS4HC_F32 = 0
 DS4HC_BF16 = 1
+DS4HC_F16 = 2
 DS4HC_FLAG_DETERMINISTIC = 1
 DS4HC_FLAG_FORCE_ROWRES = 2
 DS4HC_FLAG_FORCE_SPLITK = 4
 DS4HC_FLAG_FORCE_TILE = 8
+DS4HC_ROPE_HALF = 1
+DS4HC_ROPE_INVERSE = 2
+DS4HC_ATTN_FULL = 1
 
 EXPORTED = ("ds4hc_pre", "ds4hc_sinkhorn", "ds4hc_post", "ds4hc_fused", "ds4hc_workspace_bytes",
             "ds4hc_post_pre", "ds4hc_post_pre_workspace_bytes", "ds4hc_post_pre_noalloc",
             "ds4hc_partials", "ds4hc_partials_workspace_bytes", "ds4hc_combine",
+            "ds4hc_rope", "ds4hc_rope_frequencies", "ds4hc_latent_append", "ds4hc_latent_attn",
+            "ds4hc_latent_attn_workspace_bytes", "ds4hc_latent_prefill",
             "ds4hc_status_string", "ds4hc_last_hip_error", "ds4hc_abi_version")
 
 
@@ -44,6 +50,19 @@ class Ds4hcError(RuntimeError):
 class Params(ctypes.Structure):
     _fields_ = [("n_hc", ctypes.c_int32), ("d", ctypes.c_int32), ("rms_eps", ctypes.c_float),
                 ("sinkhorn_iters", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class Strides(ctypes.Structure):
+    """ds4hc_strides: elements between tokens and between heads."""
+    _fields_ = [("token", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class PagedCache(ctypes.Structure):
+    """ds4hc_paged_cache: the cache's layout and the batch of sequences of a call."""
+    _fields_ = [("dtype", ctypes.c_int), ("d_latent", ctypes.c_int32), ("d_rope", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p)]
 
 
 def make_params(n_hc: int, d: int, rms_eps: float = 1e-6, sinkhorn_iters: int = 20,
@@ -73,6 +92,18 @@ def load(path: str = LIB_PATH):
     lib.ds4hc_post_pre_noalloc.argtypes = [P, i64, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.ds4hc_partials.argtypes = [P, i64, ctypes.c_int, vp, vp, vp, vp, sz, vp]
     lib.ds4hc_combine.argtypes = [P, i32, i64, ctypes.c_int, i32, vp, vp, vp, vp, vp, vp, vp, vp]
+    u32, f32, f64, dt = ctypes.c_uint32, ctypes.c_float, ctypes.c_double, ctypes.c_int
+    C, S = ctypes.POINTER(PagedCache), Strides
+    lib.ds4hc_rope.argtypes = [i64, i32, i32, dt, vp, S, vp, vp, f32, u32, vp, S, vp]
+    lib.ds4hc_rope_frequencies.argtypes = [i32, f64, f64, i64, f64, f64, vp, vp]
+    lib.ds4hc_latent_append.argtypes = [C, i64, dt, vp, i64, vp, f32, vp, vp, f32, u32, vp, vp]
+    lib.ds4hc_latent_attn.argtypes = [C, i64, i32, f32, vp, S, vp, S, vp, vp, i32, vp, S, vp, vp, sz, vp]
+    lib.ds4hc_latent_attn_workspace_bytes.argtypes = [C, i64, i32]
+    lib.ds4hc_latent_attn_workspace_bytes.restype = sz
+    lib.ds4hc_latent_prefill.argtypes = [i64, i64, i32, i32, dt, f32, u32, vp, vp, vp, i64, vp, vp, vp, vp, vp]
+    for f in ("ds4hc_rope", "ds4hc_rope_frequencies", "ds4hc_latent_append", "ds4hc_latent_attn",
+              "ds4hc_latent_prefill"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("ds4hc_pre", "ds4hc_sinkhorn", "ds4hc_post", "ds4hc_fused", "ds4hc_post_pre",
               "ds4hc_post_pre_noalloc", "ds4hc_partials", "ds4hc_combine"):
         getattr(lib, f).restype = ctypes.c_int
@@ -416,3 +447,218 @@ def ds4hc_post_pre_noalloc(X, coeffs_prev, layer_out, W_next, bias_next, X_out, 
                                       _ptr(coeffs), _ptr(logits), _stream(stream)),
            "ds4hc_post_pre_noalloc")
     return X_out, layer_in, coeffs, logits
+
+
+# ------------------------------------------------------------------ operators of an attention site
+
+def ds4hc_rope_raw(N, heads, dim, dtype, x, x_strides, positions, inv_freq, amplitude, flags, y,
+                   y_strides, stream):
+    return load().ds4hc_rope(int(N), int(heads), int(dim), int(dtype), x, Strides(*x_strides),
+                             positions, inv_freq, float(amplitude), int(flags), y,
+                             Strides(*y_strides), stream)
+
+
+def ds4hc_latent_append_raw(c, N, src_dtype, kv, kv_stride, norm_weight, rms_eps, positions,
+                            inv_freq, amplitude, flags, cache, stream):
+    return load().ds4hc_latent_append(ctypes.byref(c), int(N), int(src_dtype), kv, int(kv_stride),
+                                      norm_weight, float(rms_eps), positions, inv_freq,
+                                      float(amplitude), int(flags), cache, stream)
+
+
+def ds4hc_latent_attn_raw(c, N, heads, scale, ql, ql_strides, qr, qr_strides, cache, tree_mask,
+                          mask_words, out, out_strides, lse, ws, ws_bytes, stream):
+    return load().ds4hc_latent_attn(ctypes.byref(c), int(N), int(heads), float(scale), ql,
+                                    Strides(*ql_strides), qr, Strides(*qr_strides), cache,
+                                    tree_mask, int(mask_words), out, Strides(*out_strides), lse,
+                                    ws, int(ws_bytes), stream)
+
+
+def ds4hc_latent_attn_workspace_bytes(c: PagedCache, N: int, heads: int) -> int:
+    return int(load().ds4hc_latent_attn_workspace_bytes(ctypes.byref(c), int(N), int(heads)))
+
+
+def ds4hc_latent_prefill_raw(N, S, n_seqs, heads, dtype, scale, flags, q, kv, k_rope, k_rope_stride,
+                             cu_q, cu_k, out, lse, stream):
+    return load().ds4hc_latent_prefill(int(N), int(S), int(n_seqs), int(heads), int(dtype),
+                                       float(scale), int(flags), q, kv, k_rope, int(k_rope_stride),
+                                       cu_q, cu_k, out, lse, stream)
+
+
+def _any_code(t, name, floats=(DS4HC_F32, DS4HC_BF16, DS4HC_F16)) -> int:
+    torch = _torch()
+    code = {torch.float32: DS4HC_F32, torch.bfloat16: DS4HC_BF16, torch.float16: DS4HC_F16}.get(t.dtype)
+    if code not in floats:
+        raise TypeError(f"{name}: dtype {t.dtype} is not supported")
+    return code
+
+
+def _here(stream, **tensors):
+    """Every tensor on the device that the call's stream runs on (the library
+    launches on the calling thread's current device)."""
+    torch = _torch()
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a device tensor")
+        here = torch.cuda.current_device()
+        if t.device.index != here or (stream is not None and stream.device.index != here):
+            raise ValueError(f"{name} is on {t.device}: the call runs on the current device, "
+                             f"cuda:{here}, and so must its stream")
+
+
+def _rows(t, dims, dtype, name):
+    """A [N, heads, dim] (or [N, dim]) view whose last dimension is dense."""
+    if t.dim() != len(dims) or any(d is not None and n != d for n, d in zip(t.shape, dims)) or t.dtype != dtype:
+        raise ValueError(f"{name}: expected {tuple(dims)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+
+
+def ds4hc_rope_frequencies(dim, base=10000.0, *, factor=1.0, original_length=0, beta_fast=32.0,
+                           beta_slow=1.0, device=None):
+    """Angles a position of the dim / 2 pairs (float64 tensor) and the amplitude, for
+    ds4hc_rope and ds4hc_latent_append. factor > 1 stretches the positions: all pairs
+    alike, or with the YaRN ramp if original_length is given."""
+    torch = _torch()
+    f = torch.empty(max(int(dim) // 2, 1), dtype=torch.float64)
+    amplitude = ctypes.c_float()
+    _check(load().ds4hc_rope_frequencies(int(dim), float(base), float(factor), int(original_length),
+                                         float(beta_fast), float(beta_slow), _ptr(f),
+                                         ctypes.byref(amplitude)), "ds4hc_rope_frequencies")
+    return (f if device is None else f.to(device)), amplitude.value
+
+
+def ds4hc_rope(x, positions, inv_freq, *, interleaved=True, inverse=False, amplitude=1.0, out=None,
+               stream=None):
+    """Rotary positions. x [N, heads, dim] (float32|bfloat16|float16; a view of part of
+    a head is fine, the last dimension dense), positions [N] int64, inv_freq [dim / 2]
+    float64. out may be x itself (in place). Returns out [N, heads, dim]."""
+    torch = _torch()
+    _here(stream, x=x, positions=positions, inv_freq=inv_freq, out=out)
+    dt = _any_code(x, "x")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [N, heads, dim], got {tuple(x.shape)}")
+    N, heads, dim = x.shape
+    _rows(x, (N, heads, dim), x.dtype, "x")
+    _need(positions, (N,), torch.int64, "positions")
+    _need(inv_freq, (dim // 2,), torch.float64, "inv_freq")
+    if out is None:
+        with _on(stream):
+            out = _empty((N, heads, dim), x.dtype, x.device)
+    _rows(out, (N, heads, dim), x.dtype, "out")
+    flags = (0 if interleaved else DS4HC_ROPE_HALF) | (DS4HC_ROPE_INVERSE if inverse else 0)
+    _check(ds4hc_rope_raw(N, heads, dim, dt, _ptr(x), x.stride()[:2], _ptr(positions), _ptr(inv_freq),
+                          amplitude, flags, _ptr(out), out.stride()[:2], _stream(stream)),
+           "ds4hc_rope")
+    return out
+
+
+def _paged(cache, cu_q, kv_len, block_table):
+    torch = _torch()
+    if cache.dim() != 3 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous [pages, page_size, d_latent + 64] tensor")
+    pages, page_size, D = cache.shape
+    if kv_len.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("kv_len must be [B] and block_table [B, max_pages]")
+    B = kv_len.shape[0]
+    _need(cu_q, (B + 1,), torch.int32, "cu_q")
+    _need(kv_len, (B,), torch.int32, "kv_len")
+    _need(block_table, (B, block_table.shape[1]), torch.int32, "block_table")
+    return PagedCache(_any_code(cache, "cache", (DS4HC_BF16, DS4HC_F16)), D - 64, 64, page_size, pages, B,
+                      block_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr())
+
+
+def ds4hc_latent_append(kv, positions, inv_freq, cache, cu_q, kv_len, block_table, *,
+                        norm_weight=None, rms_eps=1e-6, interleaved=True, amplitude=1.0,
+                        stream=None):
+    """Norm, rotate and store the call's N tokens into the paged cache.
+    kv [N, d_latent + 64] (latent | rope key; rows may be strided), positions [N] int64,
+    inv_freq [32] float64, cache [pages, page_size, d_latent + 64] bfloat16|float16,
+    cu_q [B + 1], kv_len [B], block_table [B, max_pages] int32, norm_weight [d_latent]
+    float32 or None (no norm). Returns cache."""
+    torch = _torch()
+    _here(stream, kv=kv, positions=positions, inv_freq=inv_freq, cache=cache, cu_q=cu_q, kv_len=kv_len,
+          block_table=block_table, norm_weight=norm_weight)
+    c = _paged(cache, cu_q, kv_len, block_table)
+    src = _any_code(kv, "kv")
+    N, D = kv.shape[0], cache.shape[2]
+    _rows(kv, (N, D), kv.dtype, "kv")
+    _need(positions, (N,), torch.int64, "positions")
+    _need(inv_freq, (32,), torch.float64, "inv_freq")
+    if norm_weight is not None:
+        _need(norm_weight, (c.d_latent,), torch.float32, "norm_weight")
+    _check(ds4hc_latent_append_raw(c, N, src, _ptr(kv), kv.stride(0) if N > 1 else D, _ptr(norm_weight),
+                                   rms_eps, _ptr(positions), _ptr(inv_freq), amplitude,
+                                   0 if interleaved else DS4HC_ROPE_HALF, _ptr(cache), _stream(stream)),
+           "ds4hc_latent_append")
+    return cache
+
+
+def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, scale, tree_mask=None,
+                      out=None, lse=None, workspace=None, stream=None, want_lse=False):
+    """Latent attention over the paged cache, absorbed form. q_latent [N, heads, d_latent]
+    and q_rope [N, heads, 64] (strided views are fine), cache and batch as in
+    ds4hc_latent_append, tree_mask [N, words] int64 or None (causal among the call's own
+    tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None). Rows
+    behind the last sequence are left as they were."""
+    torch = _torch()
+    _here(stream, q_latent=q_latent, q_rope=q_rope, cache=cache, cu_q=cu_q, kv_len=kv_len,
+          block_table=block_table, tree_mask=tree_mask, out=out, lse=lse, workspace=workspace)
+    c = _paged(cache, cu_q, kv_len, block_table)
+    if q_latent.dim() != 3:
+        raise ValueError(f"q_latent must be [N, heads, d_latent], got {tuple(q_latent.shape)}")
+    N, heads, _ = q_latent.shape
+    _rows(q_latent, (N, heads, c.d_latent), cache.dtype, "q_latent")
+    _rows(q_rope, (N, heads, 64), cache.dtype, "q_rope")
+    words = 0
+    if tree_mask is not None:
+        words = tree_mask.shape[-1]
+        _need(tree_mask, (N, words), torch.int64, "tree_mask")
+    with _on(stream):
+        if out is None:
+            out = _empty((N, heads, c.d_latent), cache.dtype, cache.device)
+        if lse is None and want_lse:
+            lse = _empty((N, heads), torch.float32, cache.device)
+        workspace, ws_bytes = _scratch(ds4hc_latent_attn_workspace_bytes(c, N, heads), workspace, cache.device)
+    _rows(out, (N, heads, c.d_latent), cache.dtype, "out")
+    if lse is not None:
+        _need(lse, (N, heads), torch.float32, "lse")
+    _check(ds4hc_latent_attn_raw(c, N, heads, scale, _ptr(q_latent), q_latent.stride()[:2], _ptr(q_rope),
+                                 q_rope.stride()[:2], _ptr(cache), _ptr(tree_mask), words, _ptr(out),
+                                 out.stride()[:2], _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)),
+           "ds4hc_latent_attn")
+    return out, lse
+
+
+def ds4hc_latent_prefill(q, kv, k_rope, cu_q, cu_k, *, scale, causal=True, out=None, lse=None,
+                         stream=None, want_lse=False):
+    """Latent attention over expanded keys and values of a ragged batch. q [N, heads, 192],
+    kv [S, heads, 256] (128 key | 128 value elements a head), k_rope [S, 64] (rows may be
+    strided), cu_q and cu_k [B + 1] int32. Returns (out [N, heads, 128], lse [N, heads]
+    float32 or None). Rows behind the last sequence are left as they were."""
+    torch = _torch()
+    _here(stream, q=q, kv=kv, k_rope=k_rope, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
+    dt = _any_code(q, "q", (DS4HC_BF16, DS4HC_F16))
+    if q.dim() != 3 or kv.dim() != 3 or cu_q.dim() != 1:
+        raise ValueError("q must be [N, heads, 192], kv [S, heads, 256] and cu_q [B + 1]")
+    N, heads, _ = q.shape
+    S, B = kv.shape[0], cu_q.shape[0] - 1
+    _need(q, (N, heads, 192), q.dtype, "q")
+    _need(kv, (S, heads, 256), q.dtype, "kv")
+    _rows(k_rope, (S, 64), q.dtype, "k_rope")
+    _need(cu_q, (B + 1,), torch.int32, "cu_q")
+    _need(cu_k, (B + 1,), torch.int32, "cu_k")
+    with _on(stream):
+        if out is None:
+            out = _empty((N, heads, 128), q.dtype, q.device)
+        if lse is None and want_lse:
+            lse = _empty((N, heads), torch.float32, q.device)
+    _need(out, (N, heads, 128), q.dtype, "out")
+    if lse is not None:
+        _need(lse, (N, heads), torch.float32, "lse")
+    _check(ds4hc_latent_prefill_raw(N, S, B, heads, dt, scale, 0 if causal else DS4HC_ATTN_FULL, _ptr(q),
+                                    _ptr(kv), _ptr(k_rope), k_rope.stride(0) if S > 1 else 64, _ptr(cu_q),
+                                    _ptr(cu_k), _ptr(out), _ptr(lse), _stream(stream)),
+           "ds4hc_latent_prefill")
+    return out, lse

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libds4hc.so")
-SOURCES = ["hc_kernels.hip", "ds4hc_api.cpp"]
+SOURCES = ["hc_kernels.hip", "rope_kernels.hip", "latent_attn.hip", "latent_prefill.hip", "ds4hc_api.cpp",
+           "latent_api.cpp"]
 # the plain device copy bench.py measures beside the op (not part of the op's ABI)
 LIB_BW = os.path.join(PKG, "libds4hc_bw.so")
 SOURCES_BW = ["bw_copy.hip"]
@@ -54,7 +55,7 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
 
 
 def _link(sources, lib, verbose, incremental):
-    objs = []
+    objs, running = [], []
     build_dir = os.path.join(PKG, "_build")
     os.makedirs(build_dir, exist_ok=True)
     for src in [os.path.join(CSRC, s) for s in sources]:
@@ -66,7 +67,10 @@ def _link(sources, lib, verbose, incremental):
         cmd = [hipcc()] + HIPCC_FLAGS + ["-I", INCLUDE, "-I", CSRC, "-c"] + lang + [src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
+        running.append((cmd, subprocess.Popen(cmd)))  # one compiler a source, side by side
+    for cmd, p in [(cmd, p, p.wait())[:2] for cmd, p in running]:
+        if p.returncode:
+            raise subprocess.CalledProcessError(p.returncode, cmd)
     tmp = lib + ".tmp%d" % os.getpid()
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:

@@ -16,14 +16,20 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "api_common.hpp"
 #include "hc_launch.hpp"
 
 namespace {
 
+using ds4hc::aligned;
+using ds4hc::hip_fail;
+using ds4hc::MAX_T;
+using ds4hc::overlap;
+using ds4hc::Range;
+
 // T at or below which the one-pass chain step and the split-K partials of the
 // split over d are the defaults.
 constexpr int64_t SPLITK_MAX_T = 160;
-constexpr int64_t MAX_T = int64_t(1) << 24;
 constexpr int MAX_ITERS = 1000;
 constexpr uint64_t MAX_WORK_ITEMS = 0xFFFFFFFFull;  // HSA dispatch grid size is 32-bit
 // The streamed partials kernel forms 32-bit byte offsets up to 64 * n * d_s;
@@ -34,25 +40,6 @@ constexpr uint32_t FORCE_FLAGS =
 constexpr uint32_t KNOWN_FLAGS = DS4HC_FLAG_DETERMINISTIC | FORCE_FLAGS;
 
 thread_local char g_last_hip_error[256] = "";
-
-ds4hc_status hip_fail(hipError_t e) {
-    snprintf(g_last_hip_error, sizeof g_last_hip_error, "%s: %s", hipGetErrorName(e),
-             hipGetErrorString(e));
-    return DS4HC_ERR_HIP;
-}
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-struct Range {
-    const void *p;
-    uint64_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
 
 int state_bytes(ds4hc_dtype dt) { return dt == DS4HC_F32 ? 4 : 2; }
 int vec_elems(ds4hc_dtype dt) { return dt == DS4HC_F32 ? 4 : 8; }
@@ -293,6 +280,12 @@ ds4hc_status post_pre_impl(const ds4hc_params *p, int64_t T, ds4hc_dtype dtype, 
 }
 
 }  // namespace
+
+ds4hc_status ds4hc::hip_fail(hipError_t e) {
+    snprintf(g_last_hip_error, sizeof g_last_hip_error, "%s: %s", hipGetErrorName(e),
+             hipGetErrorString(e));
+    return DS4HC_ERR_HIP;
+}
 
 extern "C" {
 

@@ -86,7 +86,8 @@ typedef enum {
 
 typedef enum {
     DS4HC_F32 = 0,  /* state stored as IEEE float32 */
-    DS4HC_BF16 = 1  /* state stored as bfloat16 (uint16 bit patterns) */
+    DS4HC_BF16 = 1, /* state stored as bfloat16 (uint16 bit patterns) */
+    DS4HC_F16 = 2   /* IEEE float16: the operators of an attention site only */
 } ds4hc_dtype;
 
 /* Operation constants. Defaults: rms_eps = 1e-6f, sinkhorn_iters = 20. */
@@ -267,6 +268,198 @@ ds4hc_status ds4hc_combine(const ds4hc_params *p, int32_t d_total, int64_t T, ds
                            int32_t G, const float *partials, const float *bias, const void *X_share,
                            const void *layer_out_share, void *layer_in_share, float *coeffs_opt,
                            void *X_out_share, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Operators of an attention site: what runs between ds4hc_pre (which gives the
+ * layer input) and ds4hc_post (which takes the layer output) besides the plain
+ * projections. Attention keeps ONE shared vector a token: a latent of d_latent
+ * elements, from which every head's key and value come by a fixed projection,
+ * and a rotated key of 64 elements that all heads share.
+ *
+ *   ds4hc_rope            rotary positions of the queries' (or keys') rotated part
+ *   ds4hc_latent_append   RMS-norm of the latents, rotation of the shared keys,
+ *                         store into a paged cache
+ *   ds4hc_latent_attn     absorbed form over that cache: queries are multiplied
+ *                         into the latent space beforehand, keys and values are
+ *                         the cached vectors themselves (decode, drafted chains
+ *                         and trees, chunks of a prompt)
+ *   ds4hc_latent_prefill  expanded form: keys and values a head, from a ragged
+ *                         batch of prompts
+ *
+ * The conventions at the top hold, with these additions: strides count elements;
+ * arrays of the 16-bit types and rows of strided arrays must start on 16-byte
+ * boundaries (ds4hc_rope alone takes any element-aligned address and stride);
+ * int32 and float32 arrays need 4-byte, int64, uint64 and float64 arrays 8-byte
+ * alignment. The library allocates nothing and keeps nothing between calls.
+ *
+ * What the device arrays of lengths and pages hold is not known to the host.
+ * Every entry is checked in the kernel before it is used: cu_q and cu_k entries
+ * are taken as clamped to [0, tokens] and a sequence that would end before it
+ * starts as empty, kv_len as clamped to [0, max_pages * page_size], and tokens
+ * of a page whose block_table entry is not in [0, n_pages) as not in the cache
+ * (no query sees them, an append to them stores nothing). No value in them makes
+ * a kernel read or write outside the arrays given. Sequences of one call that
+ * overlap (cu_q that does not rise) write the shared rows in any order.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Elements between two tokens and between two heads of a [tokens, heads, dim]
+ * array whose innermost dimension is dense. Not negative. */
+typedef struct {
+    int64_t token;
+    int64_t head;
+} ds4hc_strides;
+
+/* Pairs of a rotation are (2i, 2i + 1), or (i, i + dim / 2) with DS4HC_ROPE_HALF. */
+#define DS4HC_ROPE_HALF 1u
+/* Rotate by the negative angle (the transpose: undoes the rotation, and is its
+ * gradient, up to amplitude^2). ds4hc_rope only. */
+#define DS4HC_ROPE_INVERSE 2u
+
+/*
+ * ds4hc_rope -- rotary positions. For token t, head h, pair i, with the angle
+ * a = positions[t] * inv_freq[i] formed in 64 bits:
+ *   y0 = (x0 cos a - x1 sin a) * amplitude,  y1 = (x0 sin a + x1 cos a) * amplitude
+ * in float32, one rounding at the store.
+ *   x         [N, heads, dim] strided, any of the three dtypes (read). To rotate
+ *             part of a head pass the address of that part and the strides of
+ *             the whole. Strides may be 0 (a broadcast input).
+ *   positions [N]       int64   (read; any sign)
+ *   inv_freq  [dim / 2] float64 (read; radians a position)
+ *   y         [N, heads, dim] strided, dtype of x (written: these elements only)
+ * y may be exactly x with x's strides (in place); otherwise the two may not
+ * overlap, as ranges from the first to the last element. Rows of y may not
+ * overlap one another. dim is even, 2..512; heads 1..1024; N <= 2^24.
+ */
+ds4hc_status ds4hc_rope(int64_t N, int32_t heads, int32_t dim, ds4hc_dtype dtype, const void *x,
+                        ds4hc_strides x_strides, const int64_t *positions, const double *inv_freq,
+                        float amplitude, uint32_t flags, void *y, ds4hc_strides y_strides,
+                        hipStream_t stream);
+
+/*
+ * ds4hc_rope_frequencies -- HOST function, fills the HOST arrays inv_freq
+ * [dim / 2] and *amplitude for ds4hc_rope and ds4hc_latent_append:
+ *   f_i = base^(-2i / dim)                                      (factor == 1)
+ *   f_i / factor               (factor > 1, original_length == 0: interpolated)
+ *   f_i ((1 - k_i) / factor + k_i)                (factor > 1, original_length > 0)
+ * the last with the ramp of Peng et al. 2023 ("YaRN: Efficient Context Window
+ * Extension of Large Language Models"): with turns(b) = dim ln(original_length /
+ * (2 pi b)) / (2 ln base), lo = max(floor(turns(beta_fast)), 0), hi =
+ * min(ceil(turns(beta_slow)), dim / 2 - 1),
+ *   k_i = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
+ * and amplitude = 0.1 ln(factor) + 1 (1 in the other two cases). base > 1,
+ * factor >= 1, beta_fast >= beta_slow > 0 (looked at in the last case only).
+ */
+ds4hc_status ds4hc_rope_frequencies(int32_t dim, double base, double factor,
+                                    int64_t original_length, double beta_fast, double beta_slow,
+                                    double *inv_freq, float *amplitude);
+
+/*
+ * A paged cache of latent vectors, and the batch of sequences that a call
+ * handles. The cache is [n_pages, page_size, d_latent + 64] of dtype, dense;
+ * token j of sequence b lies in page block_table[b][j / page_size], at place
+ * j % page_size. The call's tokens are ragged: sequence b has tokens
+ * cu_q[b] .. cu_q[b + 1] - 1 of the call's N, and they are the LAST tokens of
+ * its kv_len[b] tokens (token i of the call's q_len for b is token
+ * kv_len[b] - q_len + i of the sequence). Tokens of the call behind the last
+ * sequence are neither read nor written.
+ */
+typedef struct {
+    ds4hc_dtype dtype;          /* DS4HC_BF16 or DS4HC_F16 */
+    int32_t d_latent;           /* 128, 256 or 512 */
+    int32_t d_rope;             /* 64 */
+    int32_t page_size;          /* tokens a page: a power of two, 1..65536 */
+    int64_t n_pages;            /* pages of the cache, >= 1 */
+    int32_t n_seqs;             /* sequences B, 0..2^20 */
+    int32_t max_pages;          /* entries of a row of block_table, >= 1;
+                                   max_pages * page_size < 2^31 */
+    const int32_t *cu_q;        /* [B + 1] */
+    const int32_t *kv_len;      /* [B], this call's tokens included */
+    const int32_t *block_table; /* [B, max_pages] */
+} ds4hc_paged_cache;
+
+/*
+ * ds4hc_latent_append -- for each token of the call, with kv = (c | r):
+ *   c' = c / sqrt(mean(c^2) + rms_eps) * norm_weight   (c' = c if norm_weight is NULL)
+ *   r' = r rotated as by ds4hc_rope
+ * in float32, rounded once to the cache's dtype and stored at the token's place.
+ * Places before token 0 of a sequence (q_len > kv_len) are passed over. The
+ * sequences' pages that are written must differ from one another: of two tokens
+ * with one place either may be kept, in parts.
+ *   kv          [N, d_latent + 64], kv_stride elements between rows, src_dtype any
+ *               of the three (read)
+ *   positions   [N] int64, inv_freq [32] float64, amplitude, flags (DS4HC_ROPE_HALF)
+ *   norm_weight [d_latent] float32 or NULL (read)
+ *   cache       (written: the tokens' places only)
+ */
+ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dtype src_dtype,
+                                 const void *kv, int64_t kv_stride, const float *norm_weight,
+                                 float rms_eps, const int64_t *positions, const double *inv_freq,
+                                 float amplitude, uint32_t flags, void *cache, hipStream_t stream);
+
+/*
+ * ds4hc_latent_attn -- attention of the call's tokens over the cache, absorbed
+ * form. For token t of sequence b, head h, over the cached tokens j that t sees:
+ *   s_j = scale * (q_latent[t][h] . c_j + q_rope[t][h] . r_j)
+ *   out[t][h] = sum_j softmax(s)_j c_j,   lse[t][h] = ln sum_j exp(s_j)
+ * Token i of the call's q_len for b sees the cached tokens before the call's
+ * own, j < kv_len[b] - q_len, and of the call's own:
+ *   tree_mask NULL: its own place and those before it;
+ *   otherwise those whose bit is set: bit d % 64 of word tree_mask[t][d / 64]
+ *   stands for token d of the call's tokens for b (its own bit included: nothing
+ *   is implied). Tokens d >= 64 * mask_words are seen by none.
+ * A row that sees nothing gives out = 0 and lse = -infinity. A cached token that
+ * holds a value that is not finite makes the rows that see it not finite and
+ * does not touch the others.
+ *   q_latent [N, heads, d_latent], q_rope [N, heads, 64] strided, c->dtype (read)
+ *   cache    (read)
+ *   tree_mask [N, mask_words] uint64 or NULL (read; mask_words 1..1024)
+ *   out      [N, heads, d_latent] strided, c->dtype (written)
+ *   lse_opt  [N, heads] float32 or NULL (written)
+ *   workspace of ds4hc_latent_attn_workspace_bytes(c, N, heads) bytes, 16-byte
+ *            aligned (may be NULL when that is 0); as for ds4hc_pre.
+ * Products are of the 16-bit inputs and sums, softmax statistics and the running
+ * output float32; the softmax weights are rounded to the 16-bit type for the
+ * second product. scale > 0; heads 1..1024; N <= 2^24. Outputs may not overlap
+ * inputs or each other, as ranges from the first to the last element; rows of
+ * out may not overlap one another.
+ */
+ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
+                               const void *q_latent, ds4hc_strides q_latent_strides,
+                               const void *q_rope, ds4hc_strides q_rope_strides, const void *cache,
+                               const uint64_t *tree_mask, int32_t mask_words, void *out,
+                               ds4hc_strides out_strides, float *lse_opt, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes ds4hc_latent_attn needs. Pure function of the host fields (the
+ * device arrays are not looked at and may be NULL); 0 for invalid arguments. */
+size_t ds4hc_latent_attn_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, int32_t heads);
+
+/* Every query sees every key of its sequence (the default is causal). */
+#define DS4HC_ATTN_FULL 1u
+
+/*
+ * ds4hc_latent_prefill -- attention over expanded keys and values of a ragged
+ * batch. Sequence b has queries cu_q[b] .. cu_q[b + 1] - 1 and keys cu_k[b] ..
+ * cu_k[b + 1] - 1; its queries are the last of its tokens: query i sees key j if
+ * j <= i + k_len - q_len (any j with DS4HC_ATTN_FULL). With q = (qn | qr):
+ *   s_j = scale * (qn . kn_j + qr . kr_j),  out = sum_j softmax(s)_j v_j,
+ *   lse = ln sum_j exp(s_j);  a row that sees nothing gives 0 and -infinity.
+ *   q      [N, heads, 128 + 64] dense, dtype BF16 or F16 (read)
+ *   kv     [S, heads, 128 + 128] dense: kn | v of each head (read)
+ *   k_rope [S, 64], k_rope_stride elements between rows, shared by the heads (read)
+ *   cu_q, cu_k [n_seqs + 1] int32 (read)
+ *   out    [N, heads, 128] dense (written), lse_opt [N, heads] float32 or NULL (written)
+ * Rows of out and lse behind the last sequence are left as they were. Values that
+ * are not finite stay with the rows that see them, as for ds4hc_latent_attn.
+ * Rounding as for ds4hc_latent_attn. heads 1..1024, N and S <= 2^24, n_seqs <= 2^20.
+ */
+ds4hc_status ds4hc_latent_prefill(int64_t N, int64_t S, int32_t n_seqs, int32_t heads,
+                                  ds4hc_dtype dtype, float scale, uint32_t flags, const void *q,
+                                  const void *kv, const void *k_rope, int64_t k_rope_stride,
+                                  const int32_t *cu_q, const int32_t *cu_k, void *out,
+                                  float *lse_opt, hipStream_t stream);
 
 /* Static, human-readable name of a status code. */
 const char *ds4hc_status_string(ds4hc_status s);
