@@ -20,6 +20,8 @@ constexpr int MAX_HEADS = 1024;
 constexpr int MAX_ROPE_DIM = 512;
 constexpr int MAX_SEQS = 1 << 20;
 constexpr int MAX_MASK_WORDS = 1024;
+constexpr int64_t MAX_KV = int64_t(1) << 30;    // tokens of a sequence
+constexpr int64_t MAX_ROWS = int64_t(1) << 30;  // tokens x heads of a call
 constexpr int64_t MAX_STRIDE = int64_t(1) << 36;  // elements: offsets stay far inside 64 bits
 
 int elem_bytes(ds4hc_dtype dt) { return dt == DS4HC_F32 ? 4 : 2; }
@@ -59,7 +61,7 @@ ds4hc_status check_cache(const ds4hc_paged_cache *c, int64_t N) {
         (c->d_latent != 128 && c->d_latent != 256 && c->d_latent != 512))
         return DS4HC_ERR_UNSUPPORTED;
     if (c->page_size > 65536 || c->n_seqs > MAX_SEQS || N > MAX_T || c->n_pages > (int64_t(1) << 31) - 1 ||
-        (int64_t)c->max_pages * c->page_size > (int64_t(1) << 31) - 1)
+        c->n_pages * c->page_size >= (int64_t(1) << 31) || (int64_t)c->max_pages * c->page_size > MAX_KV)
         return DS4HC_ERR_UNSUPPORTED;
     return DS4HC_OK;
 }
@@ -184,7 +186,8 @@ ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t he
     if (heads < 1 || !(scale > 0.f) || !isfinite(scale) || !strides_ok(ls) || !strides_ok(rs) || !strides_ok(os))
         return DS4HC_ERR_INVALID_ARG;
     if (tree_mask && mask_words < 1) return DS4HC_ERR_INVALID_ARG;
-    if (heads > MAX_HEADS || (tree_mask && mask_words > MAX_MASK_WORDS)) return DS4HC_ERR_UNSUPPORTED;
+    if (heads > MAX_HEADS || N * heads > MAX_ROWS || (tree_mask && mask_words > MAX_MASK_WORDS))
+        return DS4HC_ERR_UNSUPPORTED;
     if (N == 0 || c->n_seqs == 0) return DS4HC_OK;
     if (!batch_arrays_ok(c) || !q_latent || !q_rope || !cache || !out) return DS4HC_ERR_INVALID_ARG;
     if (!rows_aligned16(q_latent, N, heads, ls, 2) || !rows_aligned16(q_rope, N, heads, rs, 2) ||
@@ -209,7 +212,7 @@ ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t he
 }
 
 size_t ds4hc_latent_attn_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, int32_t heads) {
-    if (check_cache(c, N) != DS4HC_OK || heads < 1 || heads > MAX_HEADS || N == 0 || c->n_seqs == 0) return 0;
+    if (check_cache(c, N) != DS4HC_OK || heads < 1 || heads > MAX_HEADS || N * heads > MAX_ROWS || N == 0 || c->n_seqs == 0) return 0;
     return (size_t)ds4hc::attn_workspace_bytes(view(c), c->d_latent, heads, N);
 }
 
@@ -223,7 +226,8 @@ ds4hc_status ds4hc_latent_prefill(int64_t N, int64_t S, int32_t n_seqs, int32_t 
     if (flags & ~DS4HC_ATTN_FULL) return DS4HC_ERR_INVALID_ARG;
     if (k_rope_stride < ds4hc::LATENT_ROPE || k_rope_stride > MAX_STRIDE || k_rope_stride % 8)
         return DS4HC_ERR_INVALID_ARG;
-    if (!half_type(dtype) || heads > MAX_HEADS || N > MAX_T || S > MAX_T || n_seqs > MAX_SEQS)
+    if (!half_type(dtype) || heads > MAX_HEADS || N > MAX_T || S > MAX_T || n_seqs > MAX_SEQS ||
+        N * heads > MAX_ROWS)
         return DS4HC_ERR_UNSUPPORTED;
     if (N == 0 || n_seqs == 0) return DS4HC_OK;
     // without keys (S = 0) every row sees nothing; kv and k_rope may then be NULL

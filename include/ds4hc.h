@@ -370,10 +370,10 @@ typedef struct {
     int32_t d_latent;           /* 128, 256 or 512 */
     int32_t d_rope;             /* 64 */
     int32_t page_size;          /* tokens a page: a power of two, 1..65536 */
-    int64_t n_pages;            /* pages of the cache, >= 1 */
+    int64_t n_pages;            /* pages of the cache, >= 1; n_pages * page_size < 2^31 */
     int32_t n_seqs;             /* sequences B, 0..2^20 */
     int32_t max_pages;          /* entries of a row of block_table, >= 1;
-                                   max_pages * page_size < 2^31 */
+                                   max_pages * page_size <= 2^30 */
     const int32_t *cu_q;        /* [B + 1] */
     const int32_t *kv_len;      /* [B], this call's tokens included */
     const int32_t *block_table; /* [B, max_pages] */
@@ -421,7 +421,7 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  *            aligned (may be NULL when that is 0); as for ds4hc_pre.
  * Products are of the 16-bit inputs and sums, softmax statistics and the running
  * output float32; the softmax weights are rounded to the 16-bit type for the
- * second product. scale > 0; heads 1..1024; N <= 2^24. Outputs may not overlap
+ * second product. scale > 0; heads 1..1024; N <= 2^24, N * heads <= 2^30. Outputs may not overlap
  * inputs or each other, as ranges from the first to the last element; rows of
  * out may not overlap one another.
  */
@@ -453,7 +453,8 @@ size_t ds4hc_latent_attn_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, 
  *   out    [N, heads, 128] dense (written), lse_opt [N, heads] float32 or NULL (written)
  * Rows of out and lse behind the last sequence are left as they were. Values that
  * are not finite stay with the rows that see them, as for ds4hc_latent_attn.
- * Rounding as for ds4hc_latent_attn. heads 1..1024, N and S <= 2^24, n_seqs <= 2^20.
+ * Rounding as for ds4hc_latent_attn. heads 1..1024, N and S <= 2^24,
+ * N * heads <= 2^30, n_seqs <= 2^20.
  */
 ds4hc_status ds4hc_latent_prefill(int64_t N, int64_t S, int32_t n_seqs, int32_t heads,
                                   ds4hc_dtype dtype, float scale, uint32_t flags, const void *q,
