@@ -207,7 +207,7 @@ ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t he
     if (clash(in, outs)) return DS4HC_ERR_INVALID_ARG;
     const ds4hc::AttnArgs a{v, (int)c->dtype, c->d_latent, heads, N, scale, q_latent, ls.token, ls.head,
                             q_rope, rs.token, rs.head, cache, tree_mask, tree_mask ? mask_words : 0, out, os.token,
-                            os.head, lse_opt, workspace};
+                            os.head, lse_opt, workspace, 0};
     return done(ds4hc::launch_attn(a, stream));
 }
 

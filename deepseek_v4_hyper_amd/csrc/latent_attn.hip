@@ -1,55 +1,74 @@
 // latent_attn.hip -- attention over the paged latent cache, absorbed form.
+//
+// Per query row (a token and a head) and cached vector (c | r) of a sequence:
+//   s = scale (ql . c + qr . r),  out = softmax(s) C,  with C the latents themselves.
+// All rows of a sequence share its vectors, so a tile of cached tokens is loaded once,
+// serves as keys and (read transposed) as values, and is used for as many rows as fit.
 #include "latent_device.hpp"
 
 namespace ds4hc {
 
 namespace {
 
-constexpr int GROUPS = 256;      // workgroups: one a CU (a tile ring fills most of its LDS)
-constexpr int JOIN_BLOCKS = 1 << 20;  // of the second kernel's grid in x (a dispatch has 2^32 threads a dimension)
-constexpr int MIN_SHARE = 2;     // tiles a workgroup takes at least
+constexpr int WORKGROUPS = 256;  // one a CU: the ring of tiles fills most of its LDS
+constexpr int XCDS = 8;          // workgroup i runs on XCD i % 8
+constexpr int EXTRA = 4;         // tiles that a batch's queries and results cost as much as
 constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
 constexpr float LAZY = 8.f;      // the running maximum is raised only by more than this (in powers of 2)
 
-// Tile shapes. ROWS query rows (a row is a token and a head; all rows of a sequence share
-// its keys) by TOKENS cached tokens, four waves. With `split` every wave has all the rows
-// and a quarter of the tokens, otherwise a quarter of the rows and all the tokens.
-template <int LATENT_, int NB_, bool SPLIT_> struct Shape {
-    static constexpr int LATENT = LATENT_, NB = NB_;  // NB: blocks of 16 rows a wave
-    static constexpr bool SPLIT = SPLIT_;
+// Tile shapes. ROWS query rows by TOKENS cached tokens; ROW_WAVES waves side by side in the
+// rows, 32 each, times SETS sets of waves that take TOKENS / SETS of the tokens each, in
+// steps of 32.
+template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape {
+    static constexpr int LATENT = LATENT_, ROW_WAVES = ROW_WAVES_, SETS = SETS_;
+    static constexpr int TOKENS = 64, BUFS = 2, STEPS = TOKENS / SETS / 32;
+    static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int D = LATENT + LATENT_ROPE;
-    static constexpr int ROWS = SPLIT ? NB * 16 : NB * 64;
-    static constexpr int TOKENS = SPLIT ? 64 : 32;
-    static constexpr int KVB = SPLIT ? 1 : 2;          // blocks of 16 tokens a wave
-    static constexpr int BUFS = SPLIT ? 2 : 4;
+    static constexpr int ROWS = ROW_WAVES * 32;
     static constexpr int ROW_BYTES = LATENT * 2;
     static constexpr int ROPE_AT = TOKENS * ROW_BYTES;
     static constexpr int TILE_BYTES = TOKENS * D * 2;
-    static constexpr int WAVE_TOKENS = TOKENS / 4;     // tokens a wave loads
     static constexpr int ROWS_A_LOAD = 1024 / ROW_BYTES;
-    static constexpr int LOADS = WAVE_TOKENS / ROWS_A_LOAD + WAVE_TOKENS / 8;  // a tile and wave
-    static constexpr int KSTEPS = LATENT / 32, DBLOCKS = LATENT / 16;
+    static constexpr int LATENT_LOADS = TOKENS / ROWS_A_LOAD, ROPE_LOADS = TOKENS / 8;  // a tile
+    static constexpr int KLATENT = LATENT / 16, KSTEPS = KLATENT + LATENT_ROPE / 16, DBLOCKS = LATENT / 32;
+    static_assert(LATENT_LOADS % WAVES == 0 && ROPE_LOADS % WAVES == 0, "the waves load alike");
 };
 
 // Swizzle: 16-byte chunk c of token row r lies at chunk c ^ swz(r) of the row's place in
-// LDS. swz takes all 16 values over 16 rows and its upper 3 bits all 8 values over 8 rows,
-// so 16 lanes that read one chunk of 16 rows, and 32 lanes that read 32 bytes of 8 rows,
-// touch every bank once.
-__device__ __forceinline__ int swz(int r) { return ((r & 7) << 1) | ((r >> 3) & 1); }
+// LDS. swz takes all 16 values over 16 rows (a lane each reads the same chunk of 16 rows),
+// and its upper 2 bits all 4 values over 4 rows (a transposing read takes 64 bytes of 4 rows
+// at a time).
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 __device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
 
 // ------------------------------------------------------------------ the split of the work
 //
-// The unit of work is a tile: TOKENS cached tokens of a sequence against one tile of its
-// rows. Units are ordered by sequence, row tile, tokens; workgroup w takes the units
-// [w * share, (w + 1) * share). Lengths are read on the device, so a captured call follows
-// them. A (sequence, row tile) that lies in one workgroup's range is written by it; of one
-// that is cut every workgroup writes its part of the sums to the workspace, and the second
+// `members` workgroups of one XCD form a cluster: they take the same cached tokens at the
+// same time (one reads them from HBM, the others from the XCD's L2), each for a row tile of
+// its own. The unit of the clusters' work is a tile of cached tokens against `members` row
+// tiles; what a (sequence, batch of row tiles) costs besides its tiles (queries, results) is
+// counted as `extra` units before them. Units are ordered by sequence, batch, tokens, and
+// cluster c takes the units [c * share, (c + 1) * share). Lengths are read on the device, so a
+// captured call follows them. A batch whose tiles lie in one cluster's range is written by it;
+// of one that is cut each cluster writes its part of the sums to the workspace, and the second
 // kernel joins the parts in order.
+//
+// Workspace: share, then where each cluster starts (for the second kernel), then a place for
+// each part: sums in the order of the lanes that hold them ([row wave][LATENT / 8][64 lanes] of
+// 4 elements, so that stores and loads are of whole lines), maxima and sums [ROWS].
+
+struct Start {
+    int b, batch, tile, pad;  // sequence (-1: the cluster has nothing to do), batch, first tile of its range
+};
+struct Header {
+    int64_t share, pad;
+    Start start[WORKGROUPS];
+};
 
 struct Seq {
     int few, len;        // tokens of the call, cached tokens
     int row_tiles, kv_tiles;
+    __device__ __forceinline__ int batches(int members) const { return (row_tiles + members - 1) / members; }
 };
 
 template <class S> __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
@@ -71,31 +90,44 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {
     return v;
 }
 
-// Every wave finds by itself: the units in all, and (if `at` >= 0 and below that) the
-// sequence that unit `at` belongs to and the unit's place in it.
+template <class S> __host__ __device__ constexpr int64_t part_floats() { return (int64_t)S::ROWS * (S::LATENT + 2); }
+template <class S> __device__ __forceinline__ float *part_at(const AttnArgs &a, int64_t cluster, int second, int member) {
+    return reinterpret_cast<float *>(static_cast<Header *>(a.ws) + 1) + ((2 * cluster + second) * a.members + member) * part_floats<S>();
+}
+
+__device__ __forceinline__ int64_t wave_sum(int64_t v) {
+    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+// Every wave finds by itself: the units in all, the share of a cluster and the extra units of a
+// batch, and (b < 0 if there is none) the sequence that the cluster's first unit belongs to and
+// its place there.
 template <class S>
-__device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, int64_t group, int &b_out, int64_t &off) {
+__device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, int &extra, int64_t cluster, int &b_out, int64_t &off) {
     const int lane = threadIdx.x & 63, B = a.c.n_seqs, per = (B + 63) / 64;
-    int64_t mine = 0;
+    int64_t tiles = 0, batches = 0;
     for (int i = 0; i < per; ++i) {
         const int b = lane * per + i;
         if (b < B) {
             const Seq s = sequence<S>(a, b);
-            mine += (int64_t)s.row_tiles * s.kv_tiles;
+            batches += s.batches(a.members);
+            tiles += (int64_t)s.batches(a.members) * s.kv_tiles;
         }
     }
-    const int64_t upto = wave_prefix(mine, lane), total = __shfl(upto, 63);
-    share = (total + GROUPS - 1) / GROUPS;
-    if (share < MIN_SHARE) share = MIN_SHARE;
-    const int64_t at = group * share;
+    const int clusters = WORKGROUPS / a.members;
+    extra = (int)min(wave_sum(tiles) / clusters / 4, (int64_t)EXTRA);  // (none where a share is a few tiles)
+    const int64_t mine = tiles + batches * extra, upto = wave_prefix(mine, lane), total = __shfl(upto, 63);
+    share = (total + clusters - 1) / clusters;
+    if (share < 1) share = 1;
+    const int64_t at = cluster * share;
     b_out = -1;
     if (at >= total) return total;
-    const uint64_t in = __ballot(at >= upto - mine && at < upto);
-    const int who = __builtin_ctzll(in);
+    const int who = __builtin_ctzll(__ballot(at >= upto - mine && at < upto));
     int64_t rest = at - __shfl(upto - mine, who);
     for (int b = who * per; b < min(B, (who + 1) * per); ++b) {
         const Seq s = sequence<S>(a, b);
-        const int64_t w = (int64_t)s.row_tiles * s.kv_tiles;
+        const int64_t w = (int64_t)s.batches(a.members) * (s.kv_tiles + extra);
         if (rest < w) {
             b_out = b;
             off = rest;
@@ -105,9 +137,6 @@ __device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, 
     }
     return total;
 }
-
-// Place of a part in the workspace: sums [ROWS][LATENT], then maximum and sum [ROWS] each.
-template <class S> constexpr int64_t part_floats() { return (int64_t)S::ROWS * (S::LATENT + 2); }
 
 // ------------------------------------------------------------------ tiles
 
@@ -123,463 +152,524 @@ __device__ __forceinline__ uint64_t sees_of_tile(const AttnArgs &a, int t, int i
 }
 
 template <int DT, class S>
-__global__ __launch_bounds__(256, 1) void attn_kernel(AttnArgs a) {
-    __shared__ __align__(16) char ring[S::BUFS * S::TILE_BYTES];
+__global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
+    __shared__ __align__(256) char ring[S::BUFS * S::TILE_BYTES];
     __shared__ uint32_t not_finite[2];
-    constexpr int NB = S::NB, KVB = S::KVB;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int col = lane & 15, grp = lane >> 4;
-    // neighbours in the order of the work on one XCD (workgroups go round the 8 XCDs)
-    const int group = (blockIdx.x & 7) * (GROUPS / 8) + (blockIdx.x >> 3);
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int row_wave = wave % S::ROW_WAVES, set = wave / S::ROW_WAVES;
+    // clusters in the order of the work run on one XCD
+    const int slot = blockIdx.x / XCDS, member = slot % a.members;
+    const int cluster = (blockIdx.x % XCDS) * (WORKGROUPS / XCDS / a.members) + slot / a.members;
 
-    int64_t share, off;
-    int b;
-    const int64_t total = find_unit<S>(a, share, group, b, off);
-    if (b < 0) return;
+    int64_t share, off = 0;
+    int b, extra;
+    const int64_t total = find_unit<S>(a, share, extra, cluster, b, off);
     b = uniform(b);
     off = uniform(off);
-    int64_t left = uniform(min(share, total - group * share));
+    extra = uniform(extra);
+    if (threadIdx.x == 0 && member == 0) {
+        Header *head = static_cast<Header *>(a.ws);
+        if (cluster == 0) head->share = share;
+        Start at = {b, 0, 0, 0};
+        if (b >= 0) {
+            const int each = sequence<S>(a, b).kv_tiles + extra;
+            at.batch = (int)(off / each);
+            at.tile = max((int)(off - (int64_t)at.batch * each) - extra, 0);
+        }
+        head->start[cluster] = at;
+    }
+    if (b < 0) return;
+    int64_t left = uniform(min(share, total - cluster * share));
     const float scale2 = a.scale * LOG2E;
     const char *cache = static_cast<const char *>(a.cache);
-
-    // LDS byte offsets of this lane's reads inside a tile, for the first k step, rope step and
-    // block of the output; the others' chunks differ in higher bits, which an xor reaches
-    const int row0_in_tile = S::SPLIT ? wave * 16 : 0;  // first token of the wave's blocks
-    const uint32_t k_at = (row0_in_tile + col) * S::ROW_BYTES + ((grp ^ swz(col)) << 4);
-    const uint32_t r_at = S::ROPE_AT + (row0_in_tile + col) * 128 + ((grp ^ swz_rope(col)) << 4);
-    const int vr = grp * 4 + (col >> 2);
-    const uint32_t v_at = (row0_in_tile + vr) * S::ROW_BYTES + ((((col >> 1) & 1) ^ swz(vr)) << 4) + (col & 1) * 8;
 
     bool first_part = true;
     while (left > 0) {
         Seq sq = sequence<S>(a, b);
         sq = {uniform(sq.few), uniform(sq.len), uniform(sq.row_tiles), uniform(sq.kv_tiles)};
-        const int64_t units = (int64_t)sq.row_tiles * sq.kv_tiles;
-        if (off >= units) {  // next sequence (the units in all bound b)
+        const int each = sq.kv_tiles + extra;  // units of a batch
+        if (off >= (int64_t)sq.batches(a.members) * each) {  // next sequence (the units in all bound b)
             ++b;
             off = 0;
             continue;
         }
         const int q0 = uniform(cu_at(a.c.cu_q, b, (int)a.N));
-        const int row_tile = (int)(off / sq.kv_tiles), t_first = (int)(off - (int64_t)row_tile * sq.kv_tiles);
-        const int n = (int)min((int64_t)(sq.kv_tiles - t_first), left);
+        const int batch = (int)(off / each), u0 = (int)(off - (int64_t)batch * each), u1 = u0 + (int)min((int64_t)(each - u0), left);
+        const int t_first = max(u0 - extra, 0), n = max(u1 - extra, 0) - t_first;
+        const int row_tile = batch * a.members + member;
+        const bool part_of_first = first_part && t_first > 0;
+        first_part = false;
+        left -= u1 - u0;
+        off += u1 - u0;
+        if (n == 0 || row_tile >= sq.row_tiles) continue;
         const int n_rows = sq.few * a.heads;  // the host keeps N * heads below 2^31
         const int context = sq.len - sq.few;
 
-        // ---- rows: queries in registers
-        int tok[NB];
-        u32x4_t q[NB][S::KSTEPS + 2];
-        for (int nb = 0; nb < NB; ++nb) {
-            const int64_t r64 = (int64_t)row_tile * S::ROWS + (S::SPLIT ? 0 : wave * NB * 16) + nb * 16 + col;
-            const int r = (int)min(r64, (int64_t)n_rows - 1);  // rows behind the last repeat it
-            tok[nb] = r / a.heads;
-            const int h = r - tok[nb] * a.heads;
-            const elem_t<DT> *ql = static_cast<const elem_t<DT> *>(a.ql) + (int64_t)(q0 + tok[nb]) * a.ql_token + h * a.ql_head;
-            const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok[nb]) * a.qr_token + h * a.qr_head;
-            for (int k = 0; k < S::KSTEPS; ++k) q[nb][k] = *reinterpret_cast<const u32x4_t *>(ql + k * 32 + grp * 8);
-            for (int k = 0; k < 2; ++k) q[nb][S::KSTEPS + k] = *reinterpret_cast<const u32x4_t *>(qr + k * 32 + grp * 8);
-        }
-        float top[NB], sum[NB];
-        acc4_t acc[S::DBLOCKS][NB];
-        for (int nb = 0; nb < NB; ++nb) {
-            top[nb] = -INFINITY;
-            sum[nb] = 0.f;
-            for (int d = 0; d < S::DBLOCKS; ++d) {
-                acc[d][nb] = acc4_t{0.f, 0.f, 0.f, 0.f};
-                pin_acc(acc[d][nb]);
-            }
+        // ---- the lane's row: its query in registers
+        const int row0 = row_tile * S::ROWS + row_wave * 32;
+        const int tok = min(row0 + (lane & 31), n_rows - 1) / a.heads;  // rows behind the last repeat it
+        u32x4_t q[S::KSTEPS];
+        auto load_queries = [&]() {
+            const int head = min(row0 + (lane & 31), n_rows - 1) - tok * a.heads;
+            const elem_t<DT> *ql = static_cast<const elem_t<DT> *>(a.ql) + (int64_t)(q0 + tok) * a.ql_token + head * a.ql_head;
+            const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head;
+#pragma unroll
+            for (int k = 0; k < S::KSTEPS; ++k)
+                q[k] = *reinterpret_cast<const u32x4_t *>((k < S::KLATENT ? ql + k * 16 : qr + (k - S::KLATENT) * 16) + (lane >> 5) * 8);
+#pragma unroll
+            for (int k = 0; k < S::KSTEPS; ++k) loaded(q[k]);
+        };
+        float top = -INFINITY, from = 0.f, sum = 0.f;  // running maximum (what is subtracted: 0 if there is none), sum
+        acc16_t acc[S::DBLOCKS];
+#pragma unroll
+        for (int d = 0; d < S::DBLOCKS; ++d) {
+            acc[d] = acc16_t{};
+            pin_acc(acc[d]);
         }
 
+        // Pages: lane e holds entry e of those of the next tiles, 1 << e_shift a tile, so that the
+        // block table is read once for many tiles and its latency is not a tile's.
+        const int e_shift = max(__builtin_ctz(S::TOKENS) - a.c.page_shift, 0);
+        int pages = -1, pages_from = t_first - 64;
         // Cache rows of a tile's tokens, lane r that of token r (-1: not in the cache, or behind the end).
         auto look_up = [&](int tile) {
-            const int r = lane & (S::TOKENS - 1), j = tile * S::TOKENS + r;
-            if (a.c.page_shift < 4) {  // pages of less than 16 tokens: a lookup a lane
-                int64_t at = -1;
-                if (tile < t_first + n && j < sq.len) at = cache_row(a.c, b, j);
-                return (int)at;
+            if (tile >= t_first + n) return -1;
+            if (tile - pages_from >= 64 >> e_shift) {
+                pages_from = tile;
+                const int e = here(lane), in_tile = e >> e_shift;
+                const int j = (tile + in_tile) * S::TOKENS + ((e - (in_tile << e_shift)) << a.c.page_shift);
+                pages = -1;
+                if (tile + in_tile < t_first + n && j < sq.len) pages = a.c.block_table[(int64_t)b * a.c.max_pages + (j >> a.c.page_shift)];
+                if (pages >= a.c.n_pages) pages = -1;
+                loaded(pages);
             }
-            constexpr int PAGES = S::TOKENS / 16;
-            int page = -1;
-            for (int i = 0; i < PAGES; ++i) {
-                const int first = tile * S::TOKENS + i * 16;
-                if (tile >= t_first + n || first >= sq.len) break;
-                const int pg = scalar_load(a.c.block_table, (int64_t)b * a.c.max_pages + (first >> a.c.page_shift));
-                if ((r >> 4) == i) page = pg;
-            }
-            if (j >= sq.len || page < 0 || page >= a.c.n_pages) return -1;
-            return (page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
+            const int r = here(lane) & (S::TOKENS - 1), j = tile * S::TOKENS + r;
+            const int page = from_lane(pages, ((tile - pages_from) << e_shift) + (e_shift ? r >> a.c.page_shift : 0));
+            return page < 0 || j >= sq.len ? -1 : (page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
         };
-        // Issues a tile's loads. Tokens that are not there get the data of one that is (their
-        // places may hold anything, also NaN, which a weight of 0 would not hide).
-        auto issue = [&](int t, int rows, uint32_t buf) {
-            if (t >= t_first + n) return;
+        // A tile's loads. Tokens that are not there get the data of one that is (their places may
+        // hold anything, also NaN, which a weight of 0 would not hide). Which tokens are there, a bit each:
+        auto present = [&](int &rows) -> uint64_t {
             const uint64_t ok = __ballot(rows >= 0);
-            // (a tile with no token that is there: row 0, never looked at; the waits count on its loads)
-            rows = rows >= 0 ? rows : ok ? __shfl(rows, __builtin_ctzll(ok | 1ull << 63)) : 0;
-            const uint32_t here_lane = here(lane);
-            for (int i = 0; i < S::WAVE_TOKENS / S::ROWS_A_LOAD; ++i) {
-                const int r0 = wave * S::WAVE_TOKENS + i * S::ROWS_A_LOAD;
+            const int one = __builtin_amdgcn_readlane(rows, __builtin_ctzll(ok | 1ull << 63));
+            rows = rows >= 0 ? rows : one >= 0 ? one : 0;  // (none is there: row 0; nothing sees it)
+            return ok;
+        };
+        // The wave's load number i of the tile; `from`: lane r's is the address of token r.
+        constexpr int OWN_LATENT = S::LATENT_LOADS / S::WAVES, LOADS = OWN_LATENT + S::ROPE_LOADS / S::WAVES;
+        constexpr int OWN_ROWS = S::TOKENS / S::WAVES;  // 16 or 32: swz of a row is that of its number in the wave
+        static_assert(OWN_ROWS % 16 == 0, "the waves' rows swizzle alike");
+        auto load = [&](int i, uint64_t from, uint32_t lane16, uint32_t buf, uint64_t lanes) {
+            auto of_row = [&](int r) {
+                return (uint64_t)(uint32_t)from_lane((int)(uint32_t)from, r) | (uint64_t)(uint32_t)from_lane((int)(from >> 32), r) << 32;
+            };
+            if (i < OWN_LATENT) {
+                const int own = i * S::ROWS_A_LOAD, r0 = wave * OWN_ROWS + own;
                 if constexpr (S::ROWS_A_LOAD == 1) {
-                    const int at = __builtin_amdgcn_readlane(rows, r0);
-                    load_to_lds16(cache + (int64_t)at * (S::D * 2), (here_lane ^ swz(r0)) * 16, buf + r0 * S::ROW_BYTES);
+                    const uint64_t at = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)from, r0) |
+                                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(from >> 32), r0) << 32;
+                    load_to_lds16((const char *)at, lane16 ^ (swz(own) << 4), buf + r0 * S::ROW_BYTES, lanes);
                 } else {
                     constexpr int PER = 64 / S::ROWS_A_LOAD;  // lanes a row
-                    const int r = r0 + here_lane / PER, at = __shfl(rows, r);
-                    load_to_lds16(cache + (int64_t)at * (S::D * 2) + ((here_lane & (PER - 1)) ^ swz(r)) * 16,
-                                  buf + r0 * S::ROW_BYTES);
+                    const int r = r0 + lane16 / (16 * PER);
+                    load_to_lds16((const char *)of_row(r) + ((lane16 & (16 * PER - 16)) ^ (swz(r) << 4)), buf + r0 * S::ROW_BYTES, lanes);
                 }
-            }
-            for (int i = 0; i < S::WAVE_TOKENS / 8; ++i) {
-                const int r0 = wave * S::WAVE_TOKENS + i * 8, r = r0 + (here_lane >> 3), at = __shfl(rows, r);
-                load_to_lds16(cache + (int64_t)at * (S::D * 2) + S::ROW_BYTES + (((here_lane & 7) ^ swz_rope(r)) << 4),
-                              buf + S::ROPE_AT + r0 * 128);
+            } else {
+                const int r0 = (wave * (LOADS - OWN_LATENT) + i - OWN_LATENT) * 8, r = r0 + (lane16 >> 7);
+                load_to_lds16((const char *)of_row(r) + S::ROW_BYTES + ((lane16 & 112) ^ (swz_rope(r) << 4)), buf + S::ROPE_AT + r0 * 128,
+                              lanes);
             }
         };
+        auto address = [&](int row) { return (uint64_t)cache + (uint64_t)(uint32_t)row * (S::D * 2); };
+        auto load_all = [&](int rows, uint32_t buf) {
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(i, address(rows), here(lane) * 16, buf, ~0ull);
+        };
 
-        auto tile = [&](int t, int rows, uint32_t at) {
+        // Tile t (tokens `ok`) in LDS at `at`, and the loads of the next one, if there is one, beside it.
+        auto tile = [&](int t, uint64_t ok, uint32_t at, int rows, uint32_t at_next) {
             DS4HC_LDS char *buf = (DS4HC_LDS char *)(uintptr_t)at;
-            const uint64_t ok = __ballot(rows >= 0);
-            if (!ok) return;
             const int j0 = t * S::TOKENS;
             const bool masked = ok != ~0ull || j0 + S::TOKENS > (a.tree_mask ? context : context + 1);
             uint64_t bad = 0;  // tokens that hold a value that is not finite
-            if (masked) {  // uniform over the workgroup
+            if (masked) {  // the same in all waves
+                constexpr int CHUNKS = S::ROW_BYTES / 16;
                 if (threadIdx.x < 2) not_finite[threadIdx.x] = 0;
                 wait_and_barrier<63>();
-                constexpr int CHUNKS = S::ROW_BYTES / 16;
-                for (int i = threadIdx.x; i < S::TOKENS * CHUNKS; i += 256) {
+                for (int i = threadIdx.x; i < S::TOKENS * CHUNKS; i += S::THREADS) {
                     const u32x4_t w = lds_read16(buf + i * 16);
                     if (word_not_finite<DT>(w.x) || word_not_finite<DT>(w.y) || word_not_finite<DT>(w.z) || word_not_finite<DT>(w.w))
                         atomicOr(&not_finite[(i / CHUNKS) >> 5], 1u << ((i / CHUNKS) & 31));
                 }
                 wait_and_barrier<63>();
                 bad = ((uint64_t)uniform((int)not_finite[1]) << 32) | (uint32_t)uniform((int)not_finite[0]);
-            }
-            // S^T = K Q^T
-            acc4_t s[KVB * NB];
-            constexpr int STEPS = S::KSTEPS + 2, AHEAD = NB == 2 ? 3 : 4;
-            const uint32_t k0 = here(k_at), r0 = here(r_at);
-            auto read_k = [&](int k, int kb) {
-                return k < S::KSTEPS ? lds_read16(buf + (k0 ^ ((k & 3) << 6)) + (k >> 2) * 256 + kb * 16 * S::ROW_BYTES)
-                                     : lds_read16(buf + (r0 ^ ((k - S::KSTEPS) << 6)) + kb * 16 * 128);
-            };
-            u32x4_t x[AHEAD][KVB];
-#pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb) x[k][kb] = read_k(k, kb);
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-                u32x4_t now[KVB];
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb) {
-                    now[kb] = x[k % AHEAD][kb];
-                    if (k + AHEAD < STEPS) x[k % AHEAD][kb] = read_k(k + AHEAD, kb);
-                }
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb)
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) {
-                        if (k == 0) s[kb * NB + nb] = mfma_k32_first_v<DT>(now[kb], q[nb][k]);
-                        else mfma_k32_v<DT>(now[kb], q[nb][k], s[kb * NB + nb]);
-                    }
-                __builtin_amdgcn_sched_barrier(0);
-            }
-            mfma_results(s);
-            if (bad) {
-                // values that are not finite: zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
-                wait_and_barrier<63>();
-                constexpr int CHUNKS = S::ROW_BYTES / 16;
-                for (int i = threadIdx.x; i < S::TOKENS * CHUNKS; i += 256) {
-                    const int r = i / CHUNKS;
-                    if ((bad >> r) & 1) *reinterpret_cast<DS4HC_LDS u32x4_t *>(buf + i * 16) = u32x4_t{0, 0, 0, 0};
-                }
-                wait_and_barrier<63>();
-            }
-            u32x2_t p[KVB][NB];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                float x[KVB][4], high = -INFINITY;
-                uint64_t sees = ~0ull, nan = 0;
-                if (masked) {
-                    sees = sees_of_tile(a, q0 + tok[nb], tok[nb], j0 - context) & ok;
-                    nan = sees & bad;
-                }
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[kb][i] = s[kb * NB + nb][i] * scale2;
-                        if (masked) {
-                            const int r = row0_in_tile + kb * 16 + grp * 4 + i;
-                            x[kb][i] = (nan >> r) & 1 ? NAN : (sees >> r) & 1 ? x[kb][i] : -INFINITY;
+                if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
+                    for (int i = threadIdx.x; i < S::TOKENS * CHUNKS; i += S::THREADS)
+                        if ((bad >> (i / CHUNKS)) & 1) {
+                            const uint32_t zero = here(0);
+                            *reinterpret_cast<DS4HC_LDS u32x4_t *>(buf + i * 16) = u32x4_t{zero, zero, zero, zero};
                         }
-                        high = fmaxf(high, x[kb][i]);
-                    }
-                high = max_over_groups(high);
-                if (__any(high > top[nb] + LAZY)) {
-                    const float to = fmaxf(top[nb], high);
-                    const float keep = to == -INFINITY ? 0.f : exp2_fast(top[nb] - to);
-                    top[nb] = to;
-                    sum[nb] *= keep;
-#pragma unroll
-                    for (int d = 0; d < S::DBLOCKS; ++d) {
-                        pin_acc(acc[d][nb]);
-                        acc[d][nb] *= keep;
-                        pin_acc(acc[d][nb]);
-                    }
-                }
-                const float from = top[nb] == -INFINITY ? 0.f : top[nb];
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[kb][i] = exp2_fast(x[kb][i] - from);
-                        sum[nb] += x[kb][i];
-                    }
-                    p[kb][nb] = u32x2_t{pack2<DT>(x[kb][0], x[kb][1]), pack2<DT>(x[kb][2], x[kb][3])};
+                    wait_and_barrier<63>();
                 }
             }
-            // O^T += V^T P^T; the order of the tokens in a step is that of S^T's rows, for both operands
-            constexpr int VAHEAD = 8;
-            const uint32_t v0 = here(v_at);
-            auto read_v = [&](int d, int kb) { return lds_read_tr(buf + (v0 ^ ((d & 7) << 5)) + (d >> 3) * 256 + kb * 16 * S::ROW_BYTES); };
-            u32x2_t v[VAHEAD][KVB];
+            // LDS offsets of this lane's reads for the first k step, rope step and block of the
+            // output; the others' chunks differ in higher bits, which an xor reaches. Made anew for
+            // every tile: there are no registers to keep them.
+            const int l = here(lane), lr = l & 31, lh = l >> 5;
+            const int t0 = set * S::STEPS * 32;  // first token of the wave
+            const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + ((lh ^ swz(lr)) << 4);
+            const uint32_t r0 = S::ROPE_AT + (t0 + lr) * 128 + ((lh ^ swz_rope(lr)) << 4);
+            const int vr = lh * 4 + ((l >> 2) & 3);
+            const uint32_t v0 = (t0 + vr) * S::ROW_BYTES + (((((l >> 4) & 1) << 1 | ((l >> 1) & 1)) ^ swz(vr)) << 4) + (l & 1) * 8;
+            const uint32_t v8 = (v0 ^ 32) + 8 * S::ROW_BYTES;  // 8 rows on, swz differs in bit 1
+
+            // S^T = K Q^T of 32 tokens, the operands of the next products on their way; `between`
+            // gives other work to the vector unit while the matrix unit is busy
+            constexpr int AHEAD = 3;
+            auto products_k = [&](int step, acc16_t &s, auto &&between) {
+                // (steps in an order that uses one offset up before the next)
+                auto nth = [](int i) { return i < S::KLATENT ? i % (S::KLATENT / 8) * 8 + i / (S::KLATENT / 8) : i; };
+                auto read = [&](int i) {
+                    const int k = nth(i);
+                    return k < S::KLATENT ? lds_read16(buf + (k0 ^ ((k & 7) << 5)) + (k >> 3) * 256 + step * 32 * S::ROW_BYTES)
+                                          : lds_read16(buf + (r0 ^ ((k - S::KLATENT) << 5)) + step * 32 * 128);
+                };
+                u32x4_t x[AHEAD];
 #pragma unroll
-            for (int d = 0; d < VAHEAD; ++d)
+                for (int i = 0; i < AHEAD; ++i) x[i] = read(i);
 #pragma unroll
-                for (int kb = 0; kb < KVB; ++kb) v[d][kb] = read_v(d, kb);
-#pragma unroll
-            for (int d = 0; d < S::DBLOCKS; ++d) {
-                u32x2_t now[KVB];
-#pragma unroll
-                for (int kb = 0; kb < KVB; ++kb) {
-                    now[kb] = v[d % VAHEAD][kb];
-                    if (d + VAHEAD < S::DBLOCKS) v[d % VAHEAD][kb] = read_v(d + VAHEAD, kb);
+                for (int i = 0; i < S::KSTEPS; ++i) {
+                    const u32x4_t now = x[i % AHEAD];
+                    if (i == 0) mfma32_first_v<DT>(now, q[nth(i)], s);
+                    else mfma32_v<DT>(now, q[nth(i)], s);
+                    if (i + AHEAD < S::KSTEPS) x[i % AHEAD] = read(i + AHEAD);
+                    between(i);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            };
+            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of S^T's rows, for both operands
+            constexpr int VAHEAD = 4;
+            auto products_v = [&](int step, const u32x4_t (&p)[2], auto &&between) {
+                auto read = [&](int i) {  // block i / 2 in the order nth(), tokens 16 (i % 2) .. + 15
+                    const int d = i / 2 % (S::DBLOCKS / 4) * 4 + i / 2 / (S::DBLOCKS / 4);
+                    const uint32_t chunk = (d & 3) << 6, off = (d >> 2) * 256 + (step * 32 + (i & 1) * 16) * S::ROW_BYTES;
+                    const u32x2_t lo = lds_read_tr(buf + (v0 ^ chunk) + off), hi = lds_read_tr(buf + (v8 ^ chunk) + off);
+                    return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+                };
+                u32x4_t v[VAHEAD];
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    if constexpr (KVB == 2)
-                        acc[d][nb] = mfma_k32<DT>(u32x4_t{now[0].x, now[0].y, now[KVB - 1].x, now[KVB - 1].y},
-                                                  u32x4_t{p[0][nb].x, p[0][nb].y, p[KVB - 1][nb].x, p[KVB - 1][nb].y}, acc[d][nb]);
-                    else
-                        acc[d][nb] = mfma_k16<DT>(now[0], p[0][nb], acc[d][nb]);
+                for (int i = 0; i < VAHEAD; ++i) v[i] = read(i);
+#pragma unroll
+                for (int i = 0; i < S::DBLOCKS * 2; ++i) {
+                    const int d = i / 2 % (S::DBLOCKS / 4) * 4 + i / 2 / (S::DBLOCKS / 4);
+                    acc[d] = mfma32<DT>(v[i % VAHEAD], p[i & 1], acc[d]);
+                    if (i + VAHEAD < S::DBLOCKS * 2) v[i % VAHEAD] = read(i + VAHEAD);
+                    between(i);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
-                __builtin_amdgcn_sched_barrier(0);
+            };
+            // Softmax of a step, in pieces. The mask, and the largest logit (of the lane's row).
+            uint64_t sees = ~0ull;
+            if (masked) sees = sees_of_tile(a, q0 + tok, tok, j0 - context) & ok;
+            auto largest = [&](int step, acc16_t &s) {
+                if (masked) {
+                    const int at0 = t0 + step * 32 + (here(lane) >> 5) * 4;
+                    const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 8 * (i / 4) + i % 4;
+                        s[i] = (nan >> r) & 1 ? NAN : (see >> r) & 1 ? s[i] : -INFINITY;
+                    }
+                }
+                return max_halves(max16(s)) * scale2;
+            };
+            // A new running maximum. It is a whole number, so that what is there is scaled by a power
+            // of 2, without rounding, weights that are already 16-bit values included.
+            auto raise = [&](float high) {
+                const float was = top;
+                top = fmaxf(top, ceilf(high));
+                from = top == -INFINITY ? 0.f : top;
+                const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
+                sum *= keep;
+#pragma unroll
+                for (int d = 0; d < S::DBLOCKS; ++d) {
+                    pin_acc(acc[d]);
+                    acc[d] *= keep;
+                    pin_acc(acc[d]);
+                }
+                return keep;
+            };
+            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {  // weights 2 i and 2 i + 1
+                const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
+                sum += e0;
+                sum += e1;
+                p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+            };
+            // the next tile's loads, spread over the products (all but a second step's last): issued
+            // faster than one in some 34 cycles a CU they hold the waves up
+            constexpr int SLOTS = S::KSTEPS * S::STEPS + S::DBLOCKS * 2, LOAD_EVERY = SLOTS / LOADS;
+            static_assert(LOAD_EVERY >= 1, "a place for each load");
+            const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < t_first + n ? -1 : 0));
+            const uint64_t from = address(rows);
+            const uint32_t lane16 = here(lane) * 16;
+            auto load_some = [&](int i) {
+                if (i % LOAD_EVERY == 0 && i / LOAD_EVERY < LOADS) load(i / LOAD_EVERY, from, lane16, at_next, lanes);
+            };
+            acc16_t s;
+            u32x4_t p[2];
+            products_k(0, s, load_some);
+            if constexpr (S::STEPS == 1) {
+                mfma_results(s);
+                const float high = largest(0, s);
+                if (__any(high > top + LAZY)) raise(high);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) weight2(s, i, p);
+                products_v(0, p, [&](int i) { load_some(S::KSTEPS + i); });
+            } else {  // two steps, the softmax of each beside the products of the other, as far as can be
+                acc16_t s1;
+                u32x4_t p1[2];
+                mfma_results(s);
+                float high = largest(0, s);
+                if (__any(high > top + LAZY)) raise(high);
+                products_k(1, s1, [&](int i) {
+                    constexpr int EVERY = S::KSTEPS / 8;
+                    load_some(S::KSTEPS + i);
+                    if (i % EVERY == EVERY - 1 && i / EVERY < 8) weight2(s, i / EVERY, p);
+                });
+                mfma_results(s1);
+                high = largest(1, s1);
+                if (__any(high > top + LAZY)) {
+                    const float keep = raise(high);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
+                }
+                products_v(0, p, [&](int i) {
+                    constexpr int EVERY = S::DBLOCKS / 4;
+                    load_some(2 * S::KSTEPS + i);
+                    if (i % EVERY == EVERY - 1) weight2(s1, i / EVERY, p1);
+                });
+                products_v(1, p1, [](int) {});
             }
         };
 
-        // ---- tiles: BUFS - 1 in flight. All waves are done with tile t - 1 when they meet at
-        // the barrier of tile t, so its buffer takes tile t - 1 + BUFS.
-        wait_and_barrier<0>();  // the last part's reads of the ring
+        // ---- tiles: the next one's loads run beside this one's products. All waves are done with
+        // tile t - 1 when they meet at the barrier of tile t, so its buffer takes tile t + 1.
+        wait_and_barrier<63>();  // the last part's reads of the ring
         const uint32_t ring_at = lds_address(ring);
-        int ahead[S::BUFS - 1];  // cache rows of the tiles in flight
-#pragma unroll
-        for (int i = 0; i < S::BUFS - 1; ++i) {
-            ahead[i] = look_up(t_first + i);
-            issue(t_first + i, ahead[i], ring_at + i * S::TILE_BYTES);
-        }
-        uint32_t buf = ring_at, free_buf = ring_at + (S::BUFS - 1) * S::TILE_BYTES;
-        int next = look_up(t_first + S::BUFS - 1);
+        int rows = look_up(t_first);
+        uint64_t ok = present(rows);
+        load_all(rows, ring_at);
+        load_queries();  // (waits for the first tile, too)
+        int next = look_up(t_first + 1);
         for (int i = 0; i < n; ++i) {
-            // loads of the tiles behind this one stay in flight
-            if (S::BUFS > 2 && i + 2 < n) wait_and_barrier<2 * S::LOADS>();
-            else if (S::BUFS > 2 && i + 1 < n) wait_and_barrier<S::LOADS>();
-            else wait_and_barrier<0>();
-            issue(t_first + i + S::BUFS - 1, next, free_buf);
-            const int rows = ahead[0];
-#pragma unroll
-            for (int k = 0; k + 1 < S::BUFS - 1; ++k) ahead[k] = ahead[k + 1];
-            ahead[S::BUFS - 2] = next;
-            next = look_up(t_first + i + S::BUFS);
-            tile(t_first + i, rows, buf);
-            free_buf = buf;
-            buf = buf + S::TILE_BYTES == ring_at + S::BUFS * S::TILE_BYTES ? ring_at : buf + S::TILE_BYTES;
+            wait_and_barrier<0>();
+            rows = next;
+            const uint64_t ok_next = present(rows);
+            next = look_up(t_first + i + 2);
+            tile(t_first + i, ok, ring_at + (i & 1) * S::TILE_BYTES, rows, ring_at + ((i + 1) & 1) * S::TILE_BYTES);
+            ok = ok_next;
         }
 
         // ---- the part's result
 #pragma unroll
-        for (int d = 0; d < S::DBLOCKS; ++d)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) pin_acc(acc[d][nb]);
-        const bool whole = t_first == 0 && n == sq.kv_tiles;
-        float *part = static_cast<float *>(a.ws) + (2 * (int64_t)group + (first_part && t_first > 0 ? 0 : 1)) * part_floats<S>();
-        auto row_of = [&](int nb) { return row_tile * (int64_t)S::ROWS + (S::SPLIT ? 0 : wave * NB * 16) + nb * 16 + col; };
-        // where the lane's row goes, and its statistics
-        auto out_at = [&](int nb) {
-            const int h = (int)row_of(nb) - tok[nb] * a.heads;
-            return static_cast<elem_t<DT> *>(a.out) + (int64_t)(q0 + tok[nb]) * a.out_token + h * a.out_head;
-        };
-        auto part_at = [&](int nb) { return part + (row_of(nb) - row_tile * (int64_t)S::ROWS) * S::LATENT; };
-        auto put_sums = [&](int nb, float t, float total_sum) {
-            const int64_t r = row_of(nb);
-            if (r >= n_rows) return;
-            if (whole) {
-                if (a.lse) a.lse[(int64_t)q0 * a.heads + r] = total_sum == 0.f ? -INFINITY : (t + __log2f(total_sum)) * LN2;
-            } else {
-                const int64_t in = r - row_tile * (int64_t)S::ROWS;
-                part[S::ROWS * S::LATENT + in] = t;
-                part[S::ROWS * (S::LATENT + 1) + in] = total_sum;
+        for (int d = 0; d < S::DBLOCKS; ++d) pin_acc(acc[d]);
+        const int l = here(lane), lh = l >> 5, my_row = row0 + (l & 31), head = my_row - tok * a.heads;
+        const bool whole = t_first == 0 && n == sq.kv_tiles, mine = my_row < n_rows;  // (a part's rows behind the last: never looked at)
+        const int in = my_row - row_tile * S::ROWS;
+        float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);
+        float all = sum_halves(sum);
+        if constexpr (S::SETS == 2) {
+            // the second set's sums through LDS, brought to the common maximum
+            constexpr int WAVE_BYTES = S::DBLOCKS * 16 * 64 * 4;
+            static_assert(S::ROW_WAVES * (WAVE_BYTES + 256) <= S::BUFS * S::TILE_BYTES, "a set's sums and statistics");
+            float *st = reinterpret_cast<float *>(ring + S::ROW_WAVES * WAVE_BYTES);  // maximum, sum [row waves][32]
+            wait_and_barrier<63>();
+            if (set == 1 && lh == 0) {
+                st[row_wave * 64 + l] = top;
+                st[row_wave * 64 + 32 + l] = all;
             }
-        };
-        // four elements of a row, as they are or divided by the sum
-        auto put4 = [&](elem_t<DT> *o, acc4_t v, float inv) {
-            *reinterpret_cast<u32x2_t *>(o) = u32x2_t{pack2<DT>(v[0] * inv, v[1] * inv), pack2<DT>(v[2] * inv, v[3] * inv)};
-        };
-        if constexpr (!S::SPLIT) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const float all = sum_over_groups(sum[nb]);
-                if (grp == 0) put_sums(nb, top[nb], all);
-                if (row_of(nb) < n_rows) {
-                    if (whole) {
-                        elem_t<DT> *o = out_at(nb) + grp * 4;
-                        const float inv = all == 0.f ? 0.f : 1.f / all;
-#pragma unroll
-                        for (int d = 0; d < S::DBLOCKS; ++d) put4(o + d * 16, acc[d][nb], inv);
-                    } else {
-                        float *o = part_at(nb) + grp * 4;
-#pragma unroll
-                        for (int d = 0; d < S::DBLOCKS; ++d) *reinterpret_cast<acc4_t *>(o + d * 16) = acc[d][nb];
-                    }
-                }
-            }
-        } else {
-            // the four waves' tokens: common maximum and sums through LDS, 16 rows at a time
-            constexpr int HALF = 16 * S::LATENT * 4;  // a wave's sums of 16 rows
-            static_assert(4 * HALF + 512 <= S::BUFS * S::TILE_BYTES, "four waves' sums and statistics");
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-                const float all = sum_over_groups(sum[nb]);
-                float *st = reinterpret_cast<float *>(ring + 4 * HALF);  // [2][4][16]
-                wait_and_barrier<0>();
-                if (grp == 0) {
-                    st[wave * 16 + col] = top[nb];
-                    st[64 + wave * 16 + col] = all;
-                }
-                wait_and_barrier<0>();
-                float to = -INFINITY;  // stays so where no logit is a number above it: sums are then 0 or NaN
-                for (int w = 0; w < 4; ++w) to = fmaxf(to, st[w * 16 + col]);
-                float total_sum = 0.f;
-                for (int w = 0; w < 4; ++w)
-                    total_sum += st[64 + w * 16 + col] * (to == -INFINITY ? 1.f : exp2_fast(st[w * 16 + col] - to));
-                const float keep = to == -INFINITY ? 1.f : exp2_fast(top[nb] - to);
-                char *mine = ring + wave * HALF;
+            if (set == 1) {
 #pragma unroll
                 for (int d = 0; d < S::DBLOCKS; ++d)
-                    *reinterpret_cast<acc4_t *>(mine + ((d * 4 + grp) * 16 + col) * 16) = acc[d][nb] * keep;
-                wait_and_barrier<0>();
-                if (wave == 0 && grp == 0) put_sums(nb, to, total_sum);
 #pragma unroll
-                for (int d = 0; d < S::DBLOCKS / 4; ++d) {
-                    const int db = wave * (S::DBLOCKS / 4) + d, at = ((db * 4 + grp) * 16 + col) * 16;
-                    acc4_t v = *reinterpret_cast<const acc4_t *>(ring + at);
-#pragma unroll
-                    for (int w = 1; w < 4; ++w) v += *reinterpret_cast<const acc4_t *>(ring + w * HALF + at);
-                    if (row_of(nb) >= n_rows) continue;
-                    if (whole) put4(out_at(nb) + db * 16 + grp * 4, v, total_sum == 0.f ? 0.f : 1.f / total_sum);
-                    else *reinterpret_cast<acc4_t *>(part_at(nb) + db * 16 + grp * 4) = v;
-                }
+                    for (int i = 0; i < 4; ++i)
+                        *reinterpret_cast<acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16) =
+                            acc4_t{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
             }
+            wait_and_barrier<63>();
+            if (set == 1) continue;
+            const float other = st[row_wave * 64 + (l & 31)], to = fmaxf(top, other);
+            // (no logit that is a number, -infinity: the sums are 0 or NaN)
+            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), keep1 = to == -INFINITY ? 1.f : exp2_fast(other - to);
+            all = all * keep + st[row_wave * 64 + 32 + (l & 31)] * keep1;
+            top = to;
+#pragma unroll
+            for (int d = 0; d < S::DBLOCKS; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const acc4_t v = *reinterpret_cast<const acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[d][4 * i + e] = acc[d][4 * i + e] * keep + v[e] * keep1;
+                }
         }
-        first_part = false;
-        left -= n;
-        off += n;
+        if (whole) {
+            const float inv = all == 0.f ? 0.f : 1.f / all;
+            if (a.lse && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+            // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
+            if constexpr (S::SETS == 1) wait_and_barrier<63>();  // the last tile has been read by all
+            char *rows_at = ring + row_wave * 32 * S::ROW_BYTES * S::SETS;  // (the wave's own place; with two sets the one it has just read)
+#pragma unroll
+            for (int d = 0; d < S::DBLOCKS; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<u32x2_t *>(rows_at + (l & 31) * S::ROW_BYTES + (((d * 4 + i) ^ (l & 15)) << 4) + lh * 8) = u32x2_t{
+                        pack2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv), pack2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+            const int64_t o = (int64_t)(q0 + tok) * a.out_token + head * a.out_head;
+            constexpr int PER = S::LATENT / 8;  // lanes a row
+            for (int i = 0; i < 32; i += 64 / PER) {
+                const int r = i + l / PER, c = l % PER;
+                const int64_t to = (int64_t)(uint32_t)from_lane((int)(uint32_t)o, r) | (int64_t)from_lane((int)(o >> 32), r) << 32;
+                const u32x4_t v = *reinterpret_cast<const u32x4_t *>(rows_at + r * S::ROW_BYTES + ((c ^ (r & 15)) << 4));
+                if (row0 + r < n_rows) *reinterpret_cast<u32x4_t *>(static_cast<elem_t<DT> *>(a.out) + to + c * 8) = v;
+            }
+        } else {
+            if (lh == 0) {
+                part[S::ROWS * S::LATENT + in] = top;
+                part[S::ROWS * (S::LATENT + 1) + in] = all;
+            }
+            float *o = part + (row_wave * (S::LATENT / 8) * 64 + l) * 4;
+#pragma unroll
+            for (int d = 0; d < S::DBLOCKS; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<acc4_t *>(o + (d * 4 + i) * 256) = acc4_t{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        }
     }
 }
 
-// Joins the parts of the row tiles that were cut: a wave a row.
+// Joins the parts of the batches that were cut. Workgroup (c, member) stands at the border
+// between clusters c and c + 1. If the border cuts a batch into P parts, its P - 1 borders share
+// the work out among themselves, so that one long sequence keeps all workgroups busy, too. A
+// piece of the work is 4 elements a lane for 32 rows: one wave's, or several waves' that take the
+// parts in turn if there are more waves than pieces.
+constexpr int JOIN_WAVES = 16;
+
 template <int DT, class S>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t item = ((int64_t)blockIdx.y * JOIN_BLOCKS + blockIdx.x) * 4 + (threadIdx.x >> 6);  // token * heads + head
-    if (item >= a.N * a.heads) return;
-    const int t = (int)(item / a.heads), h = (int)(item - (int64_t)t * a.heads);
-    const int B = a.c.n_seqs, per = (B + 63) / 64;
-    const int b_of = sequence_of(a.c.cu_q, B, (int)a.N, t);
-    if (b_of < 0) return;
-    // units before this sequence, and in all
-    int64_t mine = 0, before = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = lane * per + i;
-        if (b < B) {
-            const Seq s = sequence<S>(a, b);
-            const int64_t w = (int64_t)s.row_tiles * s.kv_tiles;
-            mine += w;
-            if (b < b_of) before += w;
+__global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) {
+    constexpr int CHUNKS = S::LATENT / 8;
+    __shared__ float shared[JOIN_WAVES][6][64];
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), member = blockIdx.y;
+    const Header *header = static_cast<const Header *>(a.ws);
+    const int64_t share = uniform(header->share);
+    const Start at = header->start[blockIdx.x + 1];
+    if (at.b < 0 || at.tile == 0) return;  // no work behind the border, or it cuts nothing
+    const Seq sq = sequence<S>(a, at.b);
+    const int q0 = cu_at(a.c.cu_q, at.b, (int)a.N);
+    const int row_tile = at.batch * a.members + member;
+    if (row_tile >= sq.row_tiles) return;
+    // borders of this batch before this one, and behind it
+    const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
+    const int borders = before + behind + 1, parts = borders + 1, c0 = blockIdx.x - before;  // first part: of cluster c0
+    const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
+    const int pieces = (rows + 31) / 32 * CHUNKS;
+    const int mine = before < pieces ? (pieces - before - 1) / borders + 1 : 0;  // pieces before, before + borders, ...
+    int waves = 1;  // a piece
+    while (waves * 2 * mine <= JOIN_WAVES && waves * 2 <= parts) waves *= 2;
+    const int sub = wave % waves, at_once = JOIN_WAVES / waves;
+    const float *first = part_at<S>(a, c0, 1, member), *second = part_at<S>(a, c0 + 1, 0, member);
+    const int64_t step = 2 * a.members * part_floats<S>();
+    for (int k0 = 0; k0 < mine; k0 += at_once) {
+        const int k = k0 + wave / waves;
+        const bool real = k < mine;
+        const int piece = before + (real ? k : 0) * borders, group = piece / CHUNKS, chunk = piece % CHUNKS;
+        const int in = group * 32 + (lane & 31);
+        float top = -INFINITY, total = 0.f;
+        acc4_t acc = {0.f, 0.f, 0.f, 0.f};
+        auto join = [&](float t, float w, acc4_t v) {
+            const float to = fmaxf(top, t);
+            // (-infinity: no logit that is a number; the sums are 0 or NaN)
+            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(t - to);
+            top = to;
+            total = total * keep + w * add;
+            acc = acc * keep + v * add;
+        };
+#pragma unroll 8
+        for (int i = sub; i < parts; i += waves) {
+            const float *p = i == 0 ? first : second + (i - 1) * step;
+            join(p[S::ROWS * S::LATENT + in], p[S::ROWS * (S::LATENT + 1) + in],
+                 *reinterpret_cast<const acc4_t *>(p + ((group * CHUNKS + chunk) * 64 + lane) * 4));
+        }
+        if (waves > 1) {  // (the same for all waves)
+            shared[wave][0][lane] = top;
+            shared[wave][1][lane] = total;
+            for (int e = 0; e < 4; ++e) shared[wave][2 + e][lane] = acc[e];
+            __syncthreads();
+            if (sub == 0)
+                for (int w = wave + 1; w < wave + waves; ++w)
+                    join(shared[w][0][lane], shared[w][1][lane],
+                         acc4_t{shared[w][2][lane], shared[w][3][lane], shared[w][4][lane], shared[w][5][lane]});
+            __syncthreads();
+        }
+        if (sub == 0 && real && in < rows) {
+            const int r = row_tile * S::ROWS + in, t = q0 + r / a.heads, h = r % a.heads;
+            const float inv = total == 0.f ? 0.f : 1.f / total;
+            elem_t<DT> *o = static_cast<elem_t<DT> *>(a.out) + (int64_t)t * a.out_token + h * a.out_head + chunk * 8 + (lane >> 5) * 4;
+            *reinterpret_cast<u32x2_t *>(o) = u32x2_t{pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv)};
+            if (a.lse && chunk == 0 && lane < 32) a.lse[(int64_t)t * a.heads + h] = total == 0.f ? -INFINITY : (top + __log2f(total)) * LN2;
         }
     }
-    for (int m = 32; m; m >>= 1) {
-        mine += __shfl_xor(mine, m);
-        before += __shfl_xor(before, m);
-    }
-    int64_t share = (mine + GROUPS - 1) / GROUPS;
-    if (share < MIN_SHARE) share = MIN_SHARE;
-    const Seq sq = sequence<S>(a, b_of);
-    const int q0 = cu_at(a.c.cu_q, b_of, (int)a.N);
-    const int64_t r = (int64_t)(t - q0) * a.heads + h;
-    const int row_tile = (int)(r / S::ROWS), in = (int)(r - (int64_t)row_tile * S::ROWS);
-    const int64_t u0 = before + (int64_t)row_tile * sq.kv_tiles, u1 = u0 + sq.kv_tiles;
-    const int64_t g0 = u0 / share, g1 = (u1 - 1) / share;
-    if (g0 == g1) return;  // written whole
-    const float *ws = static_cast<const float *>(a.ws);
-    auto part = [&](int64_t g) { return ws + (2 * g + (g == g0 ? 1 : 0)) * part_floats<S>(); };
-    float to = -INFINITY;
-    for (int64_t g = g0; g <= g1; ++g) to = fmaxf(to, part(g)[S::ROWS * S::LATENT + in]);
-    constexpr int E = S::LATENT / 64;
-    float acc[E], total = 0.f;
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int64_t g = g0; g <= g1; ++g) {
-        const float *p = part(g);
-        const float keep = to == -INFINITY ? 1.f : exp2_fast(p[S::ROWS * S::LATENT + in] - to);  // (1: sums of 0, or NaN)
-        total += keep * p[S::ROWS * (S::LATENT + 1) + in];
-        for (int e = 0; e < E; ++e) acc[e] += keep * p[(int64_t)in * S::LATENT + lane * E + e];
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    elem_t<DT> *o = static_cast<elem_t<DT> *>(a.out) + (int64_t)t * a.out_token + h * a.out_head + lane * E;
-    for (int e = 0; e < E; ++e) o[e] = elem_round<DT>(acc[e] * inv);
-    if (a.lse && lane == 0) a.lse[item] = total == 0.f ? -INFINITY : (to + __log2f(total)) * LN2;
 }
+
+// How a call is run. A tile has the rows that a sequence has on average, at most 128; sequences
+// of several row tiles give them to a cluster of workgroups that load the same tokens.
+struct Plan {
+    int rows, members;
+};
+
+Plan plan(const Paged &c, int heads, int64_t N) {
+    const int64_t rows = (N * heads + c.n_seqs - 1) / c.n_seqs;
+    if (rows <= 32) return {32, 1};
+    if (rows <= 64) return {64, 1};
+    return {128, rows <= 128 ? 1 : rows <= 256 ? 2 : 4};
+}
+
+template <int LATENT> using Rows32 = Shape<LATENT, 1, 2>;
+template <int LATENT> using Rows64 = Shape<LATENT, 2, 2>;
+template <int LATENT> using Rows128 = Shape<LATENT, 4, 1>;
 
 template <int DT, class S> hipError_t run(const AttnArgs &a, hipStream_t s) {
-    const hipError_t e = launch_kernel(attn_kernel<DT, S>, dim3(GROUPS), dim3(256), s, a);
+    const hipError_t e = launch_kernel(attn_kernel<DT, S>, dim3(WORKGROUPS), dim3(S::THREADS), s, a);
     if (e != hipSuccess) return e;
-    const unsigned blocks = (unsigned)((a.N * a.heads + 3) / 4);
-    const dim3 grid(blocks < JOIN_BLOCKS ? blocks : JOIN_BLOCKS, (blocks + JOIN_BLOCKS - 1) / JOIN_BLOCKS);
-    return launch_kernel(attn_join_kernel<DT, S>, grid, dim3(256), s, a);
+    return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members), dim3(JOIN_WAVES * 64), s, a);
 }
 
-// Rows of a tile: the rows a sequence has on average.
-int tile_rows(const Paged &c, int heads, int64_t N) {
-    const int64_t rows = (N * heads + c.n_seqs - 1) / c.n_seqs;
-    return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-}
-
-template <int DT, int LATENT> hipError_t run_rows(const AttnArgs &a, hipStream_t s) {
-    switch (tile_rows(a.c, a.heads, a.N)) {
-    case 16: return run<DT, Shape<LATENT, 1, true>>(a, s);
-    case 32: return run<DT, Shape<LATENT, 2, true>>(a, s);
-    case 64: return run<DT, Shape<LATENT, 1, false>>(a, s);
-    default: return run<DT, Shape<LATENT, 2, false>>(a, s);
+template <int DT, int LATENT> hipError_t run_rows(const AttnArgs &a, int rows, hipStream_t s) {
+    switch (rows) {
+    case 32: return run<DT, Rows32<LATENT>>(a, s);
+    case 64: return run<DT, Rows64<LATENT>>(a, s);
+    default: return run<DT, Rows128<LATENT>>(a, s);
     }
 }
 
-template <int DT> hipError_t run_latent(const AttnArgs &a, hipStream_t s) {
+template <int DT> hipError_t run_latent(const AttnArgs &a, int rows, hipStream_t s) {
     switch (a.latent) {
-    case 128: return run_rows<DT, 128>(a, s);
-    case 256: return run_rows<DT, 256>(a, s);
-    default: return run_rows<DT, 512>(a, s);
+    case 128: return run_rows<DT, 128>(a, rows, s);
+    case 256: return run_rows<DT, 256>(a, rows, s);
+    default: return run_rows<DT, 512>(a, rows, s);
     }
 }
 
 }  // namespace
 
 uint64_t attn_workspace_bytes(const Paged &c, int latent, int heads, int64_t N) {
-    return 2ull * GROUPS * tile_rows(c, heads, N) * (latent + 2) * sizeof(float);
+    return sizeof(Header) + 2ull * WORKGROUPS * plan(c, heads, N).rows * (latent + 2) * sizeof(float);
 }
 
-hipError_t launch_attn(const AttnArgs &a, hipStream_t s) {
-    return a.dt == DT_BF16 ? run_latent<DT_BF16>(a, s) : run_latent<DT_F16>(a, s);
+hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {
+    AttnArgs a = args;
+    const Plan p = plan(a.c, a.heads, a.N);
+    a.members = p.members;
+    return a.dt == DT_BF16 ? run_latent<DT_BF16>(a, p.rows, s) : run_latent<DT_F16>(a, p.rows, s);
 }
 
 }  // namespace ds4hc

@@ -39,17 +39,14 @@ __device__ __forceinline__ int kv_len_at(const Paged &c, int b) {
     return v < 0 ? 0 : v > most ? most : v;
 }
 
-// A value that is the same in all lanes, loaded through the scalar cache. For arrays that
-// no kernel of the library writes.
-__device__ __forceinline__ int scalar_load(const int32_t *p, int64_t i) {
-    return ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)p)[i];
-}
-
 // Values that are the same in all lanes, into scalar registers.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int64_t uniform(int64_t v) {
     return ((int64_t)uniform((int)(v >> 32)) << 32) | (uint32_t)uniform((int)v);
 }
+
+// Lane `lane`'s value.
+__device__ __forceinline__ int from_lane(int v, int lane) { return __builtin_amdgcn_ds_bpermute(lane << 2, v); }
 
 // The value, computed anew where it stands: keeps what is made of it from being kept in
 // registers over a loop.
@@ -97,20 +94,21 @@ __device__ __forceinline__ void rope_angle(int64_t position, double inv_freq, fl
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef float acc4_t __attribute__((ext_vector_type(4)));
+typedef float acc16_t __attribute__((ext_vector_type(16)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 #define DS4HC_LDS __attribute__((address_space(3)))
 #define DS4HC_GLOBAL __attribute__((address_space(1)))
 
-// C[16 x 16] += A[16 x 32] B[32 x 16]. Lane l holds row (A) or column (B) l % 16 and
-// its 8 elements k = (l / 16) * 8 .. + 7; of C column l % 16, rows (l / 16) * 4 .. + 3.
-template <int DT> __device__ __forceinline__ acc4_t mfma_k32(u32x4_t a, u32x4_t b, acc4_t c) {
+// C[32 x 32] += A[32 x 16] B[16 x 32]. Lane l holds row (A) or column (B) l % 32 and its 8
+// elements k = (l / 32) * 8 .. + 7; of C column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4.
+template <int DT> __device__ __forceinline__ acc16_t mfma32(u32x4_t a, u32x4_t b, acc16_t c) {
     if constexpr (DT == DT_BF16) {
         typedef __bf16 v8 __attribute__((ext_vector_type(8)));
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     } else {
         typedef _Float16 v8 __attribute__((ext_vector_type(8)));
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
     }
 }
 
@@ -119,38 +117,22 @@ template <int DT> __device__ __forceinline__ acc4_t mfma_k32(u32x4_t a, u32x4_t 
 // second set of results does not fit beside 256 running sums. The compiler does not know
 // these as matrix instructions, so the wait states are written out: the s_nop before one
 // (its operands may come from a vector instruction just before), mfma_results() before
-// anything reads the results. Chains on one C need none.
-template <int DT> __device__ __forceinline__ acc4_t mfma_k32_first_v(u32x4_t a, u32x4_t b) {
-    acc4_t c;
-    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
-    else asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
-    return c;
+// anything reads the results. A chain on one C needs none.
+template <int DT> __device__ __forceinline__ void mfma32_first_v(u32x4_t a, u32x4_t b, acc16_t &c) {
+    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
+    else asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "v"(b));
 }
-template <int DT> __device__ __forceinline__ void mfma_k32_v(u32x4_t a, u32x4_t b, acc4_t &c) {
-    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
-    else asm("s_nop 1\n\tv_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
+template <int DT> __device__ __forceinline__ void mfma32_v(u32x4_t a, u32x4_t b, acc16_t &c) {
+    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
+    else asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
 }
-template <int N> __device__ __forceinline__ void mfma_results(acc4_t (&c)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) asm volatile("s_nop 15" : "+v"(c[i]));
-    asm volatile("s_nop 15" : "+v"(c[N - 1]));
-}
+// (12 wait states from this instruction to a vector instruction that reads its result.)
+__device__ __forceinline__ void mfma_results(acc16_t &c) { asm volatile("s_nop 13" : "+v"(c)); }
 
 // Keeps running sums in accumulation registers over branches and loops in which vector
 // instructions touch them too: without it the compiler carries them in vector registers
 // and copies them all over and back for every tile.
-__device__ __forceinline__ void pin_acc(acc4_t &c) { asm volatile("" : "+a"(c)); }
-
-// C[16 x 16] += A[16 x 16] B[16 x 16]: 4 elements k = (l / 16) * 4 .. + 3 a lane.
-template <int DT> __device__ __forceinline__ acc4_t mfma_k16(u32x2_t a, u32x2_t b, acc4_t c) {
-    if constexpr (DT == DT_BF16) {
-        return __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(__builtin_bit_cast(s16x4_t, a), __builtin_bit_cast(s16x4_t, b), c,
-                                                         0, 0, 0);
-    } else {
-        typedef _Float16 v4 __attribute__((ext_vector_type(4)));
-        return __builtin_amdgcn_mfma_f32_16x16x16f16(__builtin_bit_cast(v4, a), __builtin_bit_cast(v4, b), c, 0, 0, 0);
-    }
-}
+__device__ __forceinline__ void pin_acc(acc16_t &c) { asm volatile("" : "+a"(c)); }
 
 // Two float32 -> one word of two 16-bit values (a in the low half), each rounded to
 // nearest even.
@@ -162,6 +144,12 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
         const f2_t f = {a, b};
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, h2_t));
     }
+}
+
+// Both 16-bit values of a word times a factor.
+template <int DT> __device__ __forceinline__ uint32_t scale2_words(uint32_t w, float f) {
+    if constexpr (DT == DT_BF16) return pack2<DT>(bf16_lo(w) * f, bf16_hi(w) * f);
+    else return pack2<DT>(f16_lo(w) * f, f16_hi(w) * f);
 }
 
 // Transposing LDS read of a 4 x 16 block of 16-bit values in each group of 16 lanes:
@@ -176,47 +164,63 @@ __device__ __forceinline__ u32x4_t lds_read16(const DS4HC_LDS char *p) {
 }
 
 // 16 bytes a lane from base + offset (the lane's own, in bytes) to LDS byte lds + 16 * lane
-// (lds the same in all lanes). Nothing is returned in registers. The compiler does not count
-// it among the wave's loads: wait_and_barrier() waits for it, before any lane reads the
-// bytes, and until then other loads' waits are longer than they need be, never shorter.
-// (The builtin's loads are counted, and every LDS read that may alias one of them then waits
-// for all of them, the tiles ahead included.) The s_nop is the wait state that a load to LDS
-// needs after a write of m0.
+// (lds the same in all lanes); nothing where `lanes` is 0 (it is that or all ones, and all
+// lanes are active where this stands: a branch around each of the loads that run beside a
+// tile's products would split them into small blocks). Nothing is returned in registers. The
+// compiler does not count it among the wave's loads: wait_and_barrier() waits for it, before
+// any lane reads the bytes, and until then other loads' waits are longer than they need be,
+// never shorter. (The builtin's loads are counted, and every LDS read that may alias one of
+// them then waits for all of them, those of the next tile included.) Wait states: a load to
+// LDS needs one after a write of m0, and a load 5 after a vector instruction that wrote its
+// scalar address (v_readlane may stand right before).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is reserved: nothing of the compiler's is kept in it
-__device__ __forceinline__ void load_to_lds16(const char *base, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+__device__ __forceinline__ void load_to_lds16(const char *base, uint32_t offset, uint32_t lds, uint64_t lanes) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\ts_nop 2\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
                  :
-                 : "s"(lds), "v"(offset), "s"(base)
+                 : "s"(lds), "v"(offset), "s"(base), "s"(lanes)
                  : "m0", "memory");
 }
-
 // The same from an address of each lane's own.
-__device__ __forceinline__ void load_to_lds16(const char *from, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+__device__ __forceinline__ void load_to_lds16(const char *from, uint32_t lds, uint64_t lanes) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b64 exec, -1"
                  :
-                 : "s"(lds), "v"(from)
+                 : "s"(lds), "v"(from), "s"(lanes)
                  : "m0", "memory");
 }
 #pragma clang diagnostic pop
+
+// Waits for the loads that the values come from: a wait that the compiler would otherwise
+// place at their first use, inside a loop, where it would wait for the next tile as well.
+__device__ __forceinline__ void loaded(u32x4_t &v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void loaded(int &v) { asm volatile("" : "+v"(v)); }
 
 // Byte address in LDS.
 __device__ __forceinline__ uint32_t lds_address(const void *p) {
     return (uint32_t)(uintptr_t)(const DS4HC_LDS void *)p;
 }
 
-// Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ float max_over_groups(float x) {
+// Maximum and sum over lanes l and l ^ 32.
+__device__ __forceinline__ float max_halves(float x) {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    return fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
 }
-__device__ __forceinline__ float sum_over_groups(float x) {
+__device__ __forceinline__ float sum_halves(float x) {
     auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    return __uint_as_float(a[0]) + __uint_as_float(a[1]);
+}
+
+// Largest of three, and of a result's 16. (The compiler would first rewrite every value that
+// comes out of an asm block, so that a NaN is quiet.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float max16(const acc16_t &s) {
+    const float a = max3(s[0], s[1], s[2]), b = max3(s[3], s[4], s[5]), c = max3(s[6], s[7], s[8]);
+    const float d = max3(s[9], s[10], s[11]), e = max3(s[12], s[13], s[14]);
+    return max3(max3(a, b, c), max3(d, e, s[15]), s[15]);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -66,6 +66,7 @@ struct AttnArgs {
     int64_t out_token, out_head;
     float *lse;  // may be null
     void *ws;
+    int members;  // workgroups of a cluster: launch_attn sets it
 };
 uint64_t attn_workspace_bytes(const Paged &c, int latent, int heads, int64_t N);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s);
