@@ -1,49 +1,293 @@
 // latent_prefill.hip -- attention over expanded keys and values of a ragged batch.
+//
+// Per query row (a token, one head) and key of its sequence:
+//   s = scale (qn . kn + qr . kr),  out = softmax(s) V.
+// One pass over the keys with a running maximum and sum; both products on the matrix unit:
+// 640 operations a (row, key) against some 26 bytes of keys and values a key and 128 rows, so
+// that the matrix unit bounds it, and beside it the vector unit's 16 exponentials for each 20
+// products of 32 x 32.
 #include "latent_device.hpp"
 
 namespace ds4hc {
 
 namespace {
 
-// Wave a (query, head): each lane holds 3 elements of the query and 2 of the
-// running output; one key at a time.
-template <int DT>
-__global__ __launch_bounds__(64) void prefill_kernel(PrefillArgs a) {
-    constexpr int DQ = PREFILL_NOPE + LATENT_ROPE, DKV = PREFILL_NOPE + PREFILL_VALUE;
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, n = (int)a.N;
-    const int b = sequence_of(a.cu_q, a.n_seqs, n, t);
-    if (b < 0) return;
-    const int q0 = cu_at(a.cu_q, b, n), few = cu_at(a.cu_q, b + 1, n) - q0;
-    const int k0 = cu_at(a.cu_k, b, (int)a.S), len = max(cu_at(a.cu_k, b + 1, (int)a.S) - k0, 0);
-    const int seen = a.full ? len : min(len, t - q0 + len - few + 1);
-    const elem_t<DT> *q = static_cast<const elem_t<DT> *>(a.q) + ((int64_t)t * a.heads + h) * DQ;
-    const float qa = elem_load<DT>(q + lane), qb = elem_load<DT>(q + 64 + lane), qr = elem_load<DT>(q + 128 + lane);
-    float top = -INFINITY, total = 0.f, oa = 0.f, ob = 0.f;
-    for (int j = 0; j < seen; ++j) {
-        const elem_t<DT> *k = static_cast<const elem_t<DT> *>(a.kv) + ((int64_t)(k0 + j) * a.heads + h) * DKV;
-        const elem_t<DT> *r = static_cast<const elem_t<DT> *>(a.k_rope) + (int64_t)(k0 + j) * a.k_rope_stride;
-        float s = qa * elem_load<DT>(k + lane) + qb * elem_load<DT>(k + 64 + lane) + qr * elem_load<DT>(r + lane);
-        for (int m = 32; m; m >>= 1) s += __shfl_xor(s, m);
-        s *= a.scale;
-        const float high = fmaxf(top, s), keep = top == high ? 1.f : expf(top - high);
-        const float p = expf(s - high);
-        total = total * keep + p;
-        oa = oa * keep + p * elem_load<DT>(k + 128 + lane);
-        ob = ob * keep + p * elem_load<DT>(k + 192 + lane);
-        top = high;
+constexpr int THREADS = 256, WAVES = 4, ROWS = 128;  // a workgroup: 32 rows a wave, all of one head
+constexpr int TOKENS = 64;                           // keys a tile
+constexpr int KV_BYTES = (PREFILL_NOPE + PREFILL_VALUE) * 2, ROPE_BYTES = LATENT_ROPE * 2;
+constexpr int ROPE_AT = TOKENS * KV_BYTES, TILE_BYTES = TOKENS * (KV_BYTES + ROPE_BYTES);
+constexpr int DQ = PREFILL_NOPE + LATENT_ROPE;
+constexpr int KNOPE = PREFILL_NOPE / 16, KSTEPS = DQ / 16, DBLOCKS = PREFILL_VALUE / 32;
+constexpr unsigned GRID_X = 1u << 20;                // workgroups in x (a dispatch has 2^32 threads a dimension)
+constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
+constexpr float LAZY = 8.f;  // the running maximum is raised only by more than this (in powers of 2)
+
+// Swizzle of the 16-byte chunks of a token's row in LDS: 16 values over 16 rows, the upper 2
+// bits 4 values over 4 rows (for the transposing reads, 64 bytes of 4 rows at a time).
+__device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+__device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
+
+// Row tile `nth` of the batch: its sequence and its first row there; -1 if there is none.
+__device__ __forceinline__ int find_tile(const PrefillArgs &a, int nth, int &row0) {
+    const int lane = threadIdx.x & 63, B = a.n_seqs, n = (int)a.N, per = (B + 63) / 64;
+    auto tiles = [&](int b) { return (max(cu_at(a.cu_q, b + 1, n) - cu_at(a.cu_q, b, n), 0) + ROWS - 1) / ROWS; };
+    int mine = 0;
+    for (int i = 0; i < per; ++i)
+        if (lane * per + i < B) mine += tiles(lane * per + i);
+    int upto = mine;
+    for (int m = 1; m < 64; m <<= 1) {
+        const int o = __shfl_up(upto, m);
+        if (lane >= m) upto += o;
     }
-    elem_t<DT> *o = static_cast<elem_t<DT> *>(a.out) + ((int64_t)t * a.heads + h) * PREFILL_VALUE;
-    o[lane] = elem_round<DT>(total == 0.f ? 0.f : oa / total);
-    o[64 + lane] = elem_round<DT>(total == 0.f ? 0.f : ob / total);
-    if (a.lse && lane == 0) a.lse[(int64_t)t * a.heads + h] = total == 0.f ? -INFINITY : top + logf(total);
+    const uint64_t in = __ballot(nth >= upto - mine && nth < upto);
+    if (!in) return -1;
+    const int who = __builtin_ctzll(in);
+    int rest = nth - __shfl(upto - mine, who);
+    for (int b = who * per; b < min(B, (who + 1) * per); ++b) {
+        const int t = tiles(b);
+        if (rest < t) {
+            row0 = rest * ROWS;
+            return b;
+        }
+        rest -= t;
+    }
+    return -1;
+}
+
+template <int DT>
+__global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int tiles) {
+    __shared__ __align__(256) char ring[2 * TILE_BYTES];  // two workgroups a CU fill its LDS
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    // heads are neighbours in the grid: with 8 of them or more an XCD keeps to its own heads' keys.
+    // The last row tiles see the most keys and go first.
+    const unsigned id = blockIdx.y * GRID_X + blockIdx.x;
+    const int head = id % a.heads;
+    int row0 = 0;
+    const int b = uniform(find_tile(a, tiles - 1 - (int)(id / a.heads), row0));
+    if (b < 0) return;
+    row0 = uniform(row0);
+    const int q0 = uniform(cu_at(a.cu_q, b, (int)a.N)), few = uniform(cu_at(a.cu_q, b + 1, (int)a.N)) - q0;
+    const int k0 = uniform(cu_at(a.cu_k, b, (int)a.S)), len = max(uniform(cu_at(a.cu_k, b + 1, (int)a.S)) - k0, 0);
+    // keys that row i sees: the first limit(i)
+    const int before = len - few;  // may be negative
+    auto limit = [&](int i) { return a.full ? len : max(min(len, i + before + 1), 0); };
+    const int n = (limit(min(row0 + ROWS, few) - 1) + TOKENS - 1) / TOKENS;  // tiles
+    const float scale2 = a.scale * LOG2E;
+    const int my = row0 + wave * 32 + (lane & 31);
+
+    float top = -INFINITY, from = 0.f, sum = 0.f;  // running maximum (what is subtracted: 0 if there is none), sum
+    acc16_t acc[DBLOCKS];
+#pragma unroll
+    for (int d = 0; d < DBLOCKS; ++d) {
+        acc[d] = acc16_t{};
+        pin_acc(acc[d]);
+    }
+
+    if (n > 0) {
+        const int lim = limit(min(my, few - 1));  // rows behind the last repeat it
+        const char *kv = static_cast<const char *>(a.kv) + ((int64_t)k0 * a.heads + head) * KV_BYTES;
+        const char *kr = static_cast<const char *>(a.k_rope) + (int64_t)k0 * a.k_rope_stride * 2;
+        const uint32_t kv_step = (uint32_t)a.heads * KV_BYTES;  // bytes between tokens, at most 2^19
+        constexpr int KV_LOADS = TOKENS * KV_BYTES / 1024 / WAVES, LOADS = KV_LOADS + TOKENS * ROPE_BYTES / 1024 / WAVES;
+        // The wave's load number i of tile t: two tokens' keys and values, or 8 tokens' rope keys. Behind
+        // the sequence's last token that one is loaded again (what lies there is another's, and may be
+        // NaN, which a weight of 0 would not hide).
+        auto load = [&](int i, int t, uint32_t l, uint32_t buf, uint64_t lanes) {
+            const int last = len - 1 - t * TOKENS;
+            if (i < KV_LOADS) {
+                const int first = (wave * KV_LOADS + i) * 2, r = first + (l >> 5);
+                const uint32_t off = (uint32_t)__builtin_elementwise_min(r, last) * kv_step + (((l & 31) ^ swz(r)) << 4);
+                load_to_lds16(kv + (int64_t)t * TOKENS * kv_step, off, buf + first * KV_BYTES, lanes);
+            } else {
+                const int first = (wave * (LOADS - KV_LOADS) + i - KV_LOADS) * 8, r = first + (l >> 3);
+                const int64_t token = (int64_t)t * TOKENS + __builtin_elementwise_min(r, last);
+                load_to_lds16(kr + token * a.k_rope_stride * 2 + (((l & 7) ^ swz_rope(r)) << 4), buf + ROPE_AT + first * ROPE_BYTES, lanes);
+            }
+        };
+        const uint32_t ring_at = lds_address(ring);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) load(i, 0, here(lane), ring_at, ~0ull);
+        u32x4_t q[KSTEPS];
+        {
+            const elem_t<DT> *from_q = static_cast<const elem_t<DT> *>(a.q) + ((int64_t)(q0 + min(my, few - 1)) * a.heads + head) * DQ + (lane >> 5) * 8;
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k) q[k] = *reinterpret_cast<const u32x4_t *>(from_q + k * 16);
+#pragma unroll
+            for (int k = 0; k < KSTEPS; ++k) loaded(q[k]);
+        }
+
+        auto tile = [&](int t, uint32_t at, uint32_t at_next) {
+            DS4HC_LDS char *buf = (DS4HC_LDS char *)(uintptr_t)at;
+            const int j0 = t * TOKENS;
+            const bool masked = j0 + TOKENS > limit(row0);
+            uint64_t bad = 0;  // tokens whose values are not all finite
+            if (masked) {  // the same in all waves, and so is what they find
+                for (int i = 0; i < TOKENS / 4; ++i) {
+                    const u32x4_t w = lds_read16(buf + (i * 4 + (here(lane) >> 4)) * KV_BYTES + PREFILL_NOPE * 2 + (here(lane) & 15) * 16);
+                    const uint64_t lanes = __ballot(word_not_finite<DT>(w.x) || word_not_finite<DT>(w.y) || word_not_finite<DT>(w.z) || word_not_finite<DT>(w.w));
+                    for (int r = 0; r < 4; ++r) bad |= (uint64_t)((lanes >> (16 * r) & 0xFFFF) != 0) << (i * 4 + r);
+                }
+                if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
+                    wait_and_barrier<63>();
+                    for (int i = threadIdx.x; i < TOKENS * 16; i += THREADS)
+                        if ((bad >> (i >> 4)) & 1) {
+                            const uint32_t zero = here(0);
+                            *reinterpret_cast<DS4HC_LDS u32x4_t *>(buf + (i >> 4) * KV_BYTES + PREFILL_NOPE * 2 + (i & 15) * 16) = u32x4_t{zero, zero, zero, zero};
+                        }
+                    wait_and_barrier<63>();
+                }
+            }
+            // LDS offsets of this lane's reads for the first k step, rope step and block of values; the
+            // others' chunks differ in higher bits, which an xor reaches
+            const int l = here(lane), lr = l & 31, lh = l >> 5;
+            const uint32_t k_at = lr * KV_BYTES + ((lh ^ swz(lr)) << 4);
+            const uint32_t r_at = ROPE_AT + lr * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
+            const int vr = lh * 4 + ((l >> 2) & 3);
+            const uint32_t v_at = vr * KV_BYTES + PREFILL_NOPE * 2 + (((((l >> 4) & 1) << 1 | ((l >> 1) & 1)) ^ swz(vr)) << 4) + (l & 1) * 8;
+            const uint32_t v8_at = (v_at ^ 32) + 8 * KV_BYTES;  // 8 rows on, swz differs in bit 1
+
+            // S^T = K Q^T of 32 tokens, the operands of the next products on their way; `between`
+            // gives other work to the vector unit while the matrix unit is busy
+            constexpr int AHEAD = 4;
+            auto products_k = [&](int step, acc16_t &s, auto &&between) {
+                auto read = [&](int k) {
+                    return k < KNOPE ? lds_read16(buf + (k_at ^ (k << 5)) + step * 32 * KV_BYTES)
+                                     : lds_read16(buf + (r_at ^ ((k - KNOPE) << 5)) + step * 32 * ROPE_BYTES);
+                };
+                u32x4_t x[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) x[i] = read(i);
+#pragma unroll
+                for (int i = 0; i < KSTEPS; ++i) {
+                    const u32x4_t now = x[i % AHEAD];
+                    if (i == 0) mfma32_first_v<DT>(now, q[i], s);
+                    else mfma32_v<DT>(now, q[i], s);
+                    if (i + AHEAD < KSTEPS) x[i % AHEAD] = read(i + AHEAD);
+                    between(i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of S^T's rows, for both operands
+            constexpr int VAHEAD = 4;
+            auto products_v = [&](int step, const u32x4_t (&p)[2], auto &&between) {
+                auto read = [&](int i) {  // block i % DBLOCKS, tokens 16 (i / DBLOCKS) .. + 15
+                    const uint32_t chunk = (i % DBLOCKS) << 6, off = (step * 32 + (i / DBLOCKS) * 16) * KV_BYTES;
+                    const u32x2_t lo = lds_read_tr(buf + (v_at ^ chunk) + off), hi = lds_read_tr(buf + (v8_at ^ chunk) + off);
+                    return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+                };
+                u32x4_t v[VAHEAD];
+#pragma unroll
+                for (int i = 0; i < VAHEAD; ++i) v[i] = read(i);
+#pragma unroll
+                for (int i = 0; i < DBLOCKS * 2; ++i) {
+                    acc[i % DBLOCKS] = mfma32<DT>(v[i % VAHEAD], p[i / DBLOCKS], acc[i % DBLOCKS]);
+                    if (i + VAHEAD < DBLOCKS * 2) v[i % VAHEAD] = read(i + VAHEAD);
+                    between(i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            // Softmax of a step, in pieces. The mask, and the largest logit (of the lane's row).
+            const int sees_n = lim - j0;
+            const uint64_t sees = sees_n >= 64 ? ~0ull : sees_n <= 0 ? 0 : (1ull << sees_n) - 1;
+            auto largest = [&](int step, acc16_t &s) {
+                if (masked) {
+                    const int at0 = step * 32 + (here(lane) >> 5) * 4;
+                    const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const int r = 8 * (i / 4) + i % 4;
+                        s[i] = (nan >> r) & 1 ? NAN : (see >> r) & 1 ? s[i] : -INFINITY;
+                    }
+                }
+                return max_halves(max16(s)) * scale2;
+            };
+            // A new running maximum. It is a whole number, so that what is there is scaled by a power
+            // of 2, without rounding, weights that are already 16-bit values included.
+            auto raise = [&](float high) {
+                const float was = top;
+                top = fmaxf(top, ceilf(high));
+                from = top == -INFINITY ? 0.f : top;
+                const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
+                sum *= keep;
+#pragma unroll
+                for (int d = 0; d < DBLOCKS; ++d) {
+                    pin_acc(acc[d]);
+                    acc[d] *= keep;
+                    pin_acc(acc[d]);
+                }
+                return keep;
+            };
+            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {  // weights 2 i and 2 i + 1
+                const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
+                sum += e0;
+                sum += e1;
+                p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+            };
+            const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
+            const uint32_t load_lane = here(lane);
+            acc16_t s, s1;
+            u32x4_t p[2], p1[2];
+            products_k(0, s, [&](int i) {
+                if (i < LOADS) load(i, t + 1, load_lane, at_next, lanes);
+            });
+            mfma_results(s);
+            float high = largest(0, s);
+            if (__any(high > top + LAZY)) raise(high);
+            products_k(1, s1, [&](int i) {
+                if (i < 8) weight2(s, i, p);
+            });
+            mfma_results(s1);
+            high = largest(1, s1);
+            if (__any(high > top + LAZY)) {
+                const float keep = raise(high);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
+            }
+            products_v(0, p, [&](int i) { weight2(s1, i, p1); });
+            products_v(1, p1, [](int) {});
+        };
+
+        // the next tile's loads run beside this one's products. All waves are done with tile t - 1 when
+        // they meet at the barrier of tile t, so its buffer takes tile t + 1.
+        for (int t = 0; t < n; ++t) {
+            wait_and_barrier<0>();
+            tile(t, ring_at + (t & 1) * TILE_BYTES, ring_at + ((t + 1) & 1) * TILE_BYTES);
+        }
+    }
+
+    // ---- results
+#pragma unroll
+    for (int d = 0; d < DBLOCKS; ++d) pin_acc(acc[d]);
+    const int l = here(lane), lh = l >> 5;
+    const float all = sum_halves(sum), inv = all == 0.f ? 0.f : 1.f / all;
+    if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+    // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
+    wait_and_barrier<63>();  // the last tile has been read by all
+    constexpr int OUT_BYTES = PREFILL_VALUE * 2;
+    char *rows_at = ring + wave * 32 * OUT_BYTES;
+#pragma unroll
+    for (int d = 0; d < DBLOCKS; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            *reinterpret_cast<u32x2_t *>(rows_at + (l & 31) * OUT_BYTES + (((d * 4 + i) ^ (l & 15)) << 4) + lh * 8) = u32x2_t{
+                pack2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv), pack2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
+    char *out = static_cast<char *>(a.out) + ((int64_t)(q0 + row0 + wave * 32) * a.heads + head) * OUT_BYTES;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const int r = i + (l >> 4), c = l & 15;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t *>(rows_at + r * OUT_BYTES + ((c ^ (r & 15)) << 4));
+        if (row0 + wave * 32 + r < few) *reinterpret_cast<u32x4_t *>(out + (int64_t)r * a.heads * OUT_BYTES + c * 16) = v;
+    }
 }
 
 }  // namespace
 
 hipError_t launch_prefill(const PrefillArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)a.N, (unsigned)a.heads);
-    return a.dt == DT_BF16 ? launch_kernel(prefill_kernel<DT_BF16>, grid, dim3(64), s, a)
-                           : launch_kernel(prefill_kernel<DT_F16>, grid, dim3(64), s, a);
+    const int tiles = (int)(a.N / ROWS) + (int)(a.n_seqs < a.N ? a.n_seqs : a.N);  // at most
+    const uint64_t groups = (uint64_t)tiles * (uint64_t)a.heads;  // at most 2^31: N * heads is below 2^30
+    const dim3 grid((unsigned)(groups < GRID_X ? groups : GRID_X), (unsigned)((groups + GRID_X - 1) / GRID_X));
+    return a.dt == DT_BF16 ? launch_kernel(prefill_kernel<DT_BF16>, grid, dim3(THREADS), s, a, tiles)
+                           : launch_kernel(prefill_kernel<DT_F16>, grid, dim3(THREADS), s, a, tiles);
 }
 
 }  // namespace ds4hc
