@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -484,34 +485,64 @@ def ds4hc_latent_prefill_raw(N, S, n_seqs, heads, dtype, scale, flags, q, kv, k_
                                        cu_q, cu_k, out, lse, stream)
 
 
-def _any_code(t, name, floats=(DS4HC_F32, DS4HC_BF16, DS4HC_F16)) -> int:
+# These calls take a few microseconds on the GPU, so their checks are made quick: one
+# look at each tensor, and the reason spelt out only for what did not pass.
+
+@functools.lru_cache(maxsize=None)
+def _codes():
     torch = _torch()
-    code = {torch.float32: DS4HC_F32, torch.bfloat16: DS4HC_BF16, torch.float16: DS4HC_F16}.get(t.dtype)
-    if code not in floats:
+    return {torch.float32: DS4HC_F32, torch.bfloat16: DS4HC_BF16, torch.float16: DS4HC_F16}
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides(token: int, head: int) -> Strides:
+    return Strides(token, head)
+
+
+def _any_code(t, name, halves=False) -> int:
+    code = _codes().get(t.dtype)
+    if code is None or (halves and code == DS4HC_F32):
         raise TypeError(f"{name}: dtype {t.dtype} is not supported")
     return code
 
 
-def _here(stream, **tensors):
-    """Every tensor on the device that the call's stream runs on (the library
-    launches on the calling thread's current device)."""
+def _device(stream) -> int:
+    """The device that the call runs on: the calling thread's current one."""
+    here = _torch().cuda.current_device()
+    if stream is not None and stream.device.index != here:
+        raise ValueError(f"the stream is on {stream.device}, the call on the current device, cuda:{here}")
+    return here
+
+
+def _tensors(**tensors):
+    """Device tensors (the rest of a call's checks are made one by one)."""
     torch = _torch()
     for name, t in tensors.items():
-        if t is None:
-            continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
-        here = torch.cuda.current_device()
-        if t.device.index != here or (stream is not None and stream.device.index != here):
-            raise ValueError(f"{name} is on {t.device}: the call runs on the current device, "
-                             f"cuda:{here}, and so must its stream")
 
 
-def _rows(t, dims, dtype, name):
-    """A [N, heads, dim] (or [N, dim]) view whose last dimension is dense."""
-    if t.dim() != len(dims) or any(d is not None and n != d for n, d in zip(t.shape, dims)) or t.dtype != dtype:
-        raise ValueError(f"{name}: expected {tuple(dims)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _raw_stream(stream, here) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+
+
+def _dense(t, shape, dtype, name, here):
+    """A dense array on the call's device."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != here:
+        _tensors(**{name: t})
+        if t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, the call runs on the current device, cuda:{here}")
+        _need(t, shape, dtype, name)
+
+
+def _rows(t, shape, dtype, name, here):
+    """An array on the call's device whose last dimension is dense."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != here or (shape[-1] > 1 and t.stride(-1) != 1):
+        _tensors(**{name: t})
+        if t.get_device() != here:
+            raise ValueError(f"{name} is on {t.device}, the call runs on the current device, cuda:{here}")
+        if t.shape != shape or t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
         raise ValueError(f"{name}: the last dimension must be dense")
 
 
@@ -535,38 +566,46 @@ def ds4hc_rope(x, positions, inv_freq, *, interleaved=True, inverse=False, ampli
     a head is fine, the last dimension dense), positions [N] int64, inv_freq [dim / 2]
     float64. out may be x itself (in place). Returns out [N, heads, dim]."""
     torch = _torch()
-    _here(stream, x=x, positions=positions, inv_freq=inv_freq, out=out)
+    if not getattr(x, "is_cuda", False):
+        _tensors(x=x)
+    here, shape, dtype = _device(stream), x.shape, x.dtype
     dt = _any_code(x, "x")
-    if x.dim() != 3:
-        raise ValueError(f"x must be [N, heads, dim], got {tuple(x.shape)}")
-    N, heads, dim = x.shape
-    _rows(x, (N, heads, dim), x.dtype, "x")
-    _need(positions, (N,), torch.int64, "positions")
-    _need(inv_freq, (dim // 2,), torch.float64, "inv_freq")
+    if len(shape) != 3:
+        raise ValueError(f"x must be [N, heads, dim], got {tuple(shape)}")
+    N, heads, dim = shape
+    _rows(x, shape, dtype, "x", here)
+    _dense(positions, (N,), torch.int64, "positions", here)
+    _dense(inv_freq, (dim // 2,), torch.float64, "inv_freq", here)
     if out is None:
         with _on(stream):
-            out = _empty((N, heads, dim), x.dtype, x.device)
-    _rows(out, (N, heads, dim), x.dtype, "out")
+            out = _empty(shape, dtype, x.device)
+    else:
+        _rows(out, shape, dtype, "out", here)
+    xs, os_ = x.stride(), out.stride()
     flags = (0 if interleaved else DS4HC_ROPE_HALF) | (DS4HC_ROPE_INVERSE if inverse else 0)
-    _check(ds4hc_rope_raw(N, heads, dim, dt, _ptr(x), x.stride()[:2], _ptr(positions), _ptr(inv_freq),
-                          amplitude, flags, _ptr(out), out.stride()[:2], _stream(stream)),
-           "ds4hc_rope")
+    st = load().ds4hc_rope(N, heads, dim, dt, x.data_ptr(), _strides(xs[0], xs[1]), positions.data_ptr(),
+                           inv_freq.data_ptr(), amplitude, flags, out.data_ptr(), _strides(os_[0], os_[1]),
+                           _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_rope")
     return out
 
 
-def _paged(cache, cu_q, kv_len, block_table):
+def _paged(cache, cu_q, kv_len, block_table, here=None):
     torch = _torch()
-    if cache.dim() != 3 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous [pages, page_size, d_latent + 64] tensor")
-    pages, page_size, D = cache.shape
-    if kv_len.dim() != 1 or block_table.dim() != 2:
-        raise ValueError("kv_len must be [B] and block_table [B, max_pages]")
+    here = torch.cuda.current_device() if here is None else here
+    shape, table = cache.shape, block_table.shape
+    if len(shape) != 3 or kv_len.dim() != 1 or len(table) != 2:
+        raise ValueError("cache must be [pages, page_size, d_latent + 64], kv_len [B] and block_table [B, max_pages]")
+    pages, page_size, D = shape
     B = kv_len.shape[0]
-    _need(cu_q, (B + 1,), torch.int32, "cu_q")
-    _need(kv_len, (B,), torch.int32, "kv_len")
-    _need(block_table, (B, block_table.shape[1]), torch.int32, "block_table")
-    return PagedCache(_any_code(cache, "cache", (DS4HC_BF16, DS4HC_F16)), D - 64, 64, page_size, pages, B,
-                      block_table.shape[1], cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr())
+    i32 = torch.int32
+    _dense(cache, shape, cache.dtype, "cache", here)
+    _dense(cu_q, (B + 1,), i32, "cu_q", here)
+    _dense(kv_len, (B,), i32, "kv_len", here)
+    _dense(block_table, (B, table[1]), i32, "block_table", here)
+    return PagedCache(_any_code(cache, "cache", True), D - 64, 64, page_size, pages, B, table[1], cu_q.data_ptr(),
+                      kv_len.data_ptr(), block_table.data_ptr())
 
 
 def ds4hc_latent_append(kv, positions, inv_freq, cache, cu_q, kv_len, block_table, *,
@@ -578,20 +617,23 @@ def ds4hc_latent_append(kv, positions, inv_freq, cache, cu_q, kv_len, block_tabl
     cu_q [B + 1], kv_len [B], block_table [B, max_pages] int32, norm_weight [d_latent]
     float32 or None (no norm). Returns cache."""
     torch = _torch()
-    _here(stream, kv=kv, positions=positions, inv_freq=inv_freq, cache=cache, cu_q=cu_q, kv_len=kv_len,
-          block_table=block_table, norm_weight=norm_weight)
-    c = _paged(cache, cu_q, kv_len, block_table)
+    if not getattr(kv, "is_cuda", False):
+        _tensors(kv=kv)
+    here = _device(stream)
+    c = _paged(cache, cu_q, kv_len, block_table, here)
     src = _any_code(kv, "kv")
     N, D = kv.shape[0], cache.shape[2]
-    _rows(kv, (N, D), kv.dtype, "kv")
-    _need(positions, (N,), torch.int64, "positions")
-    _need(inv_freq, (32,), torch.float64, "inv_freq")
+    _rows(kv, (N, D), kv.dtype, "kv", here)
+    _dense(positions, (N,), torch.int64, "positions", here)
+    _dense(inv_freq, (32,), torch.float64, "inv_freq", here)
     if norm_weight is not None:
-        _need(norm_weight, (c.d_latent,), torch.float32, "norm_weight")
-    _check(ds4hc_latent_append_raw(c, N, src, _ptr(kv), kv.stride(0) if N > 1 else D, _ptr(norm_weight),
-                                   rms_eps, _ptr(positions), _ptr(inv_freq), amplitude,
-                                   0 if interleaved else DS4HC_ROPE_HALF, _ptr(cache), _stream(stream)),
-           "ds4hc_latent_append")
+        _dense(norm_weight, (c.d_latent,), torch.float32, "norm_weight", here)
+    st = load().ds4hc_latent_append(ctypes.byref(c), N, src, kv.data_ptr(), kv.stride(0) if N > 1 else D,
+                                    None if norm_weight is None else norm_weight.data_ptr(), rms_eps,
+                                    positions.data_ptr(), inv_freq.data_ptr(), amplitude,
+                                    0 if interleaved else DS4HC_ROPE_HALF, cache.data_ptr(), _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_latent_append")
     return cache
 
 
@@ -603,31 +645,45 @@ def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, sca
     tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None). Rows
     behind the last sequence are left as they were."""
     torch = _torch()
-    _here(stream, q_latent=q_latent, q_rope=q_rope, cache=cache, cu_q=cu_q, kv_len=kv_len,
-          block_table=block_table, tree_mask=tree_mask, out=out, lse=lse, workspace=workspace)
-    c = _paged(cache, cu_q, kv_len, block_table)
+    if not getattr(q_latent, "is_cuda", False):
+        _tensors(q_latent=q_latent)
+    here = _device(stream)
+    c = _paged(cache, cu_q, kv_len, block_table, here)
+    dtype = cache.dtype
     if q_latent.dim() != 3:
         raise ValueError(f"q_latent must be [N, heads, d_latent], got {tuple(q_latent.shape)}")
     N, heads, _ = q_latent.shape
-    _rows(q_latent, (N, heads, c.d_latent), cache.dtype, "q_latent")
-    _rows(q_rope, (N, heads, 64), cache.dtype, "q_rope")
+    shape = (N, heads, c.d_latent)
+    _rows(q_latent, shape, dtype, "q_latent", here)
+    _rows(q_rope, (N, heads, 64), dtype, "q_rope", here)
     words = 0
     if tree_mask is not None:
         words = tree_mask.shape[-1]
-        _need(tree_mask, (N, words), torch.int64, "tree_mask")
+        _dense(tree_mask, (N, words), torch.int64, "tree_mask", here)
     with _on(stream):
         if out is None:
-            out = _empty((N, heads, c.d_latent), cache.dtype, cache.device)
-        if lse is None and want_lse:
+            out = _empty(shape, dtype, cache.device)
+        else:
+            _rows(out, shape, dtype, "out", here)
+        if lse is not None:
+            _dense(lse, (N, heads), torch.float32, "lse", here)
+        elif want_lse:
             lse = _empty((N, heads), torch.float32, cache.device)
-        workspace, ws_bytes = _scratch(ds4hc_latent_attn_workspace_bytes(c, N, heads), workspace, cache.device)
-    _rows(out, (N, heads, c.d_latent), cache.dtype, "out")
-    if lse is not None:
-        _need(lse, (N, heads), torch.float32, "lse")
-    _check(ds4hc_latent_attn_raw(c, N, heads, scale, _ptr(q_latent), q_latent.stride()[:2], _ptr(q_rope),
-                                 q_rope.stride()[:2], _ptr(cache), _ptr(tree_mask), words, _ptr(out),
-                                 out.stride()[:2], _ptr(lse), _ptr(workspace), ws_bytes, _stream(stream)),
-           "ds4hc_latent_attn")
+        if workspace is not None:
+            _tensors(workspace=workspace)
+            if workspace.get_device() != here or not workspace.is_contiguous():
+                raise ValueError("workspace must be a dense array on the call's device")
+        workspace, ws_bytes = _scratch(load().ds4hc_latent_attn_workspace_bytes(ctypes.byref(c), N, heads), workspace,
+                                       cache.device)
+    ls, rs, os_ = q_latent.stride(), q_rope.stride(), out.stride()
+    st = load().ds4hc_latent_attn(ctypes.byref(c), N, heads, scale, q_latent.data_ptr(), _strides(ls[0], ls[1]),
+                                  q_rope.data_ptr(), _strides(rs[0], rs[1]), cache.data_ptr(),
+                                  None if tree_mask is None else tree_mask.data_ptr(), words, out.data_ptr(),
+                                  _strides(os_[0], os_[1]), None if lse is None else lse.data_ptr(),
+                                  None if workspace is None else workspace.data_ptr(), ws_bytes,
+                                  _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_latent_attn")
     return out, lse
 
 
@@ -638,27 +694,32 @@ def ds4hc_latent_prefill(q, kv, k_rope, cu_q, cu_k, *, scale, causal=True, out=N
     strided), cu_q and cu_k [B + 1] int32. Returns (out [N, heads, 128], lse [N, heads]
     float32 or None). Rows behind the last sequence are left as they were."""
     torch = _torch()
-    _here(stream, q=q, kv=kv, k_rope=k_rope, cu_q=cu_q, cu_k=cu_k, out=out, lse=lse)
-    dt = _any_code(q, "q", (DS4HC_BF16, DS4HC_F16))
+    if not getattr(q, "is_cuda", False):
+        _tensors(q=q)
+    here, dtype = _device(stream), q.dtype
+    dt = _any_code(q, "q", True)
     if q.dim() != 3 or kv.dim() != 3 or cu_q.dim() != 1:
         raise ValueError("q must be [N, heads, 192], kv [S, heads, 256] and cu_q [B + 1]")
     N, heads, _ = q.shape
     S, B = kv.shape[0], cu_q.shape[0] - 1
-    _need(q, (N, heads, 192), q.dtype, "q")
-    _need(kv, (S, heads, 256), q.dtype, "kv")
-    _rows(k_rope, (S, 64), q.dtype, "k_rope")
-    _need(cu_q, (B + 1,), torch.int32, "cu_q")
-    _need(cu_k, (B + 1,), torch.int32, "cu_k")
+    _dense(q, (N, heads, 192), dtype, "q", here)
+    _dense(kv, (S, heads, 256), dtype, "kv", here)
+    _rows(k_rope, (S, 64), dtype, "k_rope", here)
+    _dense(cu_q, (B + 1,), torch.int32, "cu_q", here)
+    _dense(cu_k, (B + 1,), torch.int32, "cu_k", here)
     with _on(stream):
         if out is None:
-            out = _empty((N, heads, 128), q.dtype, q.device)
-        if lse is None and want_lse:
+            out = _empty((N, heads, 128), dtype, q.device)
+        else:
+            _dense(out, (N, heads, 128), dtype, "out", here)
+        if lse is not None:
+            _dense(lse, (N, heads), torch.float32, "lse", here)
+        elif want_lse:
             lse = _empty((N, heads), torch.float32, q.device)
-    _need(out, (N, heads, 128), q.dtype, "out")
-    if lse is not None:
-        _need(lse, (N, heads), torch.float32, "lse")
-    _check(ds4hc_latent_prefill_raw(N, S, B, heads, dt, scale, 0 if causal else DS4HC_ATTN_FULL, _ptr(q),
-                                    _ptr(kv), _ptr(k_rope), k_rope.stride(0) if S > 1 else 64, _ptr(cu_q),
-                                    _ptr(cu_k), _ptr(out), _ptr(lse), _stream(stream)),
-           "ds4hc_latent_prefill")
+    st = load().ds4hc_latent_prefill(N, S, B, heads, dt, scale, 0 if causal else DS4HC_ATTN_FULL, q.data_ptr(),
+                                     kv.data_ptr(), k_rope.data_ptr(), k_rope.stride(0) if S > 1 else 64,
+                                     cu_q.data_ptr(), cu_k.data_ptr(), out.data_ptr(),
+                                     None if lse is None else lse.data_ptr(), _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_latent_prefill")
     return out, lse

@@ -73,8 +73,7 @@ struct Seq {
 
 template <class S> __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
     Seq s;
-    const int q0 = cu_at(a.c.cu_q, b, (int)a.N);
-    s.few = max(cu_at(a.c.cu_q, b + 1, (int)a.N) - q0, 0);
+    s.few = max(cu_at(a.c.cu_q, b + 1, (int)a.N) - cu_at(a.c.cu_q, b, (int)a.N), 0);
     s.len = kv_len_at(a.c, b);
     s.row_tiles = (int)(((int64_t)s.few * a.heads + S::ROWS - 1) / S::ROWS);
     s.kv_tiles = max((s.len + S::TOKENS - 1) / S::TOKENS, 1);  // no token: one empty tile, to write the zeros
@@ -104,13 +103,14 @@ __device__ __forceinline__ int64_t wave_sum(int64_t v) {
 // batch, and (b < 0 if there is none) the sequence that the cluster's first unit belongs to and
 // its place there.
 template <class S>
-__device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, int &extra, int64_t cluster, int &b_out, int64_t &off) {
+__device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, int &extra, int64_t cluster, int &b_out, int64_t &off, Seq &at_b) {
     const int lane = threadIdx.x & 63, B = a.c.n_seqs, per = (B + 63) / 64;
     int64_t tiles = 0, batches = 0;
+    Seq s{};
     for (int i = 0; i < per; ++i) {
         const int b = lane * per + i;
         if (b < B) {
-            const Seq s = sequence<S>(a, b);
+            s = sequence<S>(a, b);
             batches += s.batches(a.members);
             tiles += (int64_t)s.batches(a.members) * s.kv_tiles;
         }
@@ -125,12 +125,20 @@ __device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, 
     if (at >= total) return total;
     const int who = __builtin_ctzll(__ballot(at >= upto - mine && at < upto));
     int64_t rest = at - __shfl(upto - mine, who);
+    if (per == 1) {  // the lane's own sequence
+        b_out = who;
+        off = rest;
+        auto of = [&](int v) { return __builtin_amdgcn_readlane(v, who); };
+        at_b = {of(s.few), of(s.len), of(s.row_tiles), of(s.kv_tiles)};
+        return total;
+    }
     for (int b = who * per; b < min(B, (who + 1) * per); ++b) {
-        const Seq s = sequence<S>(a, b);
+        s = sequence<S>(a, b);
         const int64_t w = (int64_t)s.batches(a.members) * (s.kv_tiles + extra);
         if (rest < w) {
             b_out = b;
             off = rest;
+            at_b = s;
             break;
         }
         rest -= w;
@@ -163,7 +171,8 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 
     int64_t share, off = 0;
     int b, extra;
-    const int64_t total = find_unit<S>(a, share, extra, cluster, b, off);
+    Seq sq{};
+    const int64_t total = find_unit<S>(a, share, extra, cluster, b, off, sq);
     b = uniform(b);
     off = uniform(off);
     extra = uniform(extra);
@@ -172,7 +181,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         if (cluster == 0) head->share = share;
         Start at = {b, 0, 0, 0};
         if (b >= 0) {
-            const int each = sequence<S>(a, b).kv_tiles + extra;
+            const int each = sq.kv_tiles + extra;
             at.batch = (int)(off / each);
             at.tile = max((int)(off - (int64_t)at.batch * each) - extra, 0);
         }
@@ -185,11 +194,10 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 
     bool first_part = true;
     while (left > 0) {
-        Seq sq = sequence<S>(a, b);
         sq = {uniform(sq.few), uniform(sq.len), uniform(sq.row_tiles), uniform(sq.kv_tiles)};
         const int each = sq.kv_tiles + extra;  // units of a batch
         if (off >= (int64_t)sq.batches(a.members) * each) {  // next sequence (the units in all bound b)
-            ++b;
+            sq = sequence<S>(a, ++b);
             off = 0;
             continue;
         }
@@ -236,14 +244,14 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             if (tile >= t_first + n) return -1;
             if (tile - pages_from >= 64 >> e_shift) {
                 pages_from = tile;
-                const int e = here(lane), in_tile = e >> e_shift;
+                const int e = lane_here(), in_tile = e >> e_shift;
                 const int j = (tile + in_tile) * S::TOKENS + ((e - (in_tile << e_shift)) << a.c.page_shift);
                 pages = -1;
                 if (tile + in_tile < t_first + n && j < sq.len) pages = a.c.block_table[(int64_t)b * a.c.max_pages + (j >> a.c.page_shift)];
                 if (pages >= a.c.n_pages) pages = -1;
                 loaded(pages);
             }
-            const int r = here(lane) & (S::TOKENS - 1), j = tile * S::TOKENS + r;
+            const int r = lane_here() & (S::TOKENS - 1), j = tile * S::TOKENS + r;
             const int page = from_lane(pages, ((tile - pages_from) << e_shift) + (e_shift ? r >> a.c.page_shift : 0));
             return page < 0 || j >= sq.len ? -1 : (page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
         };
@@ -283,7 +291,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         auto address = [&](int row) { return (uint64_t)cache + (uint64_t)(uint32_t)row * (S::D * 2); };
         auto load_all = [&](int rows, uint32_t buf) {
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) load(i, address(rows), here(lane) * 16, buf, ~0ull);
+            for (int i = 0; i < LOADS; ++i) load(i, address(rows), lane_here() * 16, buf, ~0ull);
         };
 
         // Tile t (tokens `ok`) in LDS at `at`, and the loads of the next one, if there is one, beside it.
@@ -315,7 +323,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             // LDS offsets of this lane's reads for the first k step, rope step and block of the
             // output; the others' chunks differ in higher bits, which an xor reaches. Made anew for
             // every tile: there are no registers to keep them.
-            const int l = here(lane), lr = l & 31, lh = l >> 5;
+            const int l = lane_here(), lr = l & 31, lh = l >> 5;
             const int t0 = set * S::STEPS * 32;  // first token of the wave
             const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + ((lh ^ swz(lr)) << 4);
             const uint32_t r0 = S::ROPE_AT + (t0 + lr) * 128 + ((lh ^ swz_rope(lr)) << 4);
@@ -373,7 +381,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             if (masked) sees = sees_of_tile(a, q0 + tok, tok, j0 - context) & ok;
             auto largest = [&](int step, acc16_t &s) {
                 if (masked) {
-                    const int at0 = t0 + step * 32 + (here(lane) >> 5) * 4;
+                    const int at0 = t0 + step * 32 + (lane_here() >> 5) * 4;
                     const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -391,11 +399,13 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
+                if (__any(was != -INFINITY)) {  // (the first maximum: the sums are 0)
 #pragma unroll
-                for (int d = 0; d < S::DBLOCKS; ++d) {
-                    pin_acc(acc[d]);
-                    acc[d] *= keep;
-                    pin_acc(acc[d]);
+                    for (int d = 0; d < S::DBLOCKS; ++d) {
+                        pin_acc(acc[d]);
+                        acc[d] *= keep;
+                        pin_acc(acc[d]);
+                    }
                 }
                 return keep;
             };
@@ -411,7 +421,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             static_assert(LOAD_EVERY >= 1, "a place for each load");
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < t_first + n ? -1 : 0));
             const uint64_t from = address(rows);
-            const uint32_t lane16 = here(lane) * 16;
+            const uint32_t lane16 = lane_here() * 16;
             auto load_some = [&](int i) {
                 if (i % LOAD_EVERY == 0 && i / LOAD_EVERY < LOADS) load(i / LOAD_EVERY, from, lane16, at_next, lanes);
             };
@@ -473,7 +483,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         // ---- the part's result
 #pragma unroll
         for (int d = 0; d < S::DBLOCKS; ++d) pin_acc(acc[d]);
-        const int l = here(lane), lh = l >> 5, my_row = row0 + (l & 31), head = my_row - tok * a.heads;
+        const int l = lane_here(), lh = l >> 5, my_row = row0 + (l & 31), head = my_row - tok * a.heads;
         const bool whole = t_first == 0 && n == sq.kv_tiles, mine = my_row < n_rows;  // (a part's rows behind the last: never looked at)
         const int in = my_row - row_tile * S::ROWS;
         float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);

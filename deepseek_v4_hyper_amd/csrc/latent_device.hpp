@@ -55,6 +55,14 @@ __device__ __forceinline__ uint32_t here(uint32_t v) {
     return v;
 }
 
+// The lane's number, made anew where it stands: two instructions in place of a register that
+// is held, or spilled, over a loop.
+__device__ __forceinline__ int lane_here() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
+
 // Cache row of token j (0 <= j < max_pages << page_shift) of sequence b, -1 if
 // its page is not in the cache.
 __device__ __forceinline__ int64_t cache_row(const Paged &c, int b, int j) {

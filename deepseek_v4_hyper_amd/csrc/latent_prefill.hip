@@ -106,7 +106,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
         };
         const uint32_t ring_at = lds_address(ring);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, 0, here(lane), ring_at, ~0ull);
+        for (int i = 0; i < LOADS; ++i) load(i, 0, lane_here(), ring_at, ~0ull);
         u32x4_t q[KSTEPS];
         {
             const elem_t<DT> *from_q = static_cast<const elem_t<DT> *>(a.q) + ((int64_t)(q0 + min(my, few - 1)) * a.heads + head) * DQ + (lane >> 5) * 8;
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             uint64_t bad = 0;  // tokens whose values are not all finite
             if (masked) {  // the same in all waves, and so is what they find
                 for (int i = 0; i < TOKENS / 4; ++i) {
-                    const u32x4_t w = lds_read16(buf + (i * 4 + (here(lane) >> 4)) * KV_BYTES + PREFILL_NOPE * 2 + (here(lane) & 15) * 16);
+                    const u32x4_t w = lds_read16(buf + (i * 4 + (lane_here() >> 4)) * KV_BYTES + PREFILL_NOPE * 2 + (lane_here() & 15) * 16);
                     const uint64_t lanes = __ballot(word_not_finite<DT>(w.x) || word_not_finite<DT>(w.y) || word_not_finite<DT>(w.z) || word_not_finite<DT>(w.w));
                     for (int r = 0; r < 4; ++r) bad |= (uint64_t)((lanes >> (16 * r) & 0xFFFF) != 0) << (i * 4 + r);
                 }
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             }
             // LDS offsets of this lane's reads for the first k step, rope step and block of values; the
             // others' chunks differ in higher bits, which an xor reaches
-            const int l = here(lane), lr = l & 31, lh = l >> 5;
+            const int l = lane_here(), lr = l & 31, lh = l >> 5;
             const uint32_t k_at = lr * KV_BYTES + ((lh ^ swz(lr)) << 4);
             const uint32_t r_at = ROPE_AT + lr * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
             const int vr = lh * 4 + ((l >> 2) & 3);
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             const uint64_t sees = sees_n >= 64 ? ~0ull : sees_n <= 0 ? 0 : (1ull << sees_n) - 1;
             auto largest = [&](int step, acc16_t &s) {
                 if (masked) {
-                    const int at0 = step * 32 + (here(lane) >> 5) * 4;
+                    const int at0 = step * 32 + (lane_here() >> 5) * 4;
                     const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -209,11 +209,13 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
+                if (__any(was != -INFINITY)) {  // (the first maximum: the sums are 0)
 #pragma unroll
-                for (int d = 0; d < DBLOCKS; ++d) {
-                    pin_acc(acc[d]);
-                    acc[d] *= keep;
-                    pin_acc(acc[d]);
+                    for (int d = 0; d < DBLOCKS; ++d) {
+                        pin_acc(acc[d]);
+                        acc[d] *= keep;
+                        pin_acc(acc[d]);
+                    }
                 }
                 return keep;
             };
@@ -224,7 +226,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 p[i >> 2][i & 3] = pack2<DT>(e0, e1);
             };
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
-            const uint32_t load_lane = here(lane);
+            const uint32_t load_lane = lane_here();
             acc16_t s, s1;
             u32x4_t p[2], p1[2];
             products_k(0, s, [&](int i) {
@@ -258,7 +260,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
     // ---- results
 #pragma unroll
     for (int d = 0; d < DBLOCKS; ++d) pin_acc(acc[d]);
-    const int l = here(lane), lh = l >> 5;
+    const int l = lane_here(), lh = l >> 5;
     const float all = sum_halves(sum), inv = all == 0.f ? 0.f : 1.f / all;
     if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
     // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
