@@ -301,14 +301,15 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             const bool masked = ok != ~0ull || j0 + S::TOKENS > (a.tree_mask ? context : context + 1);
             uint64_t bad = 0;  // tokens that hold a value that is not finite
             if (masked) {  // the same in all waves
+                // Only what some rows see and others do not has to be looked at: the call's own tokens,
+                // and the copies in place of tokens that are not there, if it is one of those they copy.
                 constexpr int CHUNKS = S::ROW_BYTES / 16;
+                const int own = context - j0, copied = ok ? __builtin_ctzll(ok) : 0;
+                const int lo = copied >= own ? 0 : own, hi = copied >= own ? S::TOKENS : min(S::TOKENS, sq.len - j0);
                 if (threadIdx.x < 2) not_finite[threadIdx.x] = 0;
                 wait_and_barrier<63>();
-                for (int i = threadIdx.x; i < S::TOKENS * CHUNKS; i += S::THREADS) {
-                    const u32x4_t w = lds_read16(buf + i * 16);
-                    if (word_not_finite<DT>(w.x) || word_not_finite<DT>(w.y) || word_not_finite<DT>(w.z) || word_not_finite<DT>(w.w))
-                        atomicOr(&not_finite[(i / CHUNKS) >> 5], 1u << ((i / CHUNKS) & 31));
-                }
+                for (int i = lo * CHUNKS + threadIdx.x; i < hi * CHUNKS; i += S::THREADS)
+                    if (not_all_finite<DT>(lds_read16(buf + i * 16))) atomicOr(&not_finite[(i / CHUNKS) >> 5], 1u << ((i / CHUNKS) & 31));
                 wait_and_barrier<63>();
                 bad = ((uint64_t)uniform((int)not_finite[1]) << 32) | (uint32_t)uniform((int)not_finite[0]);
                 if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
@@ -560,29 +561,23 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 // Joins the parts of the batches that were cut. Workgroup (c, member) stands at the border
 // between clusters c and c + 1. If the border cuts a batch into P parts, its P - 1 borders share
 // the work out among themselves, so that one long sequence keeps all workgroups busy, too. A
-// piece of the work is 4 elements a lane for 32 rows: one wave's, or several waves' that take the
-// parts in turn if there are more waves than pieces.
-constexpr int JOIN_WAVES = 16;
+// piece of the work is C chunks of 8 elements for 32 rows: one wave's, or several waves' that take
+// the parts in turn if there are more waves than pieces. Where there are pieces enough, 8 or more a
+// workgroup, they are 8 chunks wide, so that a wave writes whole 128-byte lines of the output: lines
+// of which several XCDs write parts made it 39 us instead of 26 for 64 sequences of 128 heads. With
+// fewer pieces the parts are many, and more waves count: one long sequence takes 16 us with two
+// workgroups a border and one chunk a piece, 24 with one workgroup.
+constexpr int JOIN_WAVES = 16, JOIN_GROUPS = 2;  // waves a workgroup; workgroups a border and member
 
-template <int DT, class S>
-__global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) {
-    constexpr int CHUNKS = S::LATENT / 8;
-    __shared__ float shared[JOIN_WAVES][6][64];
-    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6)), member = blockIdx.y;
-    const Header *header = static_cast<const Header *>(a.ws);
-    const int64_t share = uniform(header->share);
-    const Start at = header->start[blockIdx.x + 1];
-    if (at.b < 0 || at.tile == 0) return;  // no work behind the border, or it cuts nothing
-    const Seq sq = sequence<S>(a, at.b);
+template <int DT, class S, int C>
+__device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, int before, int borders, int taker, int takers, int rows, int row_tile, int member,
+                                            float (*shared)[6][64]) {
+    constexpr int ALL = S::LATENT / 8, CHUNKS = ALL / C;  // chunks, pieces a group of 32 rows
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int parts = borders + 1, c0 = (int)blockIdx.x - before;  // first part: of cluster c0
     const int q0 = cu_at(a.c.cu_q, at.b, (int)a.N);
-    const int row_tile = at.batch * a.members + member;
-    if (row_tile >= sq.row_tiles) return;
-    // borders of this batch before this one, and behind it
-    const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
-    const int borders = before + behind + 1, parts = borders + 1, c0 = blockIdx.x - before;  // first part: of cluster c0
-    const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
     const int pieces = (rows + 31) / 32 * CHUNKS;
-    const int mine = before < pieces ? (pieces - before - 1) / borders + 1 : 0;  // pieces before, before + borders, ...
+    const int mine = taker < pieces ? (pieces - taker - 1) / takers + 1 : 0;  // pieces taker, taker + takers, ...
     int waves = 1;  // a piece
     while (waves * 2 * mine <= JOIN_WAVES && waves * 2 <= parts) waves *= 2;
     const int sub = wave % waves, at_once = JOIN_WAVES / waves;
@@ -591,42 +586,97 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) 
     for (int k0 = 0; k0 < mine; k0 += at_once) {
         const int k = k0 + wave / waves;
         const bool real = k < mine;
-        const int piece = before + (real ? k : 0) * borders, group = piece / CHUNKS, chunk = piece % CHUNKS;
+        const int piece = real ? taker + k * takers : 0, group = piece / CHUNKS, chunk = piece % CHUNKS * C;
         const int in = group * 32 + (lane & 31);
         float top = -INFINITY, total = 0.f;
-        acc4_t acc = {0.f, 0.f, 0.f, 0.f};
-        auto join = [&](float t, float w, acc4_t v) {
+        acc4_t acc[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = acc4_t{0.f, 0.f, 0.f, 0.f};
+        // brings what there is and a part to the larger maximum (-infinity: no logit that is a number; sums of 0, or NaN)
+        auto factors = [&](float t, float &keep, float &add) {
             const float to = fmaxf(top, t);
-            // (-infinity: no logit that is a number; the sums are 0 or NaN)
-            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(t - to);
+            keep = to == -INFINITY ? 1.f : exp2_fast(top - to);
+            add = to == -INFINITY ? 1.f : exp2_fast(t - to);
             top = to;
-            total = total * keep + w * add;
-            acc = acc * keep + v * add;
         };
-#pragma unroll 8
-        for (int i = sub; i < parts; i += waves) {
-            const float *p = i == 0 ? first : second + (i - 1) * step;
-            join(p[S::ROWS * S::LATENT + in], p[S::ROWS * (S::LATENT + 1) + in],
-                 *reinterpret_cast<const acc4_t *>(p + ((group * CHUNKS + chunk) * 64 + lane) * 4));
+        constexpr int AT_ONCE = C == 1 ? 4 : 2;  // parts whose loads are in flight together
+        for (int i0 = sub; i0 < parts; i0 += AT_ONCE * waves) {
+            float t[AT_ONCE], w[AT_ONCE];
+            acc4_t v[AT_ONCE][C];
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u) {
+                const int i = min(i0 + u * waves, parts - 1);
+                const float *p = i == 0 ? first : second + (i - 1) * step;
+                t[u] = p[S::ROWS * S::LATENT + in];
+                w[u] = p[S::ROWS * (S::LATENT + 1) + in];
+#pragma unroll
+                for (int c = 0; c < C; ++c) v[u][c] = *reinterpret_cast<const acc4_t *>(p + ((group * ALL + chunk + c) * 64 + lane) * 4);
+            }
+#pragma unroll
+            for (int u = 0; u < AT_ONCE; ++u)
+                if (i0 + u * waves < parts) {
+                    float keep, add;
+                    factors(t[u], keep, add);
+                    total = total * keep + w[u] * add;
+#pragma unroll
+                    for (int c = 0; c < C; ++c) acc[c] = acc[c] * keep + v[u][c] * add;
+                }
         }
         if (waves > 1) {  // (the same for all waves)
-            shared[wave][0][lane] = top;
-            shared[wave][1][lane] = total;
-            for (int e = 0; e < 4; ++e) shared[wave][2 + e][lane] = acc[e];
-            __syncthreads();
-            if (sub == 0)
-                for (int w = wave + 1; w < wave + waves; ++w)
-                    join(shared[w][0][lane], shared[w][1][lane],
-                         acc4_t{shared[w][2][lane], shared[w][3][lane], shared[w][4][lane], shared[w][5][lane]});
-            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                __syncthreads();
+                shared[wave][0][lane] = top;
+                shared[wave][1][lane] = total;
+                for (int e = 0; e < 4; ++e) shared[wave][2 + e][lane] = acc[c][e];
+                __syncthreads();
+                if (sub > 0) continue;
+                // the maximum of all, then the sums (the first wave's statistics are its own until the last chunk)
+                float to = top, sums = 0.f;
+                for (int w = wave + 1; w < wave + waves; ++w) to = fmaxf(to, shared[w][0][lane]);
+                acc4_t v = {0.f, 0.f, 0.f, 0.f};
+                for (int w = wave; w < wave + waves; ++w) {
+                    const float add = to == -INFINITY ? 1.f : exp2_fast(shared[w][0][lane] - to);
+                    sums += shared[w][1][lane] * add;
+                    v += acc4_t{shared[w][2][lane], shared[w][3][lane], shared[w][4][lane], shared[w][5][lane]} * add;
+                }
+                acc[c] = v;
+                if (c == C - 1) {
+                    top = to;
+                    total = sums;
+                }
+            }
         }
         if (sub == 0 && real && in < rows) {
             const int r = row_tile * S::ROWS + in, t = q0 + r / a.heads, h = r % a.heads;
             const float inv = total == 0.f ? 0.f : 1.f / total;
             elem_t<DT> *o = static_cast<elem_t<DT> *>(a.out) + (int64_t)t * a.out_token + h * a.out_head + chunk * 8 + (lane >> 5) * 4;
-            *reinterpret_cast<u32x2_t *>(o) = u32x2_t{pack2<DT>(acc[0] * inv, acc[1] * inv), pack2<DT>(acc[2] * inv, acc[3] * inv)};
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                *reinterpret_cast<u32x2_t *>(o + c * 8) = u32x2_t{pack2<DT>(acc[c][0] * inv, acc[c][1] * inv), pack2<DT>(acc[c][2] * inv, acc[c][3] * inv)};
             if (a.lse && chunk == 0 && lane < 32) a.lse[(int64_t)t * a.heads + h] = total == 0.f ? -INFINITY : (top + __log2f(total)) * LN2;
         }
+    }
+}
+
+template <int DT, class S>
+__global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) {
+    __shared__ float shared[JOIN_WAVES][6][64];
+    const Header *header = static_cast<const Header *>(a.ws);
+    const int64_t share = uniform(header->share);
+    const Start at = header->start[blockIdx.x + 1];
+    if (at.b < 0 || at.tile == 0) return;  // no work behind the border, or it cuts nothing
+    const Seq sq = sequence<S>(a, at.b);
+    const int member = blockIdx.y, row_tile = at.batch * a.members + member;
+    if (row_tile >= sq.row_tiles) return;
+    // borders of this batch before this one, and behind it
+    const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
+    const int borders = before + behind + 1;
+    const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
+    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) {
+        if (blockIdx.z == 0) join_pieces<DT, S, 8>(a, at, before, borders, before, borders, rows, row_tile, member, shared);
+    } else {
+        join_pieces<DT, S, 1>(a, at, before, borders, before * JOIN_GROUPS + (int)blockIdx.z, borders * JOIN_GROUPS, rows, row_tile, member, shared);
     }
 }
 
@@ -650,7 +700,7 @@ template <int LATENT> using Rows128 = Shape<LATENT, 4, 1>;
 template <int DT, class S> hipError_t run(const AttnArgs &a, hipStream_t s) {
     const hipError_t e = launch_kernel(attn_kernel<DT, S>, dim3(WORKGROUPS), dim3(S::THREADS), s, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members), dim3(JOIN_WAVES * 64), s, a);
+    return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members, JOIN_GROUPS), dim3(JOIN_WAVES * 64), s, a);
 }
 
 template <int DT, int LATENT> hipError_t run_rows(const AttnArgs &a, int rows, hipStream_t s) {

@@ -233,10 +233,11 @@ __device__ __forceinline__ float max16(const acc16_t &s) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Whether a word of two 16-bit values holds one that is not finite.
-template <int DT> __device__ __forceinline__ bool word_not_finite(uint32_t w) {
-    constexpr uint32_t E = DT == DT_BF16 ? 0x7F80u : 0x7C00u;
-    return (w & E) == E || (w & (E << 16)) == (E << 16);
+// Whether eight 16-bit values hold one that is not finite: an exponent of all ones carries
+// into the sign's place when one is added to it.
+template <int DT> __device__ __forceinline__ bool not_all_finite(u32x4_t w) {
+    constexpr uint32_t ONE = DT == DT_BF16 ? 0x00800080u : 0x04000400u, REST = 0x7FFF7FFFu;
+    return ((((w.x & REST) + ONE) | ((w.y & REST) + ONE) | ((w.z & REST) + ONE) | ((w.w & REST) + ONE)) & ~REST) != 0;
 }
 
 // Waits until at most `VM` of this wave's vector-memory operations are in flight and its

@@ -124,7 +124,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             if (masked) {  // the same in all waves, and so is what they find
                 for (int i = 0; i < TOKENS / 4; ++i) {
                     const u32x4_t w = lds_read16(buf + (i * 4 + (lane_here() >> 4)) * KV_BYTES + PREFILL_NOPE * 2 + (lane_here() & 15) * 16);
-                    const uint64_t lanes = __ballot(word_not_finite<DT>(w.x) || word_not_finite<DT>(w.y) || word_not_finite<DT>(w.z) || word_not_finite<DT>(w.w));
+                    const uint64_t lanes = __ballot(not_all_finite<DT>(w));
                     for (int r = 0; r < 4; ++r) bad |= (uint64_t)((lanes >> (16 * r) & 0xFFFF) != 0) << (i * 4 + r);
                 }
                 if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
