@@ -233,12 +233,13 @@ __device__ __forceinline__ float max16(const acc16_t &s) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// Whether eight 16-bit values hold one that is not finite: an exponent of all ones carries
-// into the sign's place when one is added to it.
-template <int DT> __device__ __forceinline__ bool not_all_finite(u32x4_t w) {
+// Not 0 if one of eight 16-bit values is not finite: an exponent of all ones carries into the
+// sign's place when one is added to it.
+template <int DT> __device__ __forceinline__ uint32_t not_finite_bits(u32x4_t w) {
     constexpr uint32_t ONE = DT == DT_BF16 ? 0x00800080u : 0x04000400u, REST = 0x7FFF7FFFu;
-    return ((((w.x & REST) + ONE) | ((w.y & REST) + ONE) | ((w.z & REST) + ONE) | ((w.w & REST) + ONE)) & ~REST) != 0;
+    return (((w.x & REST) + ONE) | ((w.y & REST) + ONE) | ((w.z & REST) + ONE) | ((w.w & REST) + ONE)) & ~REST;
 }
+template <int DT> __device__ __forceinline__ bool not_all_finite(u32x4_t w) { return not_finite_bits<DT>(w) != 0; }
 
 // Waits until at most `VM` of this wave's vector-memory operations are in flight and its
 // LDS operations are done, then for the workgroup's other waves.

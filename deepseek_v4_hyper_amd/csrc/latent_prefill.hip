@@ -88,25 +88,30 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
         const char *kv = static_cast<const char *>(a.kv) + ((int64_t)k0 * a.heads + head) * KV_BYTES;
         const char *kr = static_cast<const char *>(a.k_rope) + (int64_t)k0 * a.k_rope_stride * 2;
         const uint32_t kv_step = (uint32_t)a.heads * KV_BYTES;  // bytes between tokens, at most 2^19
+        const uint64_t rope_step = (uint64_t)a.k_rope_stride * 2;
         constexpr int KV_LOADS = TOKENS * KV_BYTES / 1024 / WAVES, LOADS = KV_LOADS + TOKENS * ROPE_BYTES / 1024 / WAVES;
         // The wave's load number i of tile t: two tokens' keys and values, or 8 tokens' rope keys. Behind
         // the sequence's last token that one is loaded again (what lies there is another's, and may be
-        // NaN, which a weight of 0 would not hide).
-        auto load = [&](int i, int t, uint32_t l, uint32_t buf, uint64_t lanes) {
-            const int last = len - 1 - t * TOKENS;
+        // NaN, which a weight of 0 would not hide). Which token is the scalar unit's work: a lane adds
+        // its half's step to its chunk (both swizzles part into the lane's share and load i's).
+        const int l0 = lane_here();
+        const uint32_t upper = -(uint32_t)(l0 >> 5), chunk0 = ((l0 & 31) ^ swz(l0 >> 5)) << 4, rope_chunk0 = ((l0 & 7) ^ swz_rope(l0 >> 3)) << 4;
+        auto load = [&](int i, int t, uint32_t buf, uint64_t lanes) {
             if (i < KV_LOADS) {
-                const int first = (wave * KV_LOADS + i) * 2, r = first + (l >> 5);
-                const uint32_t off = (uint32_t)__builtin_elementwise_min(r, last) * kv_step + (((l & 31) ^ swz(r)) << 4);
-                load_to_lds16(kv + (int64_t)t * TOKENS * kv_step, off, buf + first * KV_BYTES, lanes);
+                const int first = (wave * KV_LOADS + i) * 2, token = __builtin_elementwise_min(t * TOKENS + first, len - 1);
+                const uint32_t step = token < len - 1 ? kv_step : 0;
+                load_to_lds16(kv + (uint64_t)(uint32_t)token * kv_step, (upper & step) | (chunk0 ^ (swz(i * 2) << 4)), buf + first * KV_BYTES, lanes);
             } else {
-                const int first = (wave * (LOADS - KV_LOADS) + i - KV_LOADS) * 8, r = first + (l >> 3);
-                const int64_t token = (int64_t)t * TOKENS + __builtin_elementwise_min(r, last);
-                load_to_lds16(kr + token * a.k_rope_stride * 2 + (((l & 7) ^ swz_rope(r)) << 4), buf + ROPE_AT + first * ROPE_BYTES, lanes);
+                const int nth = i - KV_LOADS, first = (wave * (LOADS - KV_LOADS) + nth) * 8, token = __builtin_elementwise_min(t * TOKENS + first, len - 1);
+                const uint32_t on = __builtin_elementwise_min(lane_here() >> 3, len - 1 - token);
+                const char *from = kr + (uint64_t)(uint32_t)token * rope_step;
+                load_to_lds16(from + on * rope_step + (rope_chunk0 ^ (swz_rope(nth * 8) << 4)), buf + ROPE_AT + first * ROPE_BYTES, lanes);
             }
         };
+        static_assert(KV_LOADS % 8 == 0 && LOADS - KV_LOADS == 2, "a wave's first token has no part in its swizzle");
         const uint32_t ring_at = lds_address(ring);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, 0, lane_here(), ring_at, ~0ull);
+        for (int i = 0; i < LOADS; ++i) load(i, 0, ring_at, ~0ull);
         u32x4_t q[KSTEPS];
         {
             const elem_t<DT> *from_q = static_cast<const elem_t<DT> *>(a.q) + ((int64_t)(q0 + min(my, few - 1)) * a.heads + head) * DQ + (lane >> 5) * 8;
@@ -122,11 +127,15 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             const bool masked = j0 + TOKENS > limit(row0);
             uint64_t bad = 0;  // tokens whose values are not all finite
             if (masked) {  // the same in all waves, and so is what they find
-                for (int i = 0; i < TOKENS / 4; ++i) {
-                    const u32x4_t w = lds_read16(buf + (i * 4 + (lane_here() >> 4)) * KV_BYTES + PREFILL_NOPE * 2 + (lane_here() & 15) * 16);
-                    const uint64_t lanes = __ballot(not_all_finite<DT>(w));
-                    for (int r = 0; r < 4; ++r) bad |= (uint64_t)((lanes >> (16 * r) & 0xFFFF) != 0) << (i * 4 + r);
-                }
+                const DS4HC_LDS char *at_values = buf + (lane_here() >> 4) * KV_BYTES + PREFILL_NOPE * 2 + (lane_here() & 15) * 16;
+                uint32_t found = 0;
+#pragma unroll 4
+                for (int i = 0; i < TOKENS / 4; ++i) found |= not_finite_bits<DT>(lds_read16(at_values + i * 4 * KV_BYTES));
+                if (__any(found != 0))  // rarely: which
+                    for (int i = 0; i < TOKENS / 4; ++i) {
+                        const uint64_t lanes = __ballot(not_finite_bits<DT>(lds_read16(at_values + i * 4 * KV_BYTES)) != 0);
+                        for (int r = 0; r < 4; ++r) bad |= (uint64_t)((lanes >> (16 * r) & 0xFFFF) != 0) << (i * 4 + r);
+                    }
                 if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
                     wait_and_barrier<63>();
                     for (int i = threadIdx.x; i < TOKENS * 16; i += THREADS)
@@ -226,11 +235,10 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 p[i >> 2][i & 3] = pack2<DT>(e0, e1);
             };
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
-            const uint32_t load_lane = lane_here();
             acc16_t s, s1;
             u32x4_t p[2], p1[2];
             products_k(0, s, [&](int i) {
-                if (i < LOADS) load(i, t + 1, load_lane, at_next, lanes);
+                if (i < LOADS) load(i, t + 1, at_next, lanes);
             });
             mfma_results(s);
             float high = largest(0, s);
