@@ -232,19 +232,22 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
                 sum += e0;
                 sum += e1;
-                p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+                uint32_t w = pack2<DT>(e0, e1);
+                asm volatile("" : "+v"(w));  // here, beside the products, and not where it is first used
+                p[i >> 2][i & 3] = w;
             };
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
             acc16_t s, s1;
             u32x4_t p[2], p1[2];
             products_k(0, s, [&](int i) {
-                if (i < LOADS) load(i, t + 1, at_next, lanes);
+                if (i % 2 == 0) load(i / 2, t + 1, at_next, lanes);
             });
             mfma_results(s);
             float high = largest(0, s);
             if (__any(high > top + LAZY)) raise(high);
             products_k(1, s1, [&](int i) {
                 if (i < 8) weight2(s, i, p);
+                if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, t + 1, at_next, lanes);
             });
             mfma_results(s1);
             high = largest(1, s1);
