@@ -134,6 +134,15 @@ template <int DT> __device__ __forceinline__ void mfma32_v(u32x4_t a, u32x4_t b,
     if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
     else asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "v"(b));
 }
+// With B in accumulation registers, which such an instruction reads as well.
+template <int DT> __device__ __forceinline__ void mfma32_first_va(u32x4_t a, u32x4_t b, acc16_t &c) {
+    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "a"(b));
+    else asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(c) : "v"(a), "a"(b));
+}
+template <int DT> __device__ __forceinline__ void mfma32_va(u32x4_t a, u32x4_t b, acc16_t &c) {
+    if constexpr (DT == DT_BF16) asm("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "a"(b));
+    else asm("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+&v"(c) : "v"(a), "a"(b));
+}
 // (12 wait states from this instruction to a vector instruction that reads its result.)
 __device__ __forceinline__ void mfma_results(acc16_t &c) { asm volatile("s_nop 13" : "+v"(c)); }
 
@@ -201,6 +210,8 @@ __device__ __forceinline__ void load_to_lds16(const char *from, uint32_t lds, ui
 // Waits for the loads that the values come from: a wait that the compiler would otherwise
 // place at their first use, inside a loop, where it would wait for the next tile as well.
 __device__ __forceinline__ void loaded(u32x4_t &v) { asm volatile("" : "+v"(v)); }
+// The same, and the values into accumulation registers.
+__device__ __forceinline__ void loaded_acc(u32x4_t &v) { asm volatile("" : "+a"(v)); }
 __device__ __forceinline__ void loaded(int &v) { asm volatile("" : "+v"(v)); }
 
 // Byte address in LDS.

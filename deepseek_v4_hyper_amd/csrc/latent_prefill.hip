@@ -90,41 +90,52 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
         const uint32_t kv_step = (uint32_t)a.heads * KV_BYTES;  // bytes between tokens, at most 2^19
         const uint64_t rope_step = (uint64_t)a.k_rope_stride * 2;
         constexpr int KV_LOADS = TOKENS * KV_BYTES / 1024 / WAVES, LOADS = KV_LOADS + TOKENS * ROPE_BYTES / 1024 / WAVES;
-        // The wave's load number i of tile t: two tokens' keys and values, or 8 tokens' rope keys. Behind
-        // the sequence's last token that one is loaded again (what lies there is another's, and may be
-        // NaN, which a weight of 0 would not hide). Which token is the scalar unit's work: a lane adds
-        // its half's step to its chunk (both swizzles part into the lane's share and load i's).
+        // The wave's load number i of a tile: two tokens' keys and values, or 8 tokens' rope keys. Behind
+        // the sequence's last token, `room` tokens on from the tile's first, that one is loaded again (what
+        // lies there is another's, and may be NaN, which a weight of 0 would not hide). The tokens' part
+        // of an offset and the lane's chunk have no bits in common, and both swizzles part into the
+        // lane's share and load i's, so that three instructions make an offset.
         const int l0 = lane_here();
-        const uint32_t upper = -(uint32_t)(l0 >> 5), chunk0 = ((l0 & 31) ^ swz(l0 >> 5)) << 4, rope_chunk0 = ((l0 & 7) ^ swz_rope(l0 >> 3)) << 4;
-        auto load = [&](int i, int t, uint32_t buf, uint64_t lanes) {
+        const uint32_t row_off = (uint32_t)(wave * KV_LOADS * 2 + (l0 >> 5)) * kv_step, chunk0 = ((l0 & 31) ^ swz(l0 >> 5)) << 4;
+        const int rope_row = wave * (LOADS - KV_LOADS) * 8 + (l0 >> 3);
+        const uint32_t rope_chunk0 = ((l0 & 7) ^ swz_rope(l0 >> 3)) << 4;
+        auto load = [&](int i, const char *kv_tile, const char *kr_tile, int room, uint32_t buf, uint64_t lanes) {
             if (i < KV_LOADS) {
-                const int first = (wave * KV_LOADS + i) * 2, token = __builtin_elementwise_min(t * TOKENS + first, len - 1);
-                const uint32_t step = token < len - 1 ? kv_step : 0;
-                load_to_lds16(kv + (uint64_t)(uint32_t)token * kv_step, (upper & step) | (chunk0 ^ (swz(i * 2) << 4)), buf + first * KV_BYTES, lanes);
+                const uint32_t off = __builtin_elementwise_min(row_off + (uint32_t)i * 2 * kv_step, (uint32_t)room * kv_step);
+                load_to_lds16(kv_tile, (chunk0 ^ (swz(i * 2) << 4)) + off, buf + (wave * KV_LOADS + i) * 2 * KV_BYTES, lanes);
             } else {
-                const int nth = i - KV_LOADS, first = (wave * (LOADS - KV_LOADS) + nth) * 8, token = __builtin_elementwise_min(t * TOKENS + first, len - 1);
-                const uint32_t on = __builtin_elementwise_min(lane_here() >> 3, len - 1 - token);
-                const char *from = kr + (uint64_t)(uint32_t)token * rope_step;
-                load_to_lds16(from + on * rope_step + (rope_chunk0 ^ (swz_rope(nth * 8) << 4)), buf + ROPE_AT + first * ROPE_BYTES, lanes);
+                const int nth = i - KV_LOADS;
+                const uint64_t off = (uint64_t)(uint32_t)__builtin_elementwise_min(rope_row + nth * 8, room) * rope_step;
+                load_to_lds16(kr_tile + off + (rope_chunk0 ^ (swz_rope(nth * 8) << 4)), buf + ROPE_AT + (wave * (LOADS - KV_LOADS) + nth) * 8 * ROPE_BYTES, lanes);
             }
         };
         static_assert(KV_LOADS % 8 == 0 && LOADS - KV_LOADS == 2, "a wave's first token has no part in its swizzle");
         const uint32_t ring_at = lds_address(ring);
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) load(i, 0, ring_at, ~0ull);
+        for (int i = 0; i < LOADS; ++i) load(i, kv, kr, min(len - 1, TOKENS - 1), ring_at, ~0ull);
         u32x4_t q[KSTEPS];
         {
             const elem_t<DT> *from_q = static_cast<const elem_t<DT> *>(a.q) + ((int64_t)(q0 + min(my, few - 1)) * a.heads + head) * DQ + (lane >> 5) * 8;
 #pragma unroll
             for (int k = 0; k < KSTEPS; ++k) q[k] = *reinterpret_cast<const u32x4_t *>(from_q + k * 16);
 #pragma unroll
-            for (int k = 0; k < KSTEPS; ++k) loaded(q[k]);
+            for (int k = 0; k < KSTEPS; ++k) loaded_acc(q[k]);
         }
+
+        // LDS offsets of this lane's reads for the first k step, rope step and block of values; the
+        // others' chunks differ in higher bits, which an xor reaches
+        const int lr = l0 & 31, lh = l0 >> 5;
+        const uint32_t k_at = lr * KV_BYTES + ((lh ^ swz(lr)) << 4);
+        const uint32_t r_at = ROPE_AT + lr * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
+        const int vr = lh * 4 + ((l0 >> 2) & 3);
+        const uint32_t v_at = vr * KV_BYTES + PREFILL_NOPE * 2 + (((((l0 >> 4) & 1) << 1 | ((l0 >> 1) & 1)) ^ swz(vr)) << 4) + (l0 & 1) * 8;
+        const uint32_t v8_at = (v_at ^ 32) + 8 * KV_BYTES;  // 8 rows on, swz differs in bit 1
+        const int first_masked = limit(row0) / TOKENS;      // the first tile that some rows do not see whole
 
         auto tile = [&](int t, uint32_t at, uint32_t at_next) {
             DS4HC_LDS char *buf = (DS4HC_LDS char *)(uintptr_t)at;
             const int j0 = t * TOKENS;
-            const bool masked = j0 + TOKENS > limit(row0);
+            const bool masked = t >= first_masked;
             uint64_t bad = 0;  // tokens whose values are not all finite
             if (masked) {  // the same in all waves, and so is what they find
                 const DS4HC_LDS char *at_values = buf + (lane_here() >> 4) * KV_BYTES + PREFILL_NOPE * 2 + (lane_here() & 15) * 16;
@@ -146,60 +157,50 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                     wait_and_barrier<63>();
                 }
             }
-            // LDS offsets of this lane's reads for the first k step, rope step and block of values; the
-            // others' chunks differ in higher bits, which an xor reaches
-            const int l = lane_here(), lr = l & 31, lh = l >> 5;
-            const uint32_t k_at = lr * KV_BYTES + ((lh ^ swz(lr)) << 4);
-            const uint32_t r_at = ROPE_AT + lr * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
-            const int vr = lh * 4 + ((l >> 2) & 3);
-            const uint32_t v_at = vr * KV_BYTES + PREFILL_NOPE * 2 + (((((l >> 4) & 1) << 1 | ((l >> 1) & 1)) ^ swz(vr)) << 4) + (l & 1) * 8;
-            const uint32_t v8_at = (v_at ^ 32) + 8 * KV_BYTES;  // 8 rows on, swz differs in bit 1
-
-            // S^T = K Q^T of 32 tokens, the operands of the next products on their way; `between`
-            // gives other work to the vector unit while the matrix unit is busy
-            constexpr int AHEAD = 4;
-            auto products_k = [&](int step, acc16_t &s, auto &&between) {
-                auto read = [&](int k) {
+            // Reads of both products' left operands, AHEAD of them under way: S^T = K Q^T, and
+            // O^T += V^T P^T with the tokens in the order of S^T's rows for both operands
+            constexpr int AHEAD = 4, VSTEPS = DBLOCKS * 4;
+            auto read = [&](int n) {
+                if (n < 2 * KSTEPS) {
+                    const int step = n / KSTEPS, k = n % KSTEPS;
                     return k < KNOPE ? lds_read16(buf + (k_at ^ (k << 5)) + step * 32 * KV_BYTES)
                                      : lds_read16(buf + (r_at ^ ((k - KNOPE) << 5)) + step * 32 * ROPE_BYTES);
-                };
-                u32x4_t x[AHEAD];
+                }
+                const int i = n - 2 * KSTEPS;  // block i % DBLOCKS, tokens 16 (i / DBLOCKS) .. + 15
+                const uint32_t chunk = (i % DBLOCKS) << 6, off = (i / DBLOCKS) * 16 * KV_BYTES;
+                const u32x2_t lo = lds_read_tr(buf + (v_at ^ chunk) + off), hi = lds_read_tr(buf + (v8_at ^ chunk) + off);
+                return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+            };
+            u32x4_t x[AHEAD];
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) x[i] = read(i);
+            for (int i = 0; i < AHEAD; ++i) x[i] = read(i);
+            // `between` gives other work to the vector unit while the matrix unit is busy
+            auto products_k = [&](int step, acc16_t &s, auto &&between) {
 #pragma unroll
                 for (int i = 0; i < KSTEPS; ++i) {
-                    const u32x4_t now = x[i % AHEAD];
-                    if (i == 0) mfma32_first_v<DT>(now, q[i], s);
-                    else mfma32_v<DT>(now, q[i], s);
-                    if (i + AHEAD < KSTEPS) x[i % AHEAD] = read(i + AHEAD);
+                    const int n = step * KSTEPS + i;
+                    if (i == 0) mfma32_first_va<DT>(x[n % AHEAD], q[i], s);
+                    else mfma32_va<DT>(x[n % AHEAD], q[i], s);
+                    x[n % AHEAD] = read(n + AHEAD);
                     between(i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
-            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of S^T's rows, for both operands
-            constexpr int VAHEAD = 4;
-            auto products_v = [&](int step, const u32x4_t (&p)[2], auto &&between) {
-                auto read = [&](int i) {  // block i % DBLOCKS, tokens 16 (i / DBLOCKS) .. + 15
-                    const uint32_t chunk = (i % DBLOCKS) << 6, off = (step * 32 + (i / DBLOCKS) * 16) * KV_BYTES;
-                    const u32x2_t lo = lds_read_tr(buf + (v_at ^ chunk) + off), hi = lds_read_tr(buf + (v8_at ^ chunk) + off);
-                    return u32x4_t{lo.x, lo.y, hi.x, hi.y};
-                };
-                u32x4_t v[VAHEAD];
+            auto products_v = [&](const u32x4_t (&p)[2], const u32x4_t (&p1)[2], auto &&between) {
 #pragma unroll
-                for (int i = 0; i < VAHEAD; ++i) v[i] = read(i);
-#pragma unroll
-                for (int i = 0; i < DBLOCKS * 2; ++i) {
-                    acc[i % DBLOCKS] = mfma32<DT>(v[i % VAHEAD], p[i / DBLOCKS], acc[i % DBLOCKS]);
-                    if (i + VAHEAD < DBLOCKS * 2) v[i % VAHEAD] = read(i + VAHEAD);
+                for (int i = 0; i < VSTEPS; ++i) {
+                    const int n = 2 * KSTEPS + i;
+                    acc[i % DBLOCKS] = mfma32<DT>(x[n % AHEAD], i < VSTEPS / 2 ? p[i / DBLOCKS] : p1[i / DBLOCKS - 2], acc[i % DBLOCKS]);
+                    if (i + AHEAD < VSTEPS) x[n % AHEAD] = read(n + AHEAD);
                     between(i);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             };
             // Softmax of a step, in pieces. The mask, and the largest logit (of the lane's row).
-            const int sees_n = lim - j0;
-            const uint64_t sees = sees_n >= 64 ? ~0ull : sees_n <= 0 ? 0 : (1ull << sees_n) - 1;
             auto largest = [&](int step, acc16_t &s) {
                 if (masked) {
+                    const int sees_n = lim - j0;
+                    const uint64_t sees = sees_n >= 64 ? ~0ull : sees_n <= 0 ? 0 : (1ull << sees_n) - 1;
                     const int at0 = step * 32 + (lane_here() >> 5) * 4;
                     const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
 #pragma unroll
@@ -236,18 +237,20 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 asm volatile("" : "+v"(w));  // here, beside the products, and not where it is first used
                 p[i >> 2][i & 3] = w;
             };
+            const int t_next = min(t + 1, n - 1), room = min(len - 1 - t_next * TOKENS, TOKENS - 1);
+            const char *kv_next = kv + (uint64_t)(uint32_t)t_next * ((uint64_t)kv_step * TOKENS), *kr_next = kr + (uint64_t)(uint32_t)t_next * (rope_step * TOKENS);
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
             acc16_t s, s1;
             u32x4_t p[2], p1[2];
             products_k(0, s, [&](int i) {
-                if (i % 2 == 0) load(i / 2, t + 1, at_next, lanes);
+                if (i % 2 == 0) load(i / 2, kv_next, kr_next, room, at_next, lanes);
             });
             mfma_results(s);
             float high = largest(0, s);
             if (__any(high > top + LAZY)) raise(high);
             products_k(1, s1, [&](int i) {
                 if (i < 8) weight2(s, i, p);
-                if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, t + 1, at_next, lanes);
+                if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, kv_next, kr_next, room, at_next, lanes);
             });
             mfma_results(s1);
             high = largest(1, s1);
@@ -256,8 +259,11 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
 #pragma unroll
                 for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
             }
-            products_v(0, p, [&](int i) { weight2(s1, i, p1); });
-            products_v(1, p1, [](int) {});
+            // (the last weights are needed from three quarters on)
+            products_v(p, p1, [&](int i) {
+                if (i < 8 && i % 4 != 3) weight2(s1, i - i / 4, p1);
+                if (i == 8 || i == 9) weight2(s1, i - 2, p1);
+            });
         };
 
         // the next tile's loads run beside this one's products. All waves are done with tile t - 1 when
