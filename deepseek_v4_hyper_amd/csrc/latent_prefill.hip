@@ -3,16 +3,18 @@
 // Per query row (a token, one head) and key of its sequence:
 //   s = scale (qn . kn + qr . kr),  out = softmax(s) V.
 // One pass over the keys with a running maximum and sum; both products on the matrix unit:
-// 640 operations a (row, key) against some 26 bytes of keys and values a key and 128 rows, so
-// that the matrix unit bounds it, and beside it the vector unit's 16 exponentials for each 20
-// products of 32 x 32.
+// 640 operations a (row, key), while a key's 640 bytes serve 128 rows. What bounds it is the
+// issue of instructions: of a tile's some 3850 cycles a wave (128 rows, two waves a SIMD) the
+// products take 1280, the vector unit's exponentials and sums beside them about as much, loads,
+// reads and waits the rest; and the clock, which falls from 2.4 to 1.9 GHz under it. 4096 tokens
+// x 32 heads, causal: 202 us, 850 TFLOP/s; 8192 tokens: 666 us, 1.03 PFLOP/s.
 #include "latent_device.hpp"
 
 namespace ds4hc {
 
 namespace {
 
-constexpr int THREADS = 256, WAVES = 4, ROWS = 128;  // a workgroup: 32 rows a wave, all of one head
+constexpr int THREADS = 256, WAVES = 4;
 constexpr int TOKENS = 64;                           // keys a tile
 constexpr int KV_BYTES = (PREFILL_NOPE + PREFILL_VALUE) * 2, ROPE_BYTES = LATENT_ROPE * 2;
 constexpr int ROPE_AT = TOKENS * KV_BYTES, TILE_BYTES = TOKENS * (KV_BYTES + ROPE_BYTES);
@@ -22,13 +24,19 @@ constexpr unsigned GRID_X = 1u << 20;                // workgroups in x (a dispa
 constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
 constexpr float LAZY = 8.f;  // the running maximum is raised only by more than this (in powers of 2)
 
+// Tile shapes. The waves of a workgroup take 32 rows each, all of one head: 128 rows, or 64 in two
+// sets of waves of which each takes half of a tile's keys, in steps of 32.
+template <int SETS_> struct Rows {
+    static constexpr int SETS = SETS_, WAVES_OF_SET = WAVES / SETS, ROWS = WAVES_OF_SET * 32, STEPS = TOKENS / SETS / 32;
+};
+
 // Swizzle of the 16-byte chunks of a token's row in LDS: 16 values over 16 rows, the upper 2
 // bits 4 values over 4 rows (for the transposing reads, 64 bytes of 4 rows at a time).
 __device__ __forceinline__ int swz(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 __device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
 
 // Row tile `nth` of the batch: its sequence and its first row there; -1 if there is none.
-__device__ __forceinline__ int find_tile(const PrefillArgs &a, int nth, int &row0) {
+template <int ROWS> __device__ __forceinline__ int find_tile(const PrefillArgs &a, int nth, int &row0) {
     const int lane = threadIdx.x & 63, B = a.n_seqs, n = (int)a.N, per = (B + 63) / 64;
     auto tiles = [&](int b) { return (max(cu_at(a.cu_q, b + 1, n) - cu_at(a.cu_q, b, n), 0) + ROWS - 1) / ROWS; };
     int mine = 0;
@@ -54,16 +62,17 @@ __device__ __forceinline__ int find_tile(const PrefillArgs &a, int nth, int &row
     return -1;
 }
 
-template <int DT>
+template <int DT, class S>
 __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int tiles) {
     __shared__ __align__(256) char ring[2 * TILE_BYTES];  // two workgroups a CU fill its LDS
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int row_wave = wave % S::WAVES_OF_SET, set = wave / S::WAVES_OF_SET;
     // heads are neighbours in the grid: with 8 of them or more an XCD keeps to its own heads' keys.
     // The last row tiles see the most keys and go first.
     const unsigned id = blockIdx.y * GRID_X + blockIdx.x;
     const int head = id % a.heads;
     int row0 = 0;
-    const int b = uniform(find_tile(a, tiles - 1 - (int)(id / a.heads), row0));
+    const int b = uniform(find_tile<S::ROWS>(a, tiles - 1 - (int)(id / a.heads), row0));
     if (b < 0) return;
     row0 = uniform(row0);
     const int q0 = uniform(cu_at(a.cu_q, b, (int)a.N)), few = uniform(cu_at(a.cu_q, b + 1, (int)a.N)) - q0;
@@ -71,9 +80,9 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
     // keys that row i sees: the first limit(i)
     const int before = len - few;  // may be negative
     auto limit = [&](int i) { return a.full ? len : max(min(len, i + before + 1), 0); };
-    const int n = (limit(min(row0 + ROWS, few) - 1) + TOKENS - 1) / TOKENS;  // tiles
+    const int n = (limit(min(row0 + S::ROWS, few) - 1) + TOKENS - 1) / TOKENS;  // tiles
     const float scale2 = a.scale * LOG2E;
-    const int my = row0 + wave * 32 + (lane & 31);
+    const int my = row0 + row_wave * 32 + (lane & 31);
 
     float top = -INFINITY, from = 0.f, sum = 0.f;  // running maximum (what is subtracted: 0 if there is none), sum
     acc16_t acc[DBLOCKS];
@@ -125,10 +134,10 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
         // LDS offsets of this lane's reads for the first k step, rope step and block of values; the
         // others' chunks differ in higher bits, which an xor reaches
         const int lr = l0 & 31, lh = l0 >> 5;
-        const uint32_t k_at = lr * KV_BYTES + ((lh ^ swz(lr)) << 4);
-        const uint32_t r_at = ROPE_AT + lr * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
+        const uint32_t k_at = (set * 32 * (S::SETS - 1) + lr) * KV_BYTES + ((lh ^ swz(lr)) << 4);
+        const uint32_t r_at = ROPE_AT + (set * 32 * (S::SETS - 1) + lr) * ROPE_BYTES + ((lh ^ swz_rope(lr)) << 4);
         const int vr = lh * 4 + ((l0 >> 2) & 3);
-        const uint32_t v_at = vr * KV_BYTES + PREFILL_NOPE * 2 + (((((l0 >> 4) & 1) << 1 | ((l0 >> 1) & 1)) ^ swz(vr)) << 4) + (l0 & 1) * 8;
+        const uint32_t v_at = (set * 32 * (S::SETS - 1) + vr) * KV_BYTES + PREFILL_NOPE * 2 + (((((l0 >> 4) & 1) << 1 | ((l0 >> 1) & 1)) ^ swz(vr)) << 4) + (l0 & 1) * 8;
         const uint32_t v8_at = (v_at ^ 32) + 8 * KV_BYTES;  // 8 rows on, swz differs in bit 1
         const int first_masked = limit(row0) / TOKENS;      // the first tile that some rows do not see whole
 
@@ -159,14 +168,14 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             }
             // Reads of both products' left operands, AHEAD of them under way: S^T = K Q^T, and
             // O^T += V^T P^T with the tokens in the order of S^T's rows for both operands
-            constexpr int AHEAD = 4, VSTEPS = DBLOCKS * 4;
+            constexpr int AHEAD = 4, ALL_K = S::STEPS * KSTEPS, VSTEPS = S::STEPS * DBLOCKS * 2;
             auto read = [&](int n) {
-                if (n < 2 * KSTEPS) {
+                if (n < ALL_K) {
                     const int step = n / KSTEPS, k = n % KSTEPS;
                     return k < KNOPE ? lds_read16(buf + (k_at ^ (k << 5)) + step * 32 * KV_BYTES)
                                      : lds_read16(buf + (r_at ^ ((k - KNOPE) << 5)) + step * 32 * ROPE_BYTES);
                 }
-                const int i = n - 2 * KSTEPS;  // block i % DBLOCKS, tokens 16 (i / DBLOCKS) .. + 15
+                const int i = n - ALL_K;  // block i % DBLOCKS, tokens 16 (i / DBLOCKS) .. + 15
                 const uint32_t chunk = (i % DBLOCKS) << 6, off = (i / DBLOCKS) * 16 * KV_BYTES;
                 const u32x2_t lo = lds_read_tr(buf + (v_at ^ chunk) + off), hi = lds_read_tr(buf + (v8_at ^ chunk) + off);
                 return u32x4_t{lo.x, lo.y, hi.x, hi.y};
@@ -189,8 +198,8 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             auto products_v = [&](const u32x4_t (&p)[2], const u32x4_t (&p1)[2], auto &&between) {
 #pragma unroll
                 for (int i = 0; i < VSTEPS; ++i) {
-                    const int n = 2 * KSTEPS + i;
-                    acc[i % DBLOCKS] = mfma32<DT>(x[n % AHEAD], i < VSTEPS / 2 ? p[i / DBLOCKS] : p1[i / DBLOCKS - 2], acc[i % DBLOCKS]);
+                    const int n = ALL_K + i;
+                    acc[i % DBLOCKS] = mfma32<DT>(x[n % AHEAD], i < DBLOCKS * 2 ? p[i / DBLOCKS] : p1[i / DBLOCKS - 2], acc[i % DBLOCKS]);
                     if (i + AHEAD < VSTEPS) x[n % AHEAD] = read(n + AHEAD);
                     between(i);
                     __builtin_amdgcn_sched_barrier(0);
@@ -201,7 +210,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
                 if (masked) {
                     const int sees_n = lim - j0;
                     const uint64_t sees = sees_n >= 64 ? ~0ull : sees_n <= 0 ? 0 : (1ull << sees_n) - 1;
-                    const int at0 = step * 32 + (lane_here() >> 5) * 4;
+                    const int at0 = (step + set * (S::SETS - 1)) * 32 + (lane_here() >> 5) * 4;
                     const uint32_t see = (uint32_t)(sees >> at0), nan = (uint32_t)((sees & bad) >> at0);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
@@ -242,28 +251,42 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
             const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < n ? -1 : 0));
             acc16_t s, s1;
             u32x4_t p[2], p1[2];
-            products_k(0, s, [&](int i) {
-                if (i % 2 == 0) load(i / 2, kv_next, kr_next, room, at_next, lanes);
-            });
-            mfma_results(s);
-            float high = largest(0, s);
-            if (__any(high > top + LAZY)) raise(high);
-            products_k(1, s1, [&](int i) {
-                if (i < 8) weight2(s, i, p);
-                if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, kv_next, kr_next, room, at_next, lanes);
-            });
-            mfma_results(s1);
-            high = largest(1, s1);
-            if (__any(high > top + LAZY)) {
-                const float keep = raise(high);
+            if constexpr (S::STEPS == 2) {
+                products_k(0, s, [&](int i) {
+                    if (i % 2 == 0) load(i / 2, kv_next, kr_next, room, at_next, lanes);
+                });
+                mfma_results(s);
+                float high = largest(0, s);
+                if (__any(high > top + LAZY)) raise(high);
+                products_k(1, s1, [&](int i) {
+                    if (i < 8) weight2(s, i, p);
+                    if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, kv_next, kr_next, room, at_next, lanes);
+                });
+                mfma_results(s1);
+                high = largest(1, s1);
+                if (__any(high > top + LAZY)) {
+                    const float keep = raise(high);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
+                    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
+                }
+                // (the last weights are needed from three quarters on)
+                products_v(p, p1, [&](int i) {
+                    if (i < 8 && i % 4 != 3) weight2(s1, i - i / 4, p1);
+                    if (i == 8 || i == 9) weight2(s1, i - 2, p1);
+                });
+            } else {
+                products_k(0, s, [&](int i) {
+                    if (i < LOADS) load(i, kv_next, kr_next, room, at_next, lanes);
+                });
+                mfma_results(s);
+                const float high = largest(0, s);
+                if (__any(high > top + LAZY)) raise(high);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) weight2(s, i, p);
+                products_v(p, p, [&](int i) {
+                    if (i < 4) weight2(s, 4 + i, p);
+                });
             }
-            // (the last weights are needed from three quarters on)
-            products_v(p, p1, [&](int i) {
-                if (i < 8 && i % 4 != 3) weight2(s1, i - i / 4, p1);
-                if (i == 8 || i == 9) weight2(s1, i - 2, p1);
-            });
         };
 
         // the next tile's loads run beside this one's products. All waves are done with tile t - 1 when
@@ -278,35 +301,84 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a, int 
 #pragma unroll
     for (int d = 0; d < DBLOCKS; ++d) pin_acc(acc[d]);
     const int l = lane_here(), lh = l >> 5;
-    const float all = sum_halves(sum), inv = all == 0.f ? 0.f : 1.f / all;
-    if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
-    // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
+    float all = sum_halves(sum);
     wait_and_barrier<63>();  // the last tile has been read by all
+    if constexpr (S::SETS == 2) {
+        // the second set's sums through LDS, brought to the common maximum
+        constexpr int WAVE_BYTES = DBLOCKS * 16 * 64 * 4;
+        static_assert(S::WAVES_OF_SET * (WAVE_BYTES + 256) <= 2 * TILE_BYTES, "a set's sums and statistics");
+        float *st = reinterpret_cast<float *>(ring + S::WAVES_OF_SET * WAVE_BYTES);  // maximum, sum [row waves][32]
+        if (set == 1) {
+            if (lh == 0) {
+                st[row_wave * 64 + l] = top;
+                st[row_wave * 64 + 32 + l] = all;
+            }
+#pragma unroll
+            for (int d = 0; d < DBLOCKS; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16) =
+                        acc4_t{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+        }
+        wait_and_barrier<63>();
+        if (set == 1) return;
+        const float other = st[row_wave * 64 + (l & 31)], to = fmaxf(top, other);
+        // (no logit that is a number, -infinity: the sums are 0 or NaN)
+        const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), keep1 = to == -INFINITY ? 1.f : exp2_fast(other - to);
+        all = all * keep + st[row_wave * 64 + 32 + (l & 31)] * keep1;
+        top = to;
+#pragma unroll
+        for (int d = 0; d < DBLOCKS; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const acc4_t v = *reinterpret_cast<const acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[d][4 * i + e] = acc[d][4 * i + e] * keep + v[e] * keep1;
+            }
+    }
+    const float inv = all == 0.f ? 0.f : 1.f / all;
+    if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+    // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16). (A wave's own place; with
+    // two sets it lies in what that wave has just read.)
     constexpr int OUT_BYTES = PREFILL_VALUE * 2;
-    char *rows_at = ring + wave * 32 * OUT_BYTES;
+    char *rows_at = ring + row_wave * 32 * OUT_BYTES * S::SETS;
 #pragma unroll
     for (int d = 0; d < DBLOCKS; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             *reinterpret_cast<u32x2_t *>(rows_at + (l & 31) * OUT_BYTES + (((d * 4 + i) ^ (l & 15)) << 4) + lh * 8) = u32x2_t{
                 pack2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv), pack2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
-    char *out = static_cast<char *>(a.out) + ((int64_t)(q0 + row0 + wave * 32) * a.heads + head) * OUT_BYTES;
+    char *out = static_cast<char *>(a.out) + ((int64_t)(q0 + row0 + row_wave * 32) * a.heads + head) * OUT_BYTES;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
         const int r = i + (l >> 4), c = l & 15;
         const u32x4_t v = *reinterpret_cast<const u32x4_t *>(rows_at + r * OUT_BYTES + ((c ^ (r & 15)) << 4));
-        if (row0 + wave * 32 + r < few) *reinterpret_cast<u32x4_t *>(out + (int64_t)r * a.heads * OUT_BYTES + c * 16) = v;
+        if (row0 + row_wave * 32 + r < few) *reinterpret_cast<u32x4_t *>(out + (int64_t)r * a.heads * OUT_BYTES + c * 16) = v;
     }
+}
+
+template <int DT, class S> hipError_t run(const PrefillArgs &a, hipStream_t s) {
+    const int tiles = (int)(a.N / S::ROWS) + (int)(a.n_seqs < a.N ? a.n_seqs : a.N);  // at most
+    const uint64_t groups = (uint64_t)tiles * (uint64_t)a.heads;  // at most 2^31: N * heads is at most 2^30
+    const dim3 grid((unsigned)(groups < GRID_X ? groups : GRID_X), (unsigned)((groups + GRID_X - 1) / GRID_X));
+    return launch_kernel(prefill_kernel<DT, S>, grid, dim3(THREADS), s, a, tiles);
+}
+
+// 64 rows a workgroup where 128 would leave places for workgroups empty (there are 512): twice the
+// workgroups, each done with a tile of keys in 55 % of the time. 128 rows where they fill the card,
+// since they load each key half as often. Measured, 64 against 128 rows: one prompt of 2048 tokens
+// x 8 heads 38 and 54 us, x 24 heads 55 and 61, x 32 heads 72 and 66; 4096 x 12 91 and 106, x 16
+// 120 and 117, x 32 234 and 209; six ragged prompts of up to 1000 tokens x 8 heads 31 and 33, x 16 49 and 45.
+constexpr int64_t FEW_ROWS = 3 * 128 * 128;
+
+template <int DT> hipError_t run_rows(const PrefillArgs &a, hipStream_t s) {
+    return a.N * a.heads <= FEW_ROWS ? run<DT, Rows<2>>(a, s) : run<DT, Rows<1>>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_prefill(const PrefillArgs &a, hipStream_t s) {
-    const int tiles = (int)(a.N / ROWS) + (int)(a.n_seqs < a.N ? a.n_seqs : a.N);  // at most
-    const uint64_t groups = (uint64_t)tiles * (uint64_t)a.heads;  // at most 2^31: N * heads is below 2^30
-    const dim3 grid((unsigned)(groups < GRID_X ? groups : GRID_X), (unsigned)((groups + GRID_X - 1) / GRID_X));
-    return a.dt == DT_BF16 ? launch_kernel(prefill_kernel<DT_BF16>, grid, dim3(THREADS), s, a, tiles)
-                           : launch_kernel(prefill_kernel<DT_F16>, grid, dim3(THREADS), s, a, tiles);
+    return a.dt == DT_BF16 ? run_rows<DT_BF16>(a, s) : run_rows<DT_F16>(a, s);
 }
 
 }  // namespace ds4hc
