@@ -11,6 +11,7 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int MAX_PAIRS = 256;     // of a head: dim <= 512
 constexpr int MAX_SPLITS = 64;     // workgroups a token at most
+constexpr unsigned GRID_X = 1u << 20;  // tokens in x (a dispatch has fewer than 2^32 threads a dimension)
 
 // 16 bytes of consecutive elements of one row, widened.
 template <int DT> struct Vec {
@@ -45,14 +46,15 @@ template <int DT> __device__ __forceinline__ void turn(float &x0, float &x1, flo
     x1 = y1;
 }
 
-// A workgroup some heads of one token: grid (tokens, splits of the heads). The token's
+// A workgroup some heads of one token: grid (tokens, splits of the heads, tokens / 2^20). The token's
 // cosines and sines go to LDS first; then each thread turns 16 bytes at a time (VECTOR:
 // rows on 16-byte boundaries, dim a multiple of what they hold; half layout: of twice that,
 // 16 bytes of either half), or one pair.
 template <int DT, bool HALF, bool VECTOR>
 __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
     __shared__ __align__(16) float cosine[MAX_PAIRS], sine[MAX_PAIRS];
-    const int64_t t = blockIdx.x;
+    const int64_t t = (int64_t)blockIdx.z * GRID_X + blockIdx.x;
+    if (t >= a.N) return;
     const int pairs = a.dim >> 1;
     const int64_t position = a.positions[t];
     for (int i = threadIdx.x; i < pairs; i += THREADS) {
@@ -189,7 +191,7 @@ template <int DT> hipError_t launch_rope_of(const RopeArgs &a, hipStream_t s) {
     const int pieces = a.heads * (a.dim / 2) / (vector ? (a.half ? V : V / 2) : 1);
     const int64_t by_token = a.N >= 1024 ? 4 : 1;
     const int64_t splits = (pieces + THREADS * by_token - 1) / (THREADS * by_token);
-    const dim3 grid((unsigned)a.N, (unsigned)(splits < MAX_SPLITS ? splits : MAX_SPLITS));
+    const dim3 grid((unsigned)(a.N < GRID_X ? a.N : GRID_X), (unsigned)(splits < MAX_SPLITS ? splits : MAX_SPLITS), (unsigned)((a.N + GRID_X - 1) / GRID_X));
     if (a.half) return vector ? launch_kernel(rope_kernel<DT, true, true>, grid, dim3(THREADS), s, a)
                               : launch_kernel(rope_kernel<DT, true, false>, grid, dim3(THREADS), s, a);
     return vector ? launch_kernel(rope_kernel<DT, false, true>, grid, dim3(THREADS), s, a)

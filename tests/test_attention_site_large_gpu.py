@@ -77,3 +77,105 @@ def test_prefill_values_that_are_not_finite(heads):
             assert torch.equal(out[:at], clean[:at]) and torch.equal(lse[:at], clean_lse[:at])
             assert torch.equal(out[:, 0], clean[:, 0])
             assert not torch.isfinite(out[at:, 1, 127].float()).any()
+
+
+def check_tokens(bt, ql, qr, scale, out, lse, tokens, tree=None):
+    """Tokens (b, i) of a batch against the 64-bit form."""
+    flat, heads = bt.cache.view(-1, bt.latent + 64), ql.shape[1]
+    for b, i in tokens:
+        q, k, t = bt.q_len[b], bt.kv_len[b], int(bt.cu[b]) + i
+        seen = torch.arange(k) <= k - q + i
+        if tree is not None:
+            seen[max(k - q, 0):] = torch.tensor([(int(tree[t, d // 64]) >> d % 64) & 1 for d in range(max(q - k, 0), q)], dtype=torch.bool)
+        keys = flat[bt.rows(b, k)]
+        ref = attend64(torch.cat((ql[t], qr[t]), -1), keys, keys[:, :bt.latent], seen.expand(heads, k), scale)
+        assert_attention(out[t].cpu(), lse[t].cpu(), ref, [int(seen.sum())] * heads, ql.dtype, f"sequence {b} token {i}")
+
+
+def run_attn(bt, ql, qr, scale=0.07, tree=None, **kw):
+    tree = None if tree is None else tree.cuda()
+    return B.ds4hc_latent_attn(ql.cuda(), qr.cuda(), bt.cache.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.table.cuda(),
+                               scale=scale, tree_mask=tree, want_lse=True, **kw)
+
+
+@pytest.mark.parametrize("n_seqs,heads,latent,page,most", [
+    (65, 16, 512, 16, 200), (150, 3, 128, 4, 120), (300, 128, 256, 64, 150), (700, 1, 512, 2, 40), (64, 40, 512, 32, 700)])
+def test_attn_of_many_sequences(n_seqs, heads, latent, page, most):
+    """No tokens, or no cached ones, among them."""
+    say(f"[gpu] attn {n_seqs} sequences, {heads} heads, latent {latent}, page {page}")
+    g = torch.Generator().manual_seed(n_seqs)
+    q_len = torch.randint(0, 3, (n_seqs,), generator=g).tolist()
+    kv_len = [max(int(k), q) if k % 7 else 0 for k, q in zip(torch.randint(0, most, (n_seqs,), generator=g), q_len)]
+    bt = Batch(n_seqs, q_len, kv_len, page, latent, BF, extra_tokens=2)
+    ql, qr = bt.queries(heads)
+    out = torch.full((bt.N, heads, latent), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((bt.N, heads), 7.0, device="cuda")
+    run_attn(bt, ql, qr, out=out, lse=lse)
+    assert (out[-2:] == 7).all() and (lse[-2:] == 7).all()
+    check_tokens(bt, ql, qr, 0.07, out, lse, [(b, i) for b in range(n_seqs) for i in range(q_len[b])])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,latent,page,q_len,kv_len,tree", [
+    (128, 512, 64, [3, 1, 4], [2900, 700, 3100], False),  # 8 row tiles in groups of four
+    (128, 512, 16, [2, 1, 2, 1], [1300, 5000, 64, 2], False),  # in pairs
+    (100, 256, 64, [2, 5], [2600, 900], False), (77, 128, 8, [4, 4, 4], [1900, 333, 4], False),
+    (16, 512, 16, [40, 33, 2], [4000, 1500, 600], True), (24, 256, 64, [64, 17], [1000, 2100], True),
+    (128, 512, 64, [1], [20000], False), (8, 128, 1, [1, 2], [1500, 40], False), (40, 256, 2, [1], [3300], False)])
+def test_attn_cut_into_parts(dtype, heads, latent, page, q_len, kv_len, tree):
+    say(f"[gpu] attn {dtype} heads={heads} latent={latent} page={page} q={q_len} kv={kv_len} tree={tree}")
+    bt = Batch(heads + latent, q_len, kv_len, page, latent, dtype)
+    ql, qr = bt.queries(heads)
+    mask = random_tree(bt.g, q_len, 1) if tree else None
+    out, lse = run_attn(bt, ql, qr, tree=mask)
+    check_tokens(bt, ql, qr, 0.07, out, lse, [(b, i) for b in range(len(q_len)) for i in range(q_len[b])], mask)
+    again, lse_again = run_attn(bt, ql, qr, tree=mask)
+    assert torch.equal(out, again) and torch.equal(lse, lse_again)
+
+
+def test_attn_on_two_streams_at_once():
+    """Two calls that run beside each other, each with a workspace of its own."""
+    bts = [Batch(91, [1, 2, 1], [3000, 900, 40], 64, 512), Batch(93, [4], [2500], 16, 512)]
+    calls = []
+    for bt in bts:
+        ql, qr = bt.queries(64)
+        args = [t.cuda() for t in (ql, qr, bt.cache, bt.cu, bt.lens, bt.table)]
+        want = B.ds4hc_latent_attn(*args, scale=0.07, want_lse=True)
+        need = B.ds4hc_latent_attn_workspace_bytes(B._paged(*args[2:]), bt.N, 64)
+        calls.append((args, want, torch.empty_like(want[0]), torch.empty_like(want[1]),
+                      torch.empty(need, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, _, out, lse, ws, stream in calls:
+            B.ds4hc_latent_attn(*args, scale=0.07, out=out, lse=lse, workspace=ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, want, out, lse, _, _ in calls:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("n_seqs", [64, 65, 500])
+def test_append_to_many_sequences(n_seqs):
+    g = torch.Generator().manual_seed(n_seqs)
+    q_len = torch.randint(0, 4, (n_seqs,), generator=g).tolist()
+    kv_len = [q + int(k) for q, k in zip(q_len, torch.randint(0, 30, (n_seqs,), generator=g))]
+    bt = Batch(n_seqs, q_len, kv_len, 4, 128, HF, extra_tokens=3)
+    kv = torch.randn(bt.N, 192, generator=g).to(HF)
+    positions = torch.zeros(bt.N, dtype=torch.int64)  # no rotation: what is stored is what was given
+    before, cache = bt.cache.clone().view(-1, 192), bt.cache.cuda()
+    f = B.ds4hc_rope_frequencies(64)[0]
+    B.ds4hc_latent_append(kv.cuda(), positions.cuda(), f.cuda(), cache, bt.cu.cuda(), bt.lens.cuda(), bt.table.cuda())
+    for b, (q, k) in enumerate(zip(q_len, kv_len)):
+        before[bt.rows(b, k)[k - q:]] = kv[bt.cu[b]:bt.cu[b] + q]
+    assert torch.equal(cache.cpu().view(-1, 192).view(torch.int16), before.view(torch.int16))
+
+
+def test_rope_of_the_most_tokens():
+    """2^24 tokens: more threads than one dimension of a dispatch takes."""
+    n, f = 1 << 24, torch.tensor([0.25], dtype=torch.float64, device="cuda")
+    x = torch.ones(n, 1, 2, device="cuda")
+    positions = torch.arange(n, device="cuda")
+    y = B.ds4hc_rope(x, positions, f)
+    a = positions.double() * 0.25
+    want = torch.stack((a.cos() - a.sin(), a.sin() + a.cos()), -1)
+    # a part of a turn of at most half a turn in float32 (4 e in cos and sin of it), two products and a sum
+    assert ((y[:, 0].double() - want).abs() <= 2 * 16 * 2.0 ** -24 + a.abs()[:, None] * 2.0 ** -50).all()
