@@ -55,7 +55,8 @@ __device__ __forceinline__ int swz_rope(int r) { return (r >> 1) & 7; }
 //
 // Workspace: share, then where each cluster starts (for the second kernel), then a place for
 // each part: sums in the order of the lanes that hold them ([row wave][LATENT / 8][64 lanes] of
-// 4 elements, so that stores and loads are of whole lines), maxima and sums [ROWS].
+// 4 elements, so that stores and loads are of whole lines), maxima, sums of the weights and of the
+// rounded weights [ROWS].
 
 struct Start {
     int b, batch, tile, pad;  // sequence (-1: the cluster has nothing to do), batch, first tile of its range
@@ -89,7 +90,7 @@ __device__ __forceinline__ int64_t wave_prefix(int64_t v, int lane) {
     return v;
 }
 
-template <class S> __host__ __device__ constexpr int64_t part_floats() { return (int64_t)S::ROWS * (S::LATENT + 2); }
+template <class S> __host__ __device__ constexpr int64_t part_floats() { return (int64_t)S::ROWS * (S::LATENT + 3); }
 template <class S> __device__ __forceinline__ float *part_at(const AttnArgs &a, int64_t cluster, int second, int member) {
     return reinterpret_cast<float *>(static_cast<Header *>(a.ws) + 1) + ((2 * cluster + second) * a.members + member) * part_floats<S>();
 }
@@ -227,7 +228,8 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < S::KSTEPS; ++k) loaded(q[k]);
         };
-        float top = -INFINITY, from = 0.f, sum = 0.f;  // running maximum (what is subtracted: 0 if there is none), sum
+        float top = -INFINITY, from = 0.f;  // running maximum (what is subtracted: 0 if there is none)
+        float sum = 0.f, used = 0.f;        // sums of the weights and of the rounded weights
         acc16_t acc[S::DBLOCKS];
 #pragma unroll
         for (int d = 0; d < S::DBLOCKS; ++d) {
@@ -400,6 +402,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
+                used *= keep;
                 if (__any(was != -INFINITY)) {  // (the first maximum: the sums are 0)
 #pragma unroll
                     for (int d = 0; d < S::DBLOCKS; ++d) {
@@ -415,6 +418,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 sum += e0;
                 sum += e1;
                 p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+                used = add2_words<DT>(p[i >> 2][i & 3], used);
             };
             // the next tile's loads, spread over the products (all but a second step's last): issued
             // faster than one in some 34 cycles a CU they hold the waves up
@@ -488,16 +492,17 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         const bool whole = t_first == 0 && n == sq.kv_tiles, mine = my_row < n_rows;  // (a part's rows behind the last: never looked at)
         const int in = my_row - row_tile * S::ROWS;
         float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);
-        float all = sum_halves(sum);
+        float all = sum_halves(sum), all_used = sum_halves(used);
         if constexpr (S::SETS == 2) {
             // the second set's sums through LDS, brought to the common maximum
             constexpr int WAVE_BYTES = S::DBLOCKS * 16 * 64 * 4;
-            static_assert(S::ROW_WAVES * (WAVE_BYTES + 256) <= S::BUFS * S::TILE_BYTES, "a set's sums and statistics");
-            float *st = reinterpret_cast<float *>(ring + S::ROW_WAVES * WAVE_BYTES);  // maximum, sum [row waves][32]
+            static_assert(S::ROW_WAVES * (WAVE_BYTES + 384) <= S::BUFS * S::TILE_BYTES, "a set's sums and statistics");
+            float *st = reinterpret_cast<float *>(ring + S::ROW_WAVES * WAVE_BYTES);  // maximum, sums [row waves][32]
             wait_and_barrier<63>();
             if (set == 1 && lh == 0) {
-                st[row_wave * 64 + l] = top;
-                st[row_wave * 64 + 32 + l] = all;
+                st[row_wave * 96 + l] = top;
+                st[row_wave * 96 + 32 + l] = all;
+                st[row_wave * 96 + 64 + l] = all_used;
             }
             if (set == 1) {
 #pragma unroll
@@ -509,10 +514,11 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             }
             wait_and_barrier<63>();
             if (set == 1) continue;
-            const float other = st[row_wave * 64 + (l & 31)], to = fmaxf(top, other);
+            const float other = st[row_wave * 96 + (l & 31)], to = fmaxf(top, other);
             // (no logit that is a number, -infinity: the sums are 0 or NaN)
             const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), keep1 = to == -INFINITY ? 1.f : exp2_fast(other - to);
-            all = all * keep + st[row_wave * 64 + 32 + (l & 31)] * keep1;
+            all = all * keep + st[row_wave * 96 + 32 + (l & 31)] * keep1;
+            all_used = all_used * keep + st[row_wave * 96 + 64 + (l & 31)] * keep1;
             top = to;
 #pragma unroll
             for (int d = 0; d < S::DBLOCKS; ++d)
@@ -524,7 +530,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 }
         }
         if (whole) {
-            const float inv = all == 0.f ? 0.f : 1.f / all;
+            const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
             if (a.lse && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
             // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
             if constexpr (S::SETS == 1) wait_and_barrier<63>();  // the last tile has been read by all
@@ -547,6 +553,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             if (lh == 0) {
                 part[S::ROWS * S::LATENT + in] = top;
                 part[S::ROWS * (S::LATENT + 1) + in] = all;
+                part[S::ROWS * (S::LATENT + 2) + in] = all_used;
             }
             float *o = part + (row_wave * (S::LATENT / 8) * 64 + l) * 4;
 #pragma unroll
@@ -571,7 +578,7 @@ constexpr int JOIN_WAVES = 16, JOIN_GROUPS = 2;  // waves a workgroup; workgroup
 
 template <int DT, class S, int C>
 __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, int before, int borders, int taker, int takers, int rows, int row_tile, int member,
-                                            float (*shared)[6][64]) {
+                                            float (*shared)[7][64]) {
     constexpr int ALL = S::LATENT / 8, CHUNKS = ALL / C;  // chunks, pieces a group of 32 rows
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int parts = borders + 1, c0 = (int)blockIdx.x - before;  // first part: of cluster c0
@@ -588,7 +595,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
         const bool real = k < mine;
         const int piece = real ? taker + k * takers : 0, group = piece / CHUNKS, chunk = piece % CHUNKS * C;
         const int in = group * 32 + (lane & 31);
-        float top = -INFINITY, total = 0.f;
+        float top = -INFINITY, total = 0.f, used = 0.f;
         acc4_t acc[C];
 #pragma unroll
         for (int c = 0; c < C; ++c) acc[c] = acc4_t{0.f, 0.f, 0.f, 0.f};
@@ -601,7 +608,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
         };
         constexpr int AT_ONCE = C == 1 ? 4 : 2;  // parts whose loads are in flight together
         for (int i0 = sub; i0 < parts; i0 += AT_ONCE * waves) {
-            float t[AT_ONCE], w[AT_ONCE];
+            float t[AT_ONCE], w[AT_ONCE], n[AT_ONCE];
             acc4_t v[AT_ONCE][C];
 #pragma unroll
             for (int u = 0; u < AT_ONCE; ++u) {
@@ -609,6 +616,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
                 const float *p = i == 0 ? first : second + (i - 1) * step;
                 t[u] = p[S::ROWS * S::LATENT + in];
                 w[u] = p[S::ROWS * (S::LATENT + 1) + in];
+                n[u] = p[S::ROWS * (S::LATENT + 2) + in];
 #pragma unroll
                 for (int c = 0; c < C; ++c) v[u][c] = *reinterpret_cast<const acc4_t *>(p + ((group * ALL + chunk + c) * 64 + lane) * 4);
             }
@@ -618,6 +626,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
                     float keep, add;
                     factors(t[u], keep, add);
                     total = total * keep + w[u] * add;
+                    used = used * keep + n[u] * add;
 #pragma unroll
                     for (int c = 0; c < C; ++c) acc[c] = acc[c] * keep + v[u][c] * add;
                 }
@@ -628,28 +637,31 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
                 __syncthreads();
                 shared[wave][0][lane] = top;
                 shared[wave][1][lane] = total;
-                for (int e = 0; e < 4; ++e) shared[wave][2 + e][lane] = acc[c][e];
+                shared[wave][2][lane] = used;
+                for (int e = 0; e < 4; ++e) shared[wave][3 + e][lane] = acc[c][e];
                 __syncthreads();
                 if (sub > 0) continue;
                 // the maximum of all, then the sums (the first wave's statistics are its own until the last chunk)
-                float to = top, sums = 0.f;
+                float to = top, sums = 0.f, sums_used = 0.f;
                 for (int w = wave + 1; w < wave + waves; ++w) to = fmaxf(to, shared[w][0][lane]);
                 acc4_t v = {0.f, 0.f, 0.f, 0.f};
                 for (int w = wave; w < wave + waves; ++w) {
                     const float add = to == -INFINITY ? 1.f : exp2_fast(shared[w][0][lane] - to);
                     sums += shared[w][1][lane] * add;
-                    v += acc4_t{shared[w][2][lane], shared[w][3][lane], shared[w][4][lane], shared[w][5][lane]} * add;
+                    sums_used += shared[w][2][lane] * add;
+                    v += acc4_t{shared[w][3][lane], shared[w][4][lane], shared[w][5][lane], shared[w][6][lane]} * add;
                 }
                 acc[c] = v;
                 if (c == C - 1) {
                     top = to;
                     total = sums;
+                    used = sums_used;
                 }
             }
         }
         if (sub == 0 && real && in < rows) {
             const int r = row_tile * S::ROWS + in, t = q0 + r / a.heads, h = r % a.heads;
-            const float inv = total == 0.f ? 0.f : 1.f / total;
+            const float inv = used == 0.f ? 0.f : 1.f / used;
             elem_t<DT> *o = static_cast<elem_t<DT> *>(a.out) + (int64_t)t * a.out_token + h * a.out_head + chunk * 8 + (lane >> 5) * 4;
 #pragma unroll
             for (int c = 0; c < C; ++c)
@@ -661,7 +673,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
 
 template <int DT, class S>
 __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) {
-    __shared__ float shared[JOIN_WAVES][6][64];
+    __shared__ float shared[JOIN_WAVES][7][64];
     const Header *header = static_cast<const Header *>(a.ws);
     const int64_t share = uniform(header->share);
     const Start at = header->start[blockIdx.x + 1];
@@ -722,7 +734,7 @@ template <int DT> hipError_t run_latent(const AttnArgs &a, int rows, hipStream_t
 }  // namespace
 
 uint64_t attn_workspace_bytes(const Paged &c, int latent, int heads, int64_t N) {
-    return sizeof(Header) + 2ull * WORKGROUPS * plan(c, heads, N).rows * (latent + 2) * sizeof(float);
+    return sizeof(Header) + 2ull * WORKGROUPS * plan(c, heads, N).rows * (latent + 3) * sizeof(float);
 }
 
 hipError_t launch_attn(const AttnArgs &args, hipStream_t s) {

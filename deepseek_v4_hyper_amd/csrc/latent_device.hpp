@@ -71,19 +71,6 @@ __device__ __forceinline__ int64_t cache_row(const Paged &c, int b, int j) {
     return ((int64_t)page << c.page_shift) + (j & ((1 << c.page_shift) - 1));
 }
 
-// The sequence that token t of the call belongs to: the last b with cu[b] <= t,
-// if it ends behind t; -1 if there is none.
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int n_seqs, int n, int t) {
-    int lo = 0, hi = n_seqs;  // cu[lo] <= t < cu[hi], as far as cu rises
-    if (cu_at(cu, 0, n) > t || cu_at(cu, n_seqs, n) <= t) return -1;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu_at(cu, mid, n) <= t) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
 // cos and sin of position * inv_freq. The angle is formed and reduced to a part
 // of a turn in 64 bits (a float32 angle of position 2^20 is off by 2^-5), the
 // rest of it, at most half a turn, has 32 bits' precision.
@@ -106,7 +93,6 @@ typedef float acc16_t __attribute__((ext_vector_type(16)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 #define DS4HC_LDS __attribute__((address_space(3)))
-#define DS4HC_GLOBAL __attribute__((address_space(1)))
 
 // C[32 x 32] += A[32 x 16] B[16 x 32]. Lane l holds row (A) or column (B) l % 32 and its 8
 // elements k = (l / 32) * 8 .. + 7; of C column l % 32 and rows 8 (i / 4) + 4 (l / 32) + i % 4.
@@ -160,6 +146,19 @@ template <int DT> __device__ __forceinline__ uint32_t pack2(float a, float b) {
         typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
         const f2_t f = {a, b};
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, h2_t));
+    }
+}
+
+// Sum plus both 16-bit values of a word, in float32: what rounded weights are divided by, so that
+// a row's weights sum to 1 as they were used (a row that sees one token gives its values without
+// an error, and a rounding that many weights share cancels). The sum before the rounding is lse's.
+template <int DT> __device__ __forceinline__ float add2_words(uint32_t w, float sum) {
+    if constexpr (DT == DT_BF16) {
+        typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2_t, w), b2_t{(__bf16)1.f, (__bf16)1.f}, sum, false);
+    } else {
+        asm("v_fma_mix_f32 %0, %1, 1.0, %0 op_sel_hi:[1,0,0]\n\tv_fma_mix_f32 %0, %1, 1.0, %0 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "+v"(sum) : "v"(w));
+        return sum;
     }
 }
 

@@ -111,7 +111,8 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
     const float scale2 = a.scale * LOG2E;
     const int my = row0 + row_wave * 32 + (lane & 31);
 
-    float top = -INFINITY, from = 0.f, sum = 0.f;  // running maximum (what is subtracted: 0 if there is none), sum
+    float top = -INFINITY, from = 0.f;  // running maximum (what is subtracted: 0 if there is none)
+    float sum = 0.f, used = 0.f;        // sums of the weights and of the rounded weights
     acc16_t acc[DBLOCKS];
 #pragma unroll
     for (int d = 0; d < DBLOCKS; ++d) {
@@ -255,6 +256,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
+                used *= keep;
                 if (__any(was != -INFINITY)) {  // (the first maximum: the sums are 0)
 #pragma unroll
                     for (int d = 0; d < DBLOCKS; ++d) {
@@ -272,6 +274,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 uint32_t w = pack2<DT>(e0, e1);
                 asm volatile("" : "+v"(w));  // here, beside the products, and not where it is first used
                 p[i >> 2][i & 3] = w;
+                used = add2_words<DT>(w, used);
             };
             const int t_next = min(t + 1, n - 1), room = min(len - 1 - t_next * TOKENS, TOKENS - 1);
             const char *kv_next = kv + (uint64_t)(uint32_t)t_next * ((uint64_t)kv_step * TOKENS), *kr_next = kr + (uint64_t)(uint32_t)t_next * (rope_step * TOKENS);
@@ -328,17 +331,18 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
 #pragma unroll
     for (int d = 0; d < DBLOCKS; ++d) pin_acc(acc[d]);
     const int l = lane_here(), lh = l >> 5;
-    float all = sum_halves(sum);
+    float all = sum_halves(sum), all_used = sum_halves(used);
     wait_and_barrier<63>();  // the last tile has been read by all
     if constexpr (S::SETS == 2) {
         // the second set's sums through LDS, brought to the common maximum
         constexpr int WAVE_BYTES = DBLOCKS * 16 * 64 * 4;
-        static_assert(S::WAVES_OF_SET * (WAVE_BYTES + 256) <= 2 * TILE_BYTES, "a set's sums and statistics");
-        float *st = reinterpret_cast<float *>(ring + S::WAVES_OF_SET * WAVE_BYTES);  // maximum, sum [row waves][32]
+        static_assert(S::WAVES_OF_SET * (WAVE_BYTES + 384) <= 2 * TILE_BYTES, "a set's sums and statistics");
+        float *st = reinterpret_cast<float *>(ring + S::WAVES_OF_SET * WAVE_BYTES);  // maximum, sums [row waves][32]
         if (set == 1) {
             if (lh == 0) {
-                st[row_wave * 64 + l] = top;
-                st[row_wave * 64 + 32 + l] = all;
+                st[row_wave * 96 + l] = top;
+                st[row_wave * 96 + 32 + l] = all;
+                st[row_wave * 96 + 64 + l] = all_used;
             }
 #pragma unroll
             for (int d = 0; d < DBLOCKS; ++d)
@@ -349,10 +353,11 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
         }
         wait_and_barrier<63>();
         if (set == 1) return;
-        const float other = st[row_wave * 64 + (l & 31)], to = fmaxf(top, other);
+        const float other = st[row_wave * 96 + (l & 31)], to = fmaxf(top, other);
         // (no logit that is a number, -infinity: the sums are 0 or NaN)
         const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), keep1 = to == -INFINITY ? 1.f : exp2_fast(other - to);
-        all = all * keep + st[row_wave * 64 + 32 + (l & 31)] * keep1;
+        all = all * keep + st[row_wave * 96 + 32 + (l & 31)] * keep1;
+        all_used = all_used * keep + st[row_wave * 96 + 64 + (l & 31)] * keep1;
         top = to;
 #pragma unroll
         for (int d = 0; d < DBLOCKS; ++d)
@@ -363,7 +368,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 for (int e = 0; e < 4; ++e) acc[d][4 * i + e] = acc[d][4 * i + e] * keep + v[e] * keep1;
             }
     }
-    const float inv = all == 0.f ? 0.f : 1.f / all;
+    const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
     if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
     // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16). (A wave's own place; with
     // two sets it lies in what that wave has just read.)

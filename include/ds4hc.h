@@ -421,9 +421,10 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  *            aligned (may be NULL when that is 0); as for ds4hc_pre.
  * Products are of the 16-bit inputs and sums, softmax statistics and the running
  * output float32; the softmax weights are rounded to the 16-bit type for the
- * second product. scale > 0; heads 1..1024; N <= 2^24, N * heads <= 2^30. Outputs may not overlap
- * inputs or each other, as ranges from the first to the last element; rows of
- * out may not overlap one another.
+ * second product, and divided by their sum as rounded (lse is of the sum before
+ * that rounding). scale > 0; heads 1..1024; N <= 2^24, N * heads <= 2^30.
+ * Outputs may not overlap inputs or each other, as ranges from the first to the
+ * last element; rows of out may not overlap one another.
  */
 ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
                                const void *q_latent, ds4hc_strides q_latent_strides,

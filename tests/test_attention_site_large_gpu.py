@@ -179,3 +179,34 @@ def test_rope_of_the_most_tokens():
     want = torch.stack((a.cos() - a.sin(), a.sin() + a.cos()), -1)
     # a part of a turn of at most half a turn in float32 (4 e in cos and sin of it), two products and a sum
     assert ((y[:, 0].double() - want).abs() <= 2 * 16 * 2.0 ** -24 + a.abs()[:, None] * 2.0 ** -50).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads", [3, 600])
+def test_weights_sum_to_one_as_they_were_rounded(dtype, heads):
+    """A row that sees one token gives its values to the last bit: w v / w in float32 is
+    within 2 e of v, which no rounding to 16 bits sees. n equal weights, rounded alike,
+    leave the mean of the values: (n + 64) e of their sizes for the sums, u for the store."""
+    g = torch.Generator().manual_seed(97)
+    n = 90
+    q, kv, kr = (torch.randn(*s, generator=g).to(dtype) for s in ((n, heads, 192), (n, heads, 256), (n, 64)))
+    out = B.ds4hc_latent_prefill(q[:1].cuda(), kv[:1].cuda(), kr[:1].cuda(), i32([0, 1]), i32([0, 1]), scale=0.0837)[0]
+    assert torch.equal(out[0].cpu(), kv[0, :, 128:])
+    kv[:, :, :128], kr[:] = kv[:1, :, :128].clone(), kr[:1].clone()
+    out = B.ds4hc_latent_prefill(q.cuda(), kv.cuda(), kr.cuda(), i32([0, n]), i32([0, n]), scale=0.0837)[0].cpu()
+    for h in (0, 1, heads - 1):
+        v = kv[:, h, 128:].double()
+        many = torch.arange(1, n + 1).double()[:, None]
+        want, size = v.cumsum(0) / many, v.abs().cumsum(0) / many
+        assert ((out[:, h].double() - want).abs() <= 3 * (n + 64) * 2.0 ** -24 * size + torch.finfo(dtype).eps / 2 * want.abs() + 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,latent", [(16, 512), (128, 512), (40, 256), (3, 128)])
+def test_attn_of_one_token(dtype, heads, latent):
+    bt = Batch(101, [1, 1, 1], [1, 1, 1], 16, latent, dtype)
+    ql, qr = bt.queries(heads)
+    out, _ = run_attn(bt, ql, qr)
+    flat = bt.cache.view(-1, latent + 64)
+    for b in range(3):
+        assert torch.equal(out[b].cpu(), flat[bt.rows(b, 1)][:, :latent].expand(heads, latent))
