@@ -3,7 +3,16 @@
 // Per query row (a token and a head) and cached vector (c | r) of a sequence:
 //   s = scale (ql . c + qr . r),  out = softmax(s) C,  with C the latents themselves.
 // All rows of a sequence share its vectors, so a tile of cached tokens is loaded once,
-// serves as keys and (read transposed) as values, and is used for as many rows as fit.
+// serves as keys and (read transposed) as values, and is used for as many rows as fit: with
+// 128 heads 1088 * 2 operations a row against 1152 bytes a token, so that one token of 128
+// heads stands where the card's rates of memory and of matrix products meet. A workgroup a CU
+// takes 128 rows (32 a wave, their sums in its 256 accumulation registers) through tiles of 64
+// tokens, two of them in LDS; one tile takes 4.1 us while all of the card streams (4.6 TB/s).
+// Beside the tiles a workgroup spends 12 us before its first (the batch's arrays, the page, the
+// queries) and 5 behind its last (its part of the sums).
+// Measured (latent 512, bf16, both kernels in a graph): 64 sequences of up to 8192 tokens x 128
+// heads 140 us (105 and 29 us), one of 131000 tokens 80 us (59 and 18), 24 chains of 4 tokens
+// over up to 4096 111 us (91 and 23), 512 tokens over 4096 565 us (970 TFLOP/s).
 #include "latent_device.hpp"
 
 namespace ds4hc {

@@ -7,7 +7,7 @@
 // issue of instructions: of a tile's some 3850 cycles a wave (128 rows, two waves a SIMD) the
 // products take 1280, the vector unit's exponentials and sums beside them about as much, loads,
 // reads and waits the rest; and the clock, which falls from 2.4 to 1.9 GHz under it. 4096 tokens
-// x 32 heads, causal: 202 us, 850 TFLOP/s; 8192 tokens: 666 us, 1.03 PFLOP/s.
+// x 32 heads, causal: 199 us, 860 TFLOP/s; 8192 tokens: 689 us, 1.00 PFLOP/s.
 #include "latent_device.hpp"
 
 namespace ds4hc {

@@ -46,6 +46,8 @@ template <int DT> __device__ __forceinline__ void turn(float &x0, float &x1, flo
     x1 = y1;
 }
 
+// Bound by memory: 4096 tokens x 128 heads x 64, bf16, take 21.8 us (6.2 TB/s of 134 MB), 25.0 us
+// a call in a chain of them; a few tokens 3.1 us, a launch. Simple pairs of 2-byte loads took 70 us.
 // A workgroup some heads of one token: grid (tokens, splits of the heads, tokens / 2^20). The token's
 // cosines and sines go to LDS first; then each thread turns 16 bytes at a time (VECTOR:
 // rows on 16-byte boundaries, dim a multiple of what they hold; half layout: of twice that,
@@ -113,6 +115,9 @@ __device__ __forceinline__ int sequence_by_wave(const int32_t *cu, int n_seqs, i
     return found;
 }
 
+// Bound by memory, and in small calls by the chain of loads (sequence, length, page) before the
+// first store, beside which the row's own loads run: 32 tokens 3.4 us; 4096 float32 rows of 576
+// 5.5 us (16 MB, 2.9 TB/s).
 // A wave a token: LATENT / 64 consecutive elements a lane, and a pair of the rope key for each
 // of the first 32 lanes. The row is read once, kept in registers over the sum of its squares.
 template <int SRC, int DT, int LATENT>
