@@ -579,21 +579,22 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 // the work out among themselves, so that one long sequence keeps all workgroups busy, too. A
 // piece of the work is C chunks of 8 elements for 32 rows: one wave's, or several waves' that take
 // the parts in turn if there are more waves than pieces. Where there are pieces enough, 8 or more a
-// workgroup, they are 8 chunks wide, so that a wave writes whole 128-byte lines of the output: lines
-// of which several XCDs write parts made it 39 us instead of 26 for 64 sequences of 128 heads. With
-// fewer pieces the parts are many, and more waves count: one long sequence takes 16 us with two
-// workgroups a border and one chunk a piece, 24 with one workgroup.
-constexpr int JOIN_WAVES = 16, JOIN_GROUPS = 2;  // waves a workgroup; workgroups a border and member
+// workgroup, they are 8 chunks wide, so that a wave writes whole 128-byte lines of the output (of
+// which several XCDs would write parts). With fewer pieces the parts are many, and more waves count.
+// Whole calls, 8 chunks and 1: 64 sequences of 128 heads 138 and 152 us, 24 chains of 4 tokens 112
+// and 123; one token of 16 heads over 500 31 and 22 us, of 128 heads over 131000 103 and 82. (Two
+// workgroups a border, 8 waves for 16, and 8 parts in flight for 4 changed nothing beyond 2 %.)
+constexpr int JOIN_WAVES = 16;  // waves a workgroup
 
 template <int DT, class S, int C>
-__device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, int before, int borders, int taker, int takers, int rows, int row_tile, int member,
+__device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, int before, int borders, int rows, int row_tile, int member,
                                             float (*shared)[7][64]) {
     constexpr int ALL = S::LATENT / 8, CHUNKS = ALL / C;  // chunks, pieces a group of 32 rows
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int parts = borders + 1, c0 = (int)blockIdx.x - before;  // first part: of cluster c0
     const int q0 = cu_at(a.c.cu_q, at.b, (int)a.N);
     const int pieces = (rows + 31) / 32 * CHUNKS;
-    const int mine = taker < pieces ? (pieces - taker - 1) / takers + 1 : 0;  // pieces taker, taker + takers, ...
+    const int mine = before < pieces ? (pieces - before - 1) / borders + 1 : 0;  // pieces before, before + borders, ...
     int waves = 1;  // a piece
     while (waves * 2 * mine <= JOIN_WAVES && waves * 2 <= parts) waves *= 2;
     const int sub = wave % waves, at_once = JOIN_WAVES / waves;
@@ -602,7 +603,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, 
     for (int k0 = 0; k0 < mine; k0 += at_once) {
         const int k = k0 + wave / waves;
         const bool real = k < mine;
-        const int piece = real ? taker + k * takers : 0, group = piece / CHUNKS, chunk = piece % CHUNKS * C;
+        const int piece = real ? before + k * borders : 0, group = piece / CHUNKS, chunk = piece % CHUNKS * C;
         const int in = group * 32 + (lane & 31);
         float top = -INFINITY, total = 0.f, used = 0.f;
         acc4_t acc[C];
@@ -694,11 +695,8 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) 
     const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
     const int borders = before + behind + 1;
     const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
-    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) {
-        if (blockIdx.z == 0) join_pieces<DT, S, 8>(a, at, before, borders, before, borders, rows, row_tile, member, shared);
-    } else {
-        join_pieces<DT, S, 1>(a, at, before, borders, before * JOIN_GROUPS + (int)blockIdx.z, borders * JOIN_GROUPS, rows, row_tile, member, shared);
-    }
+    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) join_pieces<DT, S, 8>(a, at, before, borders, rows, row_tile, member, shared);
+    else join_pieces<DT, S, 1>(a, at, before, borders, rows, row_tile, member, shared);
 }
 
 // How a call is run. A tile has the rows that a sequence has on average, at most 128; sequences
@@ -721,7 +719,7 @@ template <int LATENT> using Rows128 = Shape<LATENT, 4, 1>;
 template <int DT, class S> hipError_t run(const AttnArgs &a, hipStream_t s) {
     const hipError_t e = launch_kernel(attn_kernel<DT, S>, dim3(WORKGROUPS), dim3(S::THREADS), s, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members, JOIN_GROUPS), dim3(JOIN_WAVES * 64), s, a);
+    return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members), dim3(JOIN_WAVES * 64), s, a);
 }
 
 template <int DT, int LATENT> hipError_t run_rows(const AttnArgs &a, int rows, hipStream_t s) {
