@@ -210,3 +210,27 @@ def test_attn_of_one_token(dtype, heads, latent):
     flat = bt.cache.view(-1, latent + 64)
     for b in range(3):
         assert torch.equal(out[b].cpu(), flat[bt.rows(b, 1)][:, :latent].expand(heads, latent))
+
+
+def test_attn_tree_of_more_tokens_than_the_cache_has():
+    """q_len > kv_len: the call's first tokens have no place; bits d of a mask still count the
+    call's tokens."""
+    bt = Batch(103, [70, 5, 3], [30, 2, 0], 16, 512)
+    ql, qr = bt.queries(16)
+    mask = random_tree(bt.g, bt.q_len, 2)
+    out, lse = run_attn(bt, ql, qr, tree=mask)
+    check_tokens(bt, ql, qr, 0.07, out, lse, [(b, i) for b in range(3) for i in range(bt.q_len[b])], mask)
+
+
+@pytest.mark.parametrize("heads", [16, 128])
+def test_attn_of_sequences_that_share_pages(heads):
+    """Two samples of one prompt: their tables name the same pages, up to the last, which is each
+    one's own; the second sequence names one page twice."""
+    bt = Batch(107, [1, 2, 1], [700, 690, 300], 64, 512)
+    bt.table[1, :10] = bt.table[0, :10]
+    bt.table[2, 3] = bt.table[2, 1]
+    flat = bt.cache.view(-1, 576)
+    assert torch.isfinite(flat[bt.rows(1, 690)].float()).all()
+    ql, qr = bt.queries(heads)
+    out, lse = run_attn(bt, ql, qr)
+    check_tokens(bt, ql, qr, 0.07, out, lse, [(0, 0), (1, 0), (1, 1), (2, 0)])
