@@ -78,14 +78,15 @@ struct Header {
 };
 
 struct Seq {
-    int few, len;        // tokens of the call, cached tokens
+    int q0, few, len;    // first token of the call, tokens of the call, cached tokens
     int row_tiles, kv_tiles;
     __device__ __forceinline__ int batches(int members) const { return (row_tiles + members - 1) / members; }
 };
 
 template <class S> __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b) {
     Seq s;
-    s.few = max(cu_at(a.c.cu_q, b + 1, (int)a.N) - cu_at(a.c.cu_q, b, (int)a.N), 0);
+    s.q0 = cu_at(a.c.cu_q, b, (int)a.N);
+    s.few = max(cu_at(a.c.cu_q, b + 1, (int)a.N) - s.q0, 0);
     s.len = kv_len_at(a.c, b);
     s.row_tiles = (int)(((int64_t)s.few * a.heads + S::ROWS - 1) / S::ROWS);
     s.kv_tiles = max((s.len + S::TOKENS - 1) / S::TOKENS, 1);  // no token: one empty tile, to write the zeros
@@ -141,7 +142,7 @@ __device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, 
         b_out = who;
         off = rest;
         auto of = [&](int v) { return __builtin_amdgcn_readlane(v, who); };
-        at_b = {of(s.few), of(s.len), of(s.row_tiles), of(s.kv_tiles)};
+        at_b = {of(s.q0), of(s.few), of(s.len), of(s.row_tiles), of(s.kv_tiles)};
         return total;
     }
     for (int b = who * per; b < min(B, (who + 1) * per); ++b) {
@@ -206,14 +207,14 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 
     bool first_part = true;
     while (left > 0) {
-        sq = {uniform(sq.few), uniform(sq.len), uniform(sq.row_tiles), uniform(sq.kv_tiles)};
+        sq = {uniform(sq.q0), uniform(sq.few), uniform(sq.len), uniform(sq.row_tiles), uniform(sq.kv_tiles)};
         const int each = sq.kv_tiles + extra;  // units of a batch
         if (off >= (int64_t)sq.batches(a.members) * each) {  // next sequence (the units in all bound b)
             sq = sequence<S>(a, ++b);
             off = 0;
             continue;
         }
-        const int q0 = uniform(cu_at(a.c.cu_q, b, (int)a.N));
+        const int q0 = sq.q0;
         const int batch = (int)(off / each), u0 = (int)(off - (int64_t)batch * each), u1 = u0 + (int)min((int64_t)(each - u0), left);
         const int t_first = max(u0 - extra, 0), n = max(u1 - extra, 0) - t_first;
         const int row_tile = batch * a.members + member;
@@ -589,12 +590,11 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 constexpr int JOIN_WAVES = 16;  // waves a workgroup
 
 template <int DT, class S, int C>
-__device__ __forceinline__ void join_pieces(const AttnArgs &a, const Start &at, int before, int borders, int rows, int row_tile, int member,
+__device__ __forceinline__ void join_pieces(const AttnArgs &a, int q0, int before, int borders, int rows, int row_tile, int member,
                                             float (*shared)[7][64]) {
     constexpr int ALL = S::LATENT / 8, CHUNKS = ALL / C;  // chunks, pieces a group of 32 rows
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int parts = borders + 1, c0 = (int)blockIdx.x - before;  // first part: of cluster c0
-    const int q0 = cu_at(a.c.cu_q, at.b, (int)a.N);
     const int pieces = (rows + 31) / 32 * CHUNKS;
     const int mine = before < pieces ? (pieces - before - 1) / borders + 1 : 0;  // pieces before, before + borders, ...
     int waves = 1;  // a piece
@@ -697,8 +697,8 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) 
     const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
     const int borders = before + behind + 1;
     const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
-    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) join_pieces<DT, S, 8>(a, at, before, borders, rows, row_tile, member, shared);
-    else join_pieces<DT, S, 1>(a, at, before, borders, rows, row_tile, member, shared);
+    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) join_pieces<DT, S, 8>(a, sq.q0, before, borders, rows, row_tile, member, shared);
+    else join_pieces<DT, S, 1>(a, sq.q0, before, borders, rows, row_tile, member, shared);
 }
 
 // How a call is run. A tile has the rows that a sequence has on average, at most 128; sequences
