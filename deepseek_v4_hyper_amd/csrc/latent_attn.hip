@@ -13,6 +13,8 @@
 // Measured (latent 512, bf16, both kernels in a graph): 64 sequences of up to 8192 tokens x 128
 // heads 140 us (105 and 29 us), one of 131000 tokens 80 us (59 and 18), 24 chains of 4 tokens
 // over up to 4096 111 us (91 and 23), 512 tokens over 4096 565 us (970 TFLOP/s).
+#include <type_traits>
+
 #include "latent_device.hpp"
 
 namespace ds4hc {
@@ -505,74 +507,89 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         const int in = my_row - row_tile * S::ROWS;
         float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);
         float all = sum_halves(sum), all_used = sum_halves(used);
-        if constexpr (S::SETS == 2) {
-            // the second set's sums through LDS, brought to the common maximum
-            constexpr int WAVE_BYTES = S::DBLOCKS * 16 * 64 * 4;
-            static_assert(S::ROW_WAVES * (WAVE_BYTES + 384) <= S::BUFS * S::TILE_BYTES, "a set's sums and statistics");
-            float *st = reinterpret_cast<float *>(ring + S::ROW_WAVES * WAVE_BYTES);  // maximum, sums [row waves][32]
-            wait_and_barrier<63>();
-            if (set == 1 && lh == 0) {
-                st[row_wave * 96 + l] = top;
-                st[row_wave * 96 + 32 + l] = all;
-                st[row_wave * 96 + 64 + l] = all_used;
-            }
-            if (set == 1) {
+        // the blocks of the output that this wave finishes: all, or with two sets its half
+        constexpr int BLOCKS = S::DBLOCKS / S::SETS, BLOCK_BYTES = 16 * 64 * 4;
+        acc16_t fin[BLOCKS];
+        if constexpr (S::SETS == 1) {
 #pragma unroll
-                for (int d = 0; d < S::DBLOCKS; ++d)
+            for (int d = 0; d < BLOCKS; ++d) fin[d] = acc[d];
+            wait_and_barrier<63>();  // the last tile has been read by all
+        } else {
+            // each set gives the other one's half through LDS, and all is brought to the common maximum
+            static_assert(S::WAVES * (BLOCKS * BLOCK_BYTES + 384) <= S::BUFS * S::TILE_BYTES, "the halves and statistics");
+            float *st = reinterpret_cast<float *>(ring + S::WAVES * BLOCKS * BLOCK_BYTES);  // maximum, sums [row waves][sets][32]
+            char *give = ring + (row_wave * 2 + set) * BLOCKS * BLOCK_BYTES + l * 16, *take = ring + (row_wave * 2 + 1 - set) * BLOCKS * BLOCK_BYTES + l * 16;
+            float *mine_st = st + (row_wave * 2 + set) * 96, *other_st = st + (row_wave * 2 + 1 - set) * 96;
+            auto give_half = [&](auto from) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *reinterpret_cast<acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16) =
-                            acc4_t{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
-            }
+                for (int d = 0; d < BLOCKS; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const acc16_t &v = acc[from.value + d];
+                        *reinterpret_cast<acc4_t *>(give + (d * 4 + i) * 1024) = acc4_t{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+                    }
+            };
             wait_and_barrier<63>();
-            if (set == 1) continue;
-            const float other = st[row_wave * 96 + (l & 31)], to = fmaxf(top, other);
+            if (lh == 0) {
+                mine_st[l] = top;
+                mine_st[32 + l] = all;
+                mine_st[64 + l] = all_used;
+            }
+            if (set == 0) give_half(std::integral_constant<int, BLOCKS>{});
+            else give_half(std::integral_constant<int, 0>{});
+            wait_and_barrier<63>();
+            const float other = other_st[l & 31], to = fmaxf(top, other);
             // (no logit that is a number, -infinity: the sums are 0 or NaN)
-            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), keep1 = to == -INFINITY ? 1.f : exp2_fast(other - to);
-            all = all * keep + st[row_wave * 96 + 32 + (l & 31)] * keep1;
-            all_used = all_used * keep + st[row_wave * 96 + 64 + (l & 31)] * keep1;
+            const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(other - to);
+            all = all * keep + other_st[32 + (l & 31)] * add;
+            all_used = all_used * keep + other_st[64 + (l & 31)] * add;
             top = to;
+            auto take_half = [&](auto from) {
 #pragma unroll
-            for (int d = 0; d < S::DBLOCKS; ++d)
+                for (int d = 0; d < BLOCKS; ++d)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const acc4_t v = *reinterpret_cast<const acc4_t *>(ring + row_wave * WAVE_BYTES + ((d * 4 + i) * 64 + l) * 16);
+                    for (int i = 0; i < 4; ++i) {
+                        const acc4_t v = *reinterpret_cast<const acc4_t *>(take + (d * 4 + i) * 1024);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[d][4 * i + e] = acc[d][4 * i + e] * keep + v[e] * keep1;
-                }
+                        for (int e = 0; e < 4; ++e) fin[d][4 * i + e] = acc[from.value + d][4 * i + e] * keep + v[e] * add;
+                    }
+            };
+            if (set == 0) take_half(std::integral_constant<int, 0>{});
+            else take_half(std::integral_constant<int, BLOCKS>{});
         }
+        const int block0 = (S::SETS - 1) * set * BLOCKS;
         if (whole) {
             const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
-            if (a.lse && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
-            // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16)
-            if constexpr (S::SETS == 1) wait_and_barrier<63>();  // the last tile has been read by all
-            char *rows_at = ring + row_wave * 32 * S::ROW_BYTES * S::SETS;  // (the wave's own place; with two sets the one it has just read)
+            if (a.lse && set == 0 && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+            // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16), in the wave's own place
+            // (with two sets in what it has just read)
+            constexpr int OUT_BYTES = BLOCKS * 64, PER = OUT_BYTES / 16, SPREAD = PER < 16 ? PER - 1 : 15;
+            char *rows_at = ring + (S::SETS == 1 ? wave * 32 * OUT_BYTES : (row_wave * 2 + 1 - set) * BLOCKS * BLOCK_BYTES);
 #pragma unroll
-            for (int d = 0; d < S::DBLOCKS; ++d)
+            for (int d = 0; d < BLOCKS; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<u32x2_t *>(rows_at + (l & 31) * S::ROW_BYTES + (((d * 4 + i) ^ (l & 15)) << 4) + lh * 8) = u32x2_t{
-                        pack2<DT>(acc[d][4 * i] * inv, acc[d][4 * i + 1] * inv), pack2<DT>(acc[d][4 * i + 2] * inv, acc[d][4 * i + 3] * inv)};
-            const int64_t o = (int64_t)(q0 + tok) * a.out_token + head * a.out_head;
-            constexpr int PER = S::LATENT / 8;  // lanes a row
+                    *reinterpret_cast<u32x2_t *>(rows_at + (l & 31) * OUT_BYTES + (((d * 4 + i) ^ (l & SPREAD)) << 4) + lh * 8) = u32x2_t{
+                        pack2<DT>(fin[d][4 * i] * inv, fin[d][4 * i + 1] * inv), pack2<DT>(fin[d][4 * i + 2] * inv, fin[d][4 * i + 3] * inv)};
+            const int64_t o = (int64_t)(q0 + tok) * a.out_token + head * a.out_head + block0 * 32;
             for (int i = 0; i < 32; i += 64 / PER) {
                 const int r = i + l / PER, c = l % PER;
                 const int64_t to = (int64_t)(uint32_t)from_lane((int)(uint32_t)o, r) | (int64_t)from_lane((int)(o >> 32), r) << 32;
-                const u32x4_t v = *reinterpret_cast<const u32x4_t *>(rows_at + r * S::ROW_BYTES + ((c ^ (r & 15)) << 4));
+                const u32x4_t v = *reinterpret_cast<const u32x4_t *>(rows_at + r * OUT_BYTES + ((c ^ (r & SPREAD)) << 4));
                 if (row0 + r < n_rows) *reinterpret_cast<u32x4_t *>(static_cast<elem_t<DT> *>(a.out) + to + c * 8) = v;
             }
         } else {
-            if (lh == 0) {
+            if (lh == 0 && set == 0) {
                 part[S::ROWS * S::LATENT + in] = top;
                 part[S::ROWS * (S::LATENT + 1) + in] = all;
                 part[S::ROWS * (S::LATENT + 2) + in] = all_used;
             }
-            float *o = part + (row_wave * (S::LATENT / 8) * 64 + l) * 4;
+            float *o = part + ((row_wave * S::DBLOCKS + block0) * 256 + l) * 4;
 #pragma unroll
-            for (int d = 0; d < S::DBLOCKS; ++d)
+            for (int d = 0; d < BLOCKS; ++d)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<acc4_t *>(o + (d * 4 + i) * 256) = acc4_t{acc[d][4 * i], acc[d][4 * i + 1], acc[d][4 * i + 2], acc[d][4 * i + 3]};
+                    *reinterpret_cast<acc4_t *>(o + (d * 4 + i) * 256) = acc4_t{fin[d][4 * i], fin[d][4 * i + 1], fin[d][4 * i + 2], fin[d][4 * i + 3]};
         }
     }
 }
