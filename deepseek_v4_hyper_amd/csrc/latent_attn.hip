@@ -598,12 +598,14 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 // between clusters c and c + 1. If the border cuts a batch into P parts, its P - 1 borders share
 // the work out among themselves, so that one long sequence keeps all workgroups busy, too. A
 // piece of the work is C chunks of 8 elements for 32 rows: one wave's, or several waves' that take
-// the parts in turn if there are more waves than pieces. Where there are pieces enough, 8 or more a
-// workgroup, they are 8 chunks wide, so that a wave writes whole 128-byte lines of the output (of
-// which several XCDs would write parts). With fewer pieces the parts are many, and more waves count.
-// Whole calls, 8 chunks and 1: 64 sequences of 128 heads 138 and 152 us, 24 chains of 4 tokens 112
-// and 123; one token of 16 heads over 500 31 and 22 us, of 128 heads over 131000 103 and 82. (Two
-// workgroups a border, 8 waves for 16, and 8 parts in flight for 4 changed nothing beyond 2 %.)
+// the parts in turn if there are more waves than pieces. Of tiles of 64 rows and more, where there
+// are 8 pieces or more a workgroup, they are 8 chunks wide, so that a wave writes whole 128-byte lines
+// of the output (of which several XCDs would write parts). With fewer pieces the parts are many, and
+// more waves count; of fewer rows the output is small. Whole calls, 8 chunks and 1: 64 sequences of
+// 128 heads 138 and 152 us, 24 chains of 4 tokens 112 and 123, 8 sequences of up to 500 42 and 52;
+// one token of 128 heads over 131000 103 and 82; 64 sequences of 16 heads 86 and 84, one over 100
+// tokens 23.7 and 22.2. (Two workgroups a border, 8 waves for 16, and 8 parts in flight for 4 changed
+// nothing beyond 2 %.)
 constexpr int JOIN_WAVES = 16;  // waves a workgroup
 
 template <int DT, class S, int C>
@@ -714,8 +716,12 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) 
     const int before = uniform((int)((at.tile - 1) / share)), behind = uniform((int)((sq.kv_tiles - at.tile - 1) / share));
     const int borders = before + behind + 1;
     const int rows = uniform(min(S::ROWS, sq.few * a.heads - row_tile * S::ROWS));
-    if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) join_pieces<DT, S, 8>(a, sq.q0, before, borders, rows, row_tile, member, shared);
-    else join_pieces<DT, S, 1>(a, sq.q0, before, borders, rows, row_tile, member, shared);
+    if constexpr (S::ROWS >= 64)
+        if ((rows + 31) / 32 * (S::LATENT / 64) >= 8 * borders) {
+            join_pieces<DT, S, 8>(a, sq.q0, before, borders, rows, row_tile, member, shared);
+            return;
+        }
+    join_pieces<DT, S, 1>(a, sq.q0, before, borders, rows, row_tile, member, shared);
 }
 
 // How a call is run. A tile has the rows that a sequence has on average, at most 128; sequences
