@@ -11,8 +11,8 @@
 // Beside the tiles a workgroup spends 12 us before its first (the batch's arrays, the page, the
 // queries) and 5 behind its last (its part of the sums).
 // Measured (latent 512, bf16, both kernels in a graph): 64 sequences of up to 8192 tokens x 128
-// heads 140 us (105 and 29 us), one of 131000 tokens 80 us (59 and 18), 24 chains of 4 tokens
-// over up to 4096 111 us (91 and 23), 512 tokens over 4096 565 us (970 TFLOP/s).
+// heads 140 us (106 and 27 us), one of 131000 tokens 82 us (59 and 20), 24 chains of 4 tokens
+// over up to 4096 113 us (90 and 24), 512 tokens over 4096 560 us (980 TFLOP/s).
 #include <type_traits>
 
 #include "latent_device.hpp"
