@@ -318,9 +318,11 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             uint64_t bad = 0;  // tokens that hold a value that is not finite
             if (masked) {  // the same in all waves
                 // Only what some rows see and others do not has to be looked at: the call's own tokens,
-                // and the copies in place of tokens that are not there, if it is one of those they copy.
+                // and the copies in place of tokens that are not there, if it is one of those they copy. (A
+                // copy of a context token is seen, as that token, by all.) If none of the tile's tokens is
+                // there, they copy the cache's first row, which may be nobody's and is seen by none.
                 constexpr int CHUNKS = S::ROW_BYTES / 16;
-                const int own = context - j0, copied = ok ? __builtin_ctzll(ok) : 0;
+                const int own = ok ? context - j0 : 0, copied = ok ? __builtin_ctzll(ok) : 0;
                 const int lo = copied >= own ? 0 : own, hi = copied >= own ? S::TOKENS : min(S::TOKENS, sq.len - j0);
                 if (threadIdx.x < 2) not_finite[threadIdx.x] = 0;
                 wait_and_barrier<63>();
