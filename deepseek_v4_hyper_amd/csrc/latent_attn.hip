@@ -26,8 +26,6 @@ constexpr int XCDS = 8;          // workgroup i runs on XCD i % 8
 // tiles that a batch's queries and results cost as much as (0, 4, 8: 64 sequences of up to 8192 x 128
 // heads 158, 143, 136 us; 24 chains over up to 4096 166, 110, 119; trees 89, 76, 78)
 constexpr int EXTRA = 4;
-constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
-constexpr float LAZY = 8.f;      // the running maximum is raised only by more than this (in powers of 2)
 
 // Tile shapes. ROWS query rows by TOKENS cached tokens; ROW_WAVES waves side by side in the
 // rows, 32 each, times SETS sets of waves that take TOKENS / SETS of the tokens each, in
@@ -242,7 +240,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
 #pragma unroll
             for (int k = 0; k < S::KSTEPS; ++k) loaded(q[k]);
         };
-        float top = -INFINITY, from = 0.f;  // running maximum (what is subtracted: 0 if there is none)
+        float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
         float sum = 0.f, used = 0.f;        // sums of the weights and of the rounded weights
         acc16_t acc[S::DBLOCKS];
 #pragma unroll
@@ -408,13 +406,16 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                         s[i] = (nan >> r) & 1 ? NAN : (see >> r) & 1 ? s[i] : -INFINITY;
                     }
                 }
-                return max_halves(max16(s)) * scale2;
+                return max_halves(max16(s));
             };
-            // A new running maximum. It is a whole number, so that what is there is scaled by a power
-            // of 2, without rounding, weights that are already 16-bit values included.
+            // A new running maximum. It is a whole number, so that what is there is scaled by a power of 2:
+            // without rounding, but for weights that become float16's subnormal numbers (LIFT: half a step
+            // of those is 2^-31 of the largest weight). Whether one is needed is looked at in one rounding,
+            // so that no weight passes 2^(LAZY + LIFT) however far from 0 the logits lie.
+            auto too_high = [&](float high) { return fmaf(high, scale2, -top) > LAZY + LIFT<DT>; };
             auto raise = [&](float high) {
                 const float was = top;
-                top = fmaxf(top, ceilf(high));
+                top = fmaxf(top, ceilf(high * scale2) - LIFT<DT>);
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
             if constexpr (S::STEPS == 1) {
                 mfma_results(s);
                 const float high = largest(0, s);
-                if (__any(high > top + LAZY)) raise(high);
+                if (__any(too_high(high))) raise(high);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) weight2(s, i, p);
                 products_v(0, p, [&](int i) { load_some(S::KSTEPS + i); });
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 u32x4_t p1[2];
                 mfma_results(s);
                 float high = largest(0, s);
-                if (__any(high > top + LAZY)) raise(high);
+                if (__any(too_high(high))) raise(high);
                 products_k(1, s1, [&](int i) {
                     constexpr int EVERY = S::KSTEPS / 8;
                     load_some(S::KSTEPS + i);
@@ -469,7 +470,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 });
                 mfma_results(s1);
                 high = largest(1, s1);
-                if (__any(high > top + LAZY)) {
+                if (__any(too_high(high))) {
                     const float keep = raise(high);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
@@ -562,7 +563,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
         const int block0 = (S::SETS - 1) * set * BLOCKS;
         if (whole) {
             const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
-            if (a.lse && set == 0 && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+            if (a.lse && set == 0 && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = row_lse<DT>(top, all);
             // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16), in the wave's own place
             // (with two sets in what it has just read)
             constexpr int OUT_BYTES = BLOCKS * 64, PER = OUT_BYTES / 16, SPREAD = PER < 16 ? PER - 1 : 15;
@@ -699,7 +700,7 @@ __device__ __forceinline__ void join_pieces(const AttnArgs &a, int q0, int befor
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 *reinterpret_cast<u32x2_t *>(o + c * 8) = u32x2_t{pack2<DT>(acc[c][0] * inv, acc[c][1] * inv), pack2<DT>(acc[c][2] * inv, acc[c][3] * inv)};
-            if (a.lse && chunk == 0 && lane < 32) a.lse[(int64_t)t * a.heads + h] = total == 0.f ? -INFINITY : (top + __log2f(total)) * LN2;
+            if (a.lse && chunk == 0 && lane < 32) a.lse[(int64_t)t * a.heads + h] = row_lse<DT>(top, total);
         }
     }
 }

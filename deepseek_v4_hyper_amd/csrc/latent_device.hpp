@@ -243,6 +243,24 @@ __device__ __forceinline__ float max16(const acc16_t &s) {
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// ------------------------------------------------------------------ softmax
+
+constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
+constexpr float LAZY = 8.f;  // the running maximum is raised only by more than this (in powers of 2)
+// The largest weight is brought to (2^(LIFT - 1), 2^LIFT]. float16 has 5 bits of exponent: with
+// the largest near 1, weights below 2^-14 would lose bits and those below 2^-25 vanish, which
+// many of them together do not deserve (131072 tokens 17.5 below one that holds 99.5 % of the
+// weight kept 0.39 % of 0.54). With 2^7, and 2^15 as the most that LAZY leaves, that begins 2^7 further
+// down, at no instruction in the loop. bfloat16 has float32's exponents.
+template <int DT> constexpr float LIFT = DT == DT_F16 ? 7.f : 0.f;
+
+// ln of the sum of exponentials, from the exponent subtracted and the sum of the weights (before
+// their rounding). LIFT is taken out first: the logarithm's error is relative to it.
+template <int DT> __device__ __forceinline__ float row_lse(float top, float sum) {
+    constexpr float UNIT = DT == DT_F16 ? 1.f / 128.f : 1.f;
+    return sum == 0.f ? -INFINITY : ((top + LIFT<DT>) + __log2f(sum * UNIT)) * LN2;
+}
+
 // Not 0 if one of eight 16-bit values is not finite: an exponent of all ones carries into the
 // sign's place when one is added to it.
 template <int DT> __device__ __forceinline__ uint32_t not_finite_bits(u32x4_t w) {

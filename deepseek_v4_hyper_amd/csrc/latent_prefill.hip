@@ -22,8 +22,6 @@ constexpr int DQ = PREFILL_NOPE + LATENT_ROPE;
 constexpr int KNOPE = PREFILL_NOPE / 16, KSTEPS = DQ / 16, DBLOCKS = PREFILL_VALUE / 32;
 constexpr int SORTED = 32;                           // sequences at most that are sorted by their keys
 constexpr unsigned GRID_X = 1u << 20;                // workgroups in x (a dispatch has 2^32 threads a dimension)
-constexpr float LN2 = 0.69314718055994530942f, LOG2E = 1.44269504088896340736f;
-constexpr float LAZY = 8.f;  // the running maximum is raised only by more than this (in powers of 2)
 
 // Tile shapes. The waves of a workgroup take 32 rows each, all of one head: 128 rows, or 64 in two
 // sets of waves of which each takes half of a tile's keys, in steps of 32.
@@ -111,7 +109,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
     const float scale2 = a.scale * LOG2E;
     const int my = row0 + row_wave * 32 + (lane & 31);
 
-    float top = -INFINITY, from = 0.f;  // running maximum (what is subtracted: 0 if there is none)
+    float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
     float sum = 0.f, used = 0.f;        // sums of the weights and of the rounded weights
     acc16_t acc[DBLOCKS];
 #pragma unroll
@@ -246,13 +244,16 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                         s[i] = (nan >> r) & 1 ? NAN : (see >> r) & 1 ? s[i] : -INFINITY;
                     }
                 }
-                return max_halves(max16(s)) * scale2;
+                return max_halves(max16(s));
             };
-            // A new running maximum. It is a whole number, so that what is there is scaled by a power
-            // of 2, without rounding, weights that are already 16-bit values included.
+            // A new running maximum. It is a whole number, so that what is there is scaled by a power of 2:
+            // without rounding, but for weights that become float16's subnormal numbers (LIFT: half a step
+            // of those is 2^-31 of the largest weight). Whether one is needed is looked at in one rounding,
+            // so that no weight passes 2^(LAZY + LIFT) however far from 0 the logits lie.
+            auto too_high = [&](float high) { return fmaf(high, scale2, -top) > LAZY + LIFT<DT>; };
             auto raise = [&](float high) {
                 const float was = top;
-                top = fmaxf(top, ceilf(high));
+                top = fmaxf(top, ceilf(high * scale2) - LIFT<DT>);
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
@@ -287,14 +288,14 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 });
                 mfma_results(s);
                 float high = largest(0, s);
-                if (__any(high > top + LAZY)) raise(high);
+                if (__any(too_high(high))) raise(high);
                 products_k(1, s1, [&](int i) {
                     if (i < 8) weight2(s, i, p);
                     if (i % 2 == 0 && KSTEPS / 2 + i / 2 < LOADS) load(KSTEPS / 2 + i / 2, kv_next, kr_next, room, at_next, lanes);
                 });
                 mfma_results(s1);
                 high = largest(1, s1);
-                if (__any(high > top + LAZY)) {
+                if (__any(too_high(high))) {
                     const float keep = raise(high);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
@@ -310,7 +311,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 });
                 mfma_results(s);
                 const float high = largest(0, s);
-                if (__any(high > top + LAZY)) raise(high);
+                if (__any(too_high(high))) raise(high);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) weight2(s, i, p);
                 products_v(p, p, [&](int i) {
@@ -369,7 +370,7 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
             }
     }
     const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
-    if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = all == 0.f ? -INFINITY : (top + __log2f(all)) * LN2;
+    if (a.lse && lh == 0 && my < few) a.lse[(int64_t)(q0 + my) * a.heads + head] = row_lse<DT>(top, all);
     // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16). (A wave's own place; with
     // two sets it lies in what that wave has just read.)
     constexpr int OUT_BYTES = PREFILL_VALUE * 2;

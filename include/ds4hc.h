@@ -422,8 +422,10 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  * Products are of the 16-bit inputs and sums, softmax statistics and the running
  * output float32; the softmax weights are rounded to the 16-bit type for the
  * second product, and divided by their sum as rounded (lse is of the sum before
- * that rounding). Logits are float32: beyond 2^24 their last place is more than a
- * unit, and rows with logits beyond 2^30 may become NaN.
+ * that rounding). In float16 that rounding keeps its relative size down to 2^-20
+ * of the row's largest weight and weights below 2^-31 of it become 0; in bfloat16
+ * there is no such end. Logits are float32: beyond 2^24 their last place is more
+ * than a unit, and rows with logits beyond 2^30 (float16: 2^27) may become NaN.
  * scale > 0; heads 1..1024; N <= 2^24, N * heads <= 2^30.
  * Outputs may not overlap inputs or each other, as ranges from the first to the
  * last element; rows of out may not overlap one another.

@@ -66,3 +66,89 @@ def test_attn_tiles_without_a_token_in_sequences_of_one_workgroup(heads):
     bt = Batch(211, q_len, kv_len, 64, 128, BF)
     no_sequence_has_page_0(bt, math.nan)
     check_holes(bt, heads, [(b, b % 3) for b in range(0, 299, 2)] + [(299, p) for p in (0, 7, 8, 50, 93)], None)
+
+# ------------------------------------------------------------------ float16 weights
+
+def one_over_many(n, d, seed):
+    """n keys of d elements whose logits under the query are normal, and a first one 17.5 above
+    them that has 99.5 % of the weight. Element 5, which the query does not look at, is 1 in all
+    keys but the first, where it is 0: its output is what the others weigh."""
+    g = torch.Generator().manual_seed(seed)
+    q = torch.randn(d, generator=g)
+    q[5] = 0
+    q = q.to(HF)
+    k = torch.randn(n, d, generator=g)
+    scale = 1 / q.double().norm().item()
+    k[0] = q.float() * (17.5 * scale)
+    k[:, 5] = 1
+    k[0, 5] = 0
+    return q, k.to(HF), scale
+
+
+def assert_tail(got, q, k, v, scale, where):
+    """Every weight is rounded once, by u of it or half a step of the subnormals, 2^-25; the
+    largest is above 2^6. With n of them numerator and denominator are each off by at most
+    u + n 2^-31 of the weights' sum; logits and sums as in site_testlib."""
+    n, u, e = len(k), 2.0 ** -11, 2.0 ** -24
+    q, k, v = q.double(), k.double(), v.double()
+    s = k @ q * scale
+    w = torch.softmax(s, 0)
+    out, size = w @ v, w @ v.abs()
+    ds = (len(q) + 8) * e * scale * (k.abs() @ q.abs()).max()
+    bound = (2 * u + 4 * ds + 2 * (n + 64) * e) * size + u * out.abs() + 2 * n * 2.0 ** -31 * v.abs().amax(0)
+    over = ((got.double() - out).abs() / bound).max().item()
+    assert over <= 1.0, f"{where}: {over:.3g} times the bound; element 5 {got[5].item():.5f} for {out[5].item():.5f}"
+
+
+@pytest.mark.parametrize("heads", [1, 64, 128])  # 32, 64 and 128 rows a tile
+def test_attn_float16_keeps_the_weights_of_many_small_ones(heads):
+    """As many sequences as workgroups, all of the same pages, so that each is summed in one run."""
+    n, page = 131072, 4096
+    q, k, scale = one_over_many(n, 192, 221)
+    cache = k.view(n // page, page, 192).contiguous().cuda()
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").expand(256, -1).contiguous()
+    queries = q.cuda().expand(256, heads, 192)
+    cu = torch.arange(257, dtype=torch.int32, device="cuda")
+    lens = torch.full((256,), n, dtype=torch.int32, device="cuda")
+    out, lse = B.ds4hc_latent_attn(queries[..., :128], queries[..., 128:], cache, cu, lens, table, scale=scale, want_lse=True)
+    want = torch.logsumexp(k.double() @ q.double() * scale, 0).item()
+    for b, h in ((0, 0), (100, heads // 2), (255, heads - 1)):
+        assert_tail(out[b, h].cpu(), q, k, k[:, :128], scale, f"sequence {b} head {h}")
+        assert abs(lse[b, h].item() - want) < 1e-3
+
+
+@pytest.mark.parametrize("rows", [1, 49153])  # 64 and 128 rows a workgroup
+def test_prefill_float16_keeps_the_weights_of_many_small_ones(rows):
+    n = 131072
+    q, k, scale = one_over_many(n, 192, 223)
+    kv = torch.cat((k[:, :128], k[:, :128]), -1).view(n, 1, 256).contiguous()
+    cu = lambda v: torch.tensor([0, v], dtype=torch.int32, device="cuda")  # noqa: E731
+    out, lse = B.ds4hc_latent_prefill(q.cuda().expand(rows, 1, 192).contiguous(), kv.cuda(), k[:, 128:].contiguous().cuda(),
+                                      cu(rows), cu(n), scale=scale, causal=False, want_lse=True)
+    for r in {0, rows // 2, rows - 1}:
+        assert_tail(out[r, 0].cpu(), q, k, k[:, :128], scale, f"row {r}")
+
+
+@pytest.mark.parametrize("dtype,far", [(BF, 2.0 ** 30), (HF, 2.0 ** 27)])
+def test_far_logits_stay_finite(dtype, far):
+    """Up to the documented end of the logits' range, on both sides of 0 and of every step of the
+    running maximum: keys along the query, so that logit j is `far` times a number of [-1, 1]."""
+    g = torch.Generator().manual_seed(227)
+    n, heads = 500, 64
+    q = (torch.randn(192, generator=g) * 64).to(dtype)
+    for size in (far, far / 7, far / 64, 2.0 ** 14):
+        k = (q.float() * (2 * torch.rand(n, 1, generator=g) - 1)).to(dtype)
+        s = k.double() @ q.double()
+        scale = 0.999 * size / s.abs().max().item()
+        cu = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+        table = torch.arange(32, dtype=torch.int32, device="cuda")[None]
+        cache = torch.zeros(512, 192, dtype=dtype)
+        cache[:n] = k
+        many = q.cuda().expand(2, heads, 192)
+        out, lse = B.ds4hc_latent_attn(many[..., :128], many[..., 128:], cache.view(32, 16, 192).cuda(), cu(0, 2), cu(n), table,
+                                       scale=scale, want_lse=True)
+        assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all(), size
+        kv = torch.cat((k[:, :128], k[:, :128]), -1).view(n, 1, 256).expand(n, heads, 256).contiguous().cuda()
+        out, lse = B.ds4hc_latent_prefill(q.cuda().expand(n, heads, 192).contiguous(), kv, k[:, 128:].contiguous().cuda(), cu(0, n),
+                                          cu(0, n), scale=scale, want_lse=True)
+        assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all(), size
