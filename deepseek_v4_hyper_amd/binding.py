@@ -550,7 +550,7 @@ def ds4hc_rope_frequencies(dim, base=10000.0, *, factor=1.0, original_length=0, 
                            beta_slow=1.0, device=None):
     """Angles a position of the dim / 2 pairs (float64 tensor) and the amplitude, for
     ds4hc_rope and ds4hc_latent_append. factor > 1 stretches the positions: all pairs
-    alike, or with the YaRN ramp if original_length is given."""
+    alike, or by the ramp in include/ds4hc.h if original_length is given."""
     torch = _torch()
     f = torch.empty(max(int(dim) // 2, 1), dtype=torch.float64)
     amplitude = ctypes.c_float()

@@ -138,7 +138,9 @@ ds4hc_status ds4hc_rope_frequencies(int32_t dim, double base, double factor, int
     if (ramp) {
         const double per = dim / (2.0 * log(base)), len = (double)original_length / (2.0 * M_PI);
         lo = fmax(floor(per * log(len / beta_fast)), 0.0);
-        hi = fmin(ceil(per * log(len / beta_slow)), dim / 2 - 1.0);
+        // behind the last pair (dim / 2 - 1) for long trained lengths: the ramp's slope is what
+        // counts, and pairs that make more than beta_slow turns are not to be stretched fully
+        hi = fmin(ceil(per * log(len / beta_slow)), dim - 1.0);
     }
     for (int i = 0; i < dim / 2; ++i) {
         const double f = pow(base, -2.0 * i / dim);

@@ -343,12 +343,17 @@ ds4hc_status ds4hc_rope(int64_t N, int32_t heads, int32_t dim, ds4hc_dtype dtype
  *   f_i = base^(-2i / dim)                                      (factor == 1)
  *   f_i / factor               (factor > 1, original_length == 0: interpolated)
  *   f_i ((1 - k_i) / factor + k_i)                (factor > 1, original_length > 0)
- * the last with the ramp of Peng et al. 2023 ("YaRN: Efficient Context Window
- * Extension of Large Language Models"): with turns(b) = dim ln(original_length /
- * (2 pi b)) / (2 ln base), lo = max(floor(turns(beta_fast)), 0), hi =
- * min(ceil(turns(beta_slow)), dim / 2 - 1),
+ * the last after Peng et al. 2023 ("YaRN: Efficient Context Window Extension of
+ * Large Language Models"): pairs that make beta_fast turns or more over the trained
+ * length stay as they are, those of beta_slow or fewer are stretched fully. With the
+ * pair that makes b turns, pair(b) = dim ln(original_length / (2 pi b)) / (2 ln base),
+ * lo = max(floor(pair(beta_fast)), 0), hi = min(ceil(pair(beta_slow)), dim - 1),
  *   k_i = 1 - clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
- * and amplitude = 0.1 ln(factor) + 1 (1 in the other two cases). base > 1,
+ * and amplitude = 0.1 ln(factor) + 1 (1 in the other two cases). Between the ends
+ * the ramp is linear in the pair's index, the form in common use, which trained
+ * weights expect; the paper's own is linear in the turns (dim 64, length 4096,
+ * factor 40: pair 16 keeps 0.55 of its frequency here, 0.20 there). hi may lie
+ * behind the last pair, as it does for long trained lengths. base > 1,
  * factor >= 1, beta_fast >= beta_slow > 0 (looked at in the last case only).
  */
 ds4hc_status ds4hc_rope_frequencies(int32_t dim, double base, double factor,
