@@ -300,7 +300,9 @@ ds4hc_status ds4hc_combine(const ds4hc_params *p, int32_t d_total, int64_t T, ds
  * of a page whose block_table entry is not in [0, n_pages) as not in the cache
  * (no query sees them, an append to them stores nothing). No value in them makes
  * a kernel read or write outside the arrays given. Sequences of one call that
- * overlap (cu_q that does not rise) write the shared rows in any order.
+ * overlap (cu_q that does not rise) write the shared rows in any order, and
+ * ds4hc_latent_prefill, whose grid has room for N queries, may then leave others
+ * unwritten.
  * ---------------------------------------------------------------------------
  */
 
@@ -368,7 +370,8 @@ ds4hc_status ds4hc_rope_frequencies(int32_t dim, double base, double factor,
  * cu_q[b] .. cu_q[b + 1] - 1 of the call's N, and they are the LAST tokens of
  * its kv_len[b] tokens (token i of the call's q_len for b is token
  * kv_len[b] - q_len + i of the sequence). Tokens of the call behind the last
- * sequence are neither read nor written.
+ * sequence have no effect and their outputs are left as they were; their inputs
+ * may be read (all N rows must be there).
  */
 typedef struct {
     ds4hc_dtype dtype;          /* DS4HC_BF16 or DS4HC_F16 */
@@ -414,9 +417,11 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  *   otherwise those whose bit is set: bit d % 64 of word tree_mask[t][d / 64]
  *   stands for token d of the call's tokens for b (its own bit included: nothing
  *   is implied). Tokens d >= 64 * mask_words are seen by none.
- * A row that sees nothing gives out = 0 and lse = -infinity. A cached token that
- * holds a value that is not finite makes the rows that see it not finite and
- * does not touch the others.
+ * A row that sees nothing gives out = 0 and lse = -infinity, and so does one all of
+ * whose logits are -infinity. A NaN in a cached token, or an infinity in its latent,
+ * makes the rows that see it not finite, in some of their elements at least. An
+ * infinity in its rotated part gives an infinite logit: -infinity is a weight of 0,
+ * +infinity makes the row not finite. Rows that do not see the token stay right.
  *   q_latent [N, heads, d_latent], q_rope [N, heads, 64] strided, c->dtype (read)
  *   cache    (read)
  *   tree_mask [N, mask_words] uint64 or NULL (read; mask_words 1..1024)
@@ -461,8 +466,10 @@ size_t ds4hc_latent_attn_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, 
  *   k_rope [S, 64], k_rope_stride elements between rows, shared by the heads (read)
  *   cu_q, cu_k [n_seqs + 1] int32 (read)
  *   out    [N, heads, 128] dense (written), lse_opt [N, heads] float32 or NULL (written)
- * Rows of out and lse behind the last sequence are left as they were. Values that
- * are not finite stay with the rows that see them, as for ds4hc_latent_attn.
+ * Rows of out and lse behind the last sequence are left as they were. Keys and
+ * values that are not finite touch no row that does not see them; of those that do,
+ * a NaN or an infinite value makes elements not finite at least, and an infinite
+ * key an infinite logit, as for ds4hc_latent_attn.
  * Rounding as for ds4hc_latent_attn. heads 1..1024, N and S <= 2^24,
  * N * heads <= 2^30, n_seqs <= 2^20.
  */

@@ -6,7 +6,7 @@ import torch
 
 from deepseek_v4_hyper_amd import binding as B
 from hc_testlib import say
-from site_testlib import Batch, assert_attention, random_tree
+from site_testlib import Batch, assert_attention, attend64, random_tree
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -152,3 +152,82 @@ def test_far_logits_stay_finite(dtype, far):
         out, lse = B.ds4hc_latent_prefill(q.cuda().expand(n, heads, 192).contiguous(), kv, k[:, 128:].contiguous().cuda(), cu(0, n),
                                           cu(0, n), scale=scale, want_lse=True)
         assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all(), size
+
+# ------------------------------------------------------------------ infinite logits
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("heads", [8, 64, 128])
+def test_attn_a_logit_of_minus_infinity_is_a_weight_of_0(heads, tree):
+    """An infinity in a cached token's rotated part: the rows that see it and whose product with
+    it is negative pass over the token; where it is positive they are not finite."""
+    bt = Batch(231, [4, 1], [300, 130], 64, 512)
+    ql, qr = bt.queries(heads)
+    qr[:, ::2, 9], qr[:, 1::2, 9] = -1.0, 1.0
+    mask = random_tree(bt.g, bt.q_len, 1) if tree else None
+    ref = bt.reference(ql, qr, 0.07, mask, [])
+    flat = bt.cache.view(-1, 576)
+    for j in (5, 200, 296, 297):  # context, and the call's own first two tokens
+        kept = flat[bt.rows(0, 300)[j]].clone()
+        flat[bt.rows(0, 300)[j], 512 + 9] = math.inf
+        out, lse = B.ds4hc_latent_attn(ql.cuda(), qr.cuda(), bt.cache.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.table.cuda(),
+                                       scale=0.07, tree_mask=None if mask is None else mask.cuda(), want_lse=True)
+        out, lse = out.cpu(), lse.cpu()
+        with_it = bt.reference(ql[:, ::2], qr[:, ::2], 0.07, mask, [])
+        for t in range(5):
+            sees = t < 4 and (j < 296 or (j - 296 <= t if mask is None else bool(int(mask[t, 0]) >> (j - 296) & 1)))
+            r, n = with_it[t]
+            r = r[:3] + (ref[t][0][3][::2],)  # (the logits' error bound of the finite ones)
+            assert_attention(out[t, ::2], lse[t, ::2], r, n, BF, f"token {t}, infinity at {j}")
+            if sees:
+                assert not torch.isfinite(out[t, 1::2].float()).any()
+            else:
+                assert_attention(out[t, 1::2], lse[t, 1::2], tuple(x[1::2] for x in ref[t][0]), n, BF, f"token {t}, infinity at {j}")
+        flat[bt.rows(0, 300)[j]] = kept
+
+
+def test_attn_rows_whose_every_logit_is_minus_infinity():
+    """They are as rows that see nothing, in a tile that all rows see whole, in a masked one and
+    over several parts."""
+    for kv in (64, 130, 2000):
+        bt = Batch(233, [1], [kv], 64, 512)
+        ql, qr = bt.queries(64)
+        qr[:, ::2, 9], qr[:, 1::2, 9] = -1.0, 1.0
+        bt.cache[..., 512 + 9] = math.inf
+        bt.cache.view(-1, 576)[bt.rows(0, kv)[kv - 1], 512 + 9] = math.inf
+        out, lse = B.ds4hc_latent_attn(ql.cuda(), qr.cuda(), bt.cache.cuda(), bt.cu.cuda(), bt.lens.cuda(), bt.table.cuda(),
+                                       scale=0.07, want_lse=True)
+        assert (out[0, ::2] == 0).all() and (lse[0, ::2] == -math.inf).all()
+        assert not torch.isfinite(out[0, 1::2].float()).any()
+
+
+@pytest.mark.parametrize("heads", [2, 400])  # 64 and 128 rows a workgroup
+@pytest.mark.parametrize("part", ["head", "shared"])
+def test_prefill_a_logit_of_minus_infinity_is_a_weight_of_0(heads, part):
+    """An infinite key: rows that see it with a negative product pass over it, those with a positive
+    one are not finite, those that do not see it are as ever. (To the bound, not to the bit: 32 rows
+    share the decision to raise a running maximum, which scales each by a power of 2 of its own and
+    moves the rounding of x - maximum, as the bound's share for the logits counts.)"""
+    g = torch.Generator().manual_seed(239)
+    n = 150
+    q, kv, kr = (torch.randn(*s, generator=g).to(BF) for s in ((n, heads, 192), (n, heads, 256), (n, 64)))
+    e = 7 if part == "head" else 128 + 9
+    q[:, :, e] = torch.where(torch.arange(n) % 2 == 0, -1.0, 1.0).to(BF)[:, None]
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for at in (0, 40, 64, 149):
+        was = kv[at, :, 7].clone(), kr[at, 9].clone()
+        if part == "head":
+            kv[at, :, 7] = math.inf
+        else:
+            kr[at, 9] = math.inf
+        out, lse = [t.cpu() for t in B.ds4hc_latent_prefill(q.cuda(), kv.cuda(), kr.cuda(), cu, cu, scale=0.08, want_lse=True)]
+        odd = at + (at + 1) % 2
+        assert not torch.isfinite(out[odd::2].float()).any()
+        even = at + at % 2
+        for h in (0, heads - 1):
+            seen = torch.ones(n, n, dtype=torch.bool).tril()
+            seen[:, at] = False
+            keys = torch.cat((kv[:, h, :128], kr), -1)
+            for rows in (slice(0, at), slice(even, n, 2)):
+                ref = attend64(q[rows, h], keys, kv[:, h, 128:], seen[rows], 0.08)
+                assert_attention(out[rows, h], lse[rows, h], ref, seen[rows].sum(-1), BF, f"infinity at {at}, head {h}")
+        kv[at, :, 7], kr[at, 9] = was
