@@ -71,7 +71,7 @@ __global__ __launch_bounds__(THREADS) void rope_kernel(RopeArgs a) {
     const elem_t<DT> *x = static_cast<const elem_t<DT> *>(a.x) + t * a.x_token;
     elem_t<DT> *y = static_cast<elem_t<DT> *>(a.y) + t * a.y_token;
     const int pieces = a.heads * each;
-#pragma unroll DT == DT_F16 ? 1 : 4
+#pragma unroll 1  // (4: the same within 2 % for all types and layouts, 2 % slower for one head)
     for (int k = blockIdx.y * THREADS + threadIdx.x; k < pieces; k += gridDim.y * THREADS) {
         const int h = k / each, i = k - h * each;
         const elem_t<DT> *xh = x + h * a.x_head;
@@ -192,9 +192,13 @@ template <int DT> hipError_t launch_rope_of(const RopeArgs &a, hipStream_t s) {
     const bool rows16 = ((uintptr_t)a.x | (uintptr_t)a.y | (uintptr_t)((a.x_token | a.y_token | a.x_head | a.y_head) * B)) % 16 == 0;
     const bool vector = rows16 && a.dim % (a.half ? 2 * V : V) == 0;
     // a workgroup has four pieces a thread where the tokens alone fill the chip (they share the
-    // token's cosines and sines, 32 or more of them in 64 bits), one where they do not: 128 heads x
-    // 64, four pieces and one: 256 tokens 4.4 and 4.0 us, 512 5.1 and 5.0, 1024 7.0 and 7.5, 8192 46
-    // and 56. (Pairs in place of 16 bytes, what rows on other boundaries get: 11 us at 1024, 90 at 8192.)
+    // token's cosines and sines, 32 or more of them in 64 bits), one where they do not. bf16, heads x
+    // 64, four pieces and one: 128 heads, 256 tokens 4.4 and 4.0 us, 512 5.1 and 5.0, 1024 7.1 and 7.6,
+    // 4096 22.8 and 23.4, 8192 45 and 56; 64 heads, 1024 tokens 4.8 and 5.0, 2048 6.9 and 7.5, 8192 22.6 and
+    // 23.5; up to 32 heads (256 pieces) both are the same launch. float32, 128 heads, 1024 tokens 12.6 and 13.0,
+    // 8192 111 and 115. Half layout: equal within 2 % but for 16-bit types at 8192 x 128, 55 and 48. Pairs in
+    // place of 16 bytes, what rows on other boundaries get: 1024 x 128 11.3 and 16.5, 8192 x 128 94 and 157,
+    // 8192 x 8 9.3 and 9.4, 8192 x 1 5.6 either way.
     const int pieces = a.heads * (a.dim / 2) / (vector ? (a.half ? V : V / 2) : 1);
     const int64_t by_token = a.N >= 1024 ? 4 : 1;
     const int64_t splits = (pieces + THREADS * by_token - 1) / (THREADS * by_token);
