@@ -72,16 +72,21 @@ __device__ __forceinline__ int64_t cache_row(const Paged &c, int b, int j) {
 }
 
 // cos and sin of position * inv_freq. The angle is formed and reduced to a part
-// of a turn in 64 bits (a float32 angle of position 2^20 is off by 2^-5), the
-// rest of it, at most half a turn, has 32 bits' precision.
+// of a turn in 64 bits (a float32 angle of position 2^20 is off by 2^-5). The
+// functions are of its float32 part, and what that leaves, d, turns the pair by
+// (1, d): at most 1.35 x 2^-24 off over 2^25 angles of positions to 10^6, 1.92
+// without it, for 0.9 us of 27 for 65536 tokens of one head, 0.1 of 5.6 for 8192
+// and no time with many heads. (64-bit functions, 0.50, add 5 us and 0.7.)
 __device__ __forceinline__ void rope_angle(int64_t position, double inv_freq, float amplitude,
                                            float &c, float &s) {
     double turns = (double)position * inv_freq * 0.15915494309189533577;  // 1 / (2 pi)
     turns -= rint(turns);
+    const double half_turns = 2.0 * turns;
+    const float rounded = (float)half_turns, d = (float)((half_turns - rounded) * 3.14159265358979323846);
     float sn, cs;
-    sincospif((float)(2.0 * turns), &sn, &cs);
-    c = cs * amplitude;
-    s = sn * amplitude;
+    sincospif(rounded, &sn, &cs);
+    c = fmaf(-d, sn, cs) * amplitude;
+    s = fmaf(d, cs, sn) * amplitude;
 }
 
 // ------------------------------------------------------------------ matrix tiles

@@ -231,3 +231,26 @@ def test_prefill_a_logit_of_minus_infinity_is_a_weight_of_0(heads, part):
                 ref = attend64(q[rows, h], keys, kv[:, h, 128:], seen[rows], 0.08)
                 assert_attention(out[rows, h], lse[rows, h], ref, seen[rows].sum(-1), BF, f"infinity at {at}, head {h}")
         kv[at, :, 7], kr[at, 9] = was
+
+
+# ------------------------------------------------------------------ angles
+
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_angles_are_not_rounded_to_float32(interleaved):
+    """x = (1, 0) gives cos and sin themselves. The float32 functions are documented to a unit in the
+    last place, at most 2^-24 below 1; one sum brings in what rounding the reduced angle left, 2^-25
+    at most; its parts' roundings and the angle's 64-bit product are far below (rounded to float32,
+    the angle of up to half a turn alone would be off by pi 2^-25)."""
+    n = 1 << 19
+    f = B.ds4hc_rope_frequencies(64)[0].cuda()
+    g = torch.Generator().manual_seed(241)
+    positions = torch.randint(0, 1000000, (n,), generator=g).cuda()
+    x = torch.zeros(n, 1, 64, device="cuda")
+    first = x[..., 0::2] if interleaved else x[..., :32]
+    first.fill_(1)
+    y = B.ds4hc_rope(x, positions, f, interleaved=interleaved)[:, 0].double()
+    c, s = (y[:, 0::2], y[:, 1::2]) if interleaved else (y[:, :32], y[:, 32:])
+    a = positions.double()[:, None] * f
+    bound = 1.5 * 2.0 ** -24 + a * 2.0 ** -50 + 2.0 ** -40
+    worst = max(((c - a.cos()).abs() / bound).max().item(), ((s - a.sin()).abs() / bound).max().item())
+    assert worst <= 1, worst
