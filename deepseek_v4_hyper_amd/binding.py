@@ -658,8 +658,10 @@ def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, sca
     _rows(q_rope, (N, heads, 64), dtype, "q_rope", here)
     words = 0
     if tree_mask is not None:
-        words = tree_mask.shape[-1]
+        words = tree_mask.shape[-1] if tree_mask.dim() else 0
         _dense(tree_mask, (N, words), torch.int64, "tree_mask", here)
+        if words < 1:  # (has no address: would be taken for no mask)
+            raise ValueError("tree_mask must be [N, words] of one word a token at least")
     with _on(stream):
         if out is None:
             out = _empty(shape, dtype, cache.device)

@@ -254,3 +254,14 @@ def test_rope_angles_are_not_rounded_to_float32(interleaved):
     bound = 1.5 * 2.0 ** -24 + a * 2.0 ** -50 + 2.0 ** -40
     worst = max(((c - a.cos()).abs() / bound).max().item(), ((s - a.sin()).abs() / bound).max().item())
     assert worst <= 1, worst
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_a_tree_mask_without_words_is_refused():
+    """An array of no elements has no address, and a call without a mask is another one: causal."""
+    bt = Batch(251, [2], [10], 16, 128)
+    ql, qr = bt.queries(2)
+    args = [t.cuda() for t in (ql, qr, bt.cache, bt.cu, bt.lens, bt.table)]
+    with pytest.raises(ValueError, match="tree_mask"):
+        B.ds4hc_latent_attn(*args, scale=0.07, tree_mask=torch.zeros(2, 0, dtype=torch.int64, device="cuda"))
