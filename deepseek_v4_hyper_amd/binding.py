@@ -486,7 +486,8 @@ def ds4hc_latent_prefill_raw(N, S, n_seqs, heads, dtype, scale, flags, q, kv, k_
 
 
 # These calls take a few microseconds on the GPU, so their checks are made quick: one
-# look at each tensor, and the reason spelt out only for what did not pass.
+# look at each tensor, and the reason spelt out only for what did not pass. They record no
+# gradient: outputs of inputs that require one are detached.
 
 @functools.lru_cache(maxsize=None)
 def _codes():
@@ -564,7 +565,8 @@ def ds4hc_rope(x, positions, inv_freq, *, interleaved=True, inverse=False, ampli
                stream=None):
     """Rotary positions. x [N, heads, dim] (float32|bfloat16|float16; a view of part of
     a head is fine, the last dimension dense), positions [N] int64, inv_freq [dim / 2]
-    float64. out may be x itself (in place). Returns out [N, heads, dim]."""
+    float64. out may be x itself (in place). Returns out [N, heads, dim], detached; the
+    gradient of x is that of out rotated with inverse=True."""
     torch = _torch()
     if not getattr(x, "is_cuda", False):
         _tensors(x=x)
@@ -642,8 +644,8 @@ def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, sca
     """Latent attention over the paged cache, absorbed form. q_latent [N, heads, d_latent]
     and q_rope [N, heads, 64] (strided views are fine), cache and batch as in
     ds4hc_latent_append, tree_mask [N, words] int64 or None (causal among the call's own
-    tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None). Rows
-    behind the last sequence are left as they were."""
+    tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None), detached.
+    Rows behind the last sequence are left as they were."""
     torch = _torch()
     if not getattr(q_latent, "is_cuda", False):
         _tensors(q_latent=q_latent)
@@ -694,7 +696,7 @@ def ds4hc_latent_prefill(q, kv, k_rope, cu_q, cu_k, *, scale, causal=True, out=N
     """Latent attention over expanded keys and values of a ragged batch. q [N, heads, 192],
     kv [S, heads, 256] (128 key | 128 value elements a head), k_rope [S, 64] (rows may be
     strided), cu_q and cu_k [B + 1] int32. Returns (out [N, heads, 128], lse [N, heads]
-    float32 or None). Rows behind the last sequence are left as they were."""
+    float32 or None), detached. Rows behind the last sequence are left as they were."""
     torch = _torch()
     if not getattr(q, "is_cuda", False):
         _tensors(q=q)

@@ -7,12 +7,14 @@
 // 128 heads 1088 * 2 operations a row against 1152 bytes a token, so that one token of 128
 // heads stands where the card's rates of memory and of matrix products meet. A workgroup a CU
 // takes 128 rows (32 a wave, their sums in its 256 accumulation registers) through tiles of 64
-// tokens, two of them in LDS; one tile takes 4.1 us while all of the card streams (4.6 TB/s).
-// Beside the tiles a workgroup spends 12 us before its first (the batch's arrays, the page, the
-// queries) and 5 behind its last (its part of the sums).
+// tokens, two of them in LDS.
+// This kernel with 1, 8, 16, 32 and 64 tiles a workgroup (one sequence, 128 heads): 30, 62, 97, 180
+// and 409 us. That is 26 us beside the tiles (the batch's arrays, the page, the queries, the first
+// tile's way to LDS; the part of the sums behind the last) and 4.4 a tile (4.3 TB/s), 5.2 and 7.2 where
+// the cache is past 300 and 600 MB. Latent 256: 16 us and 2.8 a tile.
 // Measured (latent 512, bf16, both kernels in a graph): 64 sequences of up to 8192 tokens x 128
-// heads 140 us (106 and 27 us), one of 131000 tokens 82 us (59 and 20), 24 chains of 4 tokens
-// over up to 4096 113 us (90 and 24), 512 tokens over 4096 560 us (980 TFLOP/s).
+// heads 140 us (106 and 26 us), one of 131000 tokens 82 us (59 and 20), 24 chains of 4 tokens
+// over up to 4096 112 us (89 and 24), 512 tokens over 4096 556 us (985 TFLOP/s).
 #include <type_traits>
 
 #include "latent_device.hpp"
@@ -430,7 +432,10 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn_kernel(AttnArgs a) {
                 }
                 return keep;
             };
-            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {  // weights 2 i and 2 i + 1
+            // Weights 2 i and 2 i + 1, rounded to the type that the second product takes. (In two 16-bit
+            // parts they would double that product, half of all, to take the error of an output from
+            // 1.25 times that of float32 weights to 1.)
+            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {
                 const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
                 sum += e0;
                 sum += e1;
@@ -733,6 +738,9 @@ __global__ __launch_bounds__(JOIN_WAVES * 64) void attn_join_kernel(AttnArgs a) 
 // 110, 125; x 128 rows 230, 152, 139. Clusters of 1, 2 and 4 tiles of 128: 24 sequences x 512 rows
 // 120, 110, 109 us; 8 x up to 640 79, 76, 75; 128 rows a sequence, one tile, 139, 170, 270; a chunk
 // of 65536 rows 558, 554, 564. (One sequence of 128 rows alone is 5 % faster in two tiles of 64.)
+// The average is all that the host knows. It serves unlike sequences badly: 64 of one token x 128
+// heads take 150 us, a chunk of 512 tokens 556, both in one call 873, since each single token's
+// row tile gets a cluster of four.
 struct Plan {
     int rows, members;
 };

@@ -3,11 +3,15 @@
 // Per query row (a token, one head) and key of its sequence:
 //   s = scale (qn . kn + qr . kr),  out = softmax(s) V.
 // One pass over the keys with a running maximum and sum; both products on the matrix unit:
-// 640 operations a (row, key), while a key's 640 bytes serve 128 rows. What bounds it is the
-// issue of instructions: of a tile's some 3850 cycles a wave (128 rows, two waves a SIMD) the
-// products take 1280, the vector unit's exponentials and sums beside them about as much, loads,
-// reads and waits the rest; and the clock, which falls from 2.4 to 1.9 GHz under it. 4096 tokens
-// x 32 heads, causal: 199 us, 860 TFLOP/s; 8192 tokens: 689 us, 1.00 PFLOP/s.
+// 640 operations a (row, key), while a key's 640 bytes serve 128 rows. What bounds it, by counters
+// (4096 tokens x 32 heads, 128 rows a workgroup, two waves a SIMD): a wave is on a tile for 4770
+// cycles. 2000 it issues (302 vector instructions, 40 products among them, 58 of LDS, 85 scalar), 1420 it
+// waits for its turn, 1340 for data, results and the other waves. The matrix unit is busy 1280 of
+// them a wave, the vector unit 1180 besides, both at once 540. A workgroup alone on its CU takes 1.86 us a
+// tile, two 2.68 for both. The clock falls from 2.4 to 1.94 GHz. 66 tiles one behind another in each of
+// 512 places are 162 us; the rest of the call are places out of work: CUs are busy 83 % of its time
+// (8192 tokens: 93 %, 4450 cycles). 4096 tokens x 32 heads, causal: 187-210 us, 860 TFLOP/s, without a
+// mask 347 us, 990 TFLOP/s; 8192 tokens, causal: 686 us, 1.00 PFLOP/s; 4096 x 128 heads 755 us, 910.
 #include "latent_device.hpp"
 
 namespace ds4hc {
@@ -268,7 +272,10 @@ __global__ __launch_bounds__(THREADS, 2) void prefill_kernel(PrefillArgs a) {
                 }
                 return keep;
             };
-            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {  // weights 2 i and 2 i + 1
+            // Weights 2 i and 2 i + 1, rounded to the type that the second product takes. (In two 16-bit
+            // parts they would double that product, 40 % of all, to take the error of an output from
+            // 1.3 times that of float32 weights to 1.)
+            auto weight2 = [&](const acc16_t &s, int i, u32x4_t (&p)[2]) {
                 const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
                 sum += e0;
                 sum += e1;

@@ -46,7 +46,7 @@ template <int DT> __device__ __forceinline__ void turn(float &x0, float &x1, flo
     x1 = y1;
 }
 
-// Bound by memory: 4096 tokens x 128 heads x 64, bf16, take 21.8 us (6.2 TB/s of 134 MB), 25.0 us
+// Bound by memory: 4096 tokens x 128 heads x 64, bf16, take 21.9 us (6.1 TB/s of 134 MB), 25.2 us
 // a call in a chain of them; a few tokens 3.1 us, a launch. Simple pairs of 2-byte loads took 70 us.
 // A workgroup some heads of one token: grid (tokens, splits of the heads, tokens / 2^20). The token's
 // cosines and sines go to LDS first; then each thread turns 16 bytes at a time (VECTOR:

@@ -291,7 +291,8 @@ ds4hc_status ds4hc_combine(const ds4hc_params *p, int32_t d_total, int64_t T, ds
  * arrays of the 16-bit types and rows of strided arrays must start on 16-byte
  * boundaries (ds4hc_rope alone takes any element-aligned address and stride);
  * int32 and float32 arrays need 4-byte, int64, uint64 and float64 arrays 8-byte
- * alignment. The library allocates nothing and keeps nothing between calls.
+ * alignment. The library allocates nothing and keeps nothing between calls. These
+ * are operators of inference; of rotation the transpose is there (its gradient).
  *
  * What the device arrays of lengths and pages hold is not known to the host.
  * Every entry is checked in the kernel before it is used: cu_q and cu_k entries
@@ -428,7 +429,10 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  *   out      [N, heads, d_latent] strided, c->dtype (written)
  *   lse_opt  [N, heads] float32 or NULL (written)
  *   workspace of ds4hc_latent_attn_workspace_bytes(c, N, heads) bytes, 16-byte
- *            aligned (may be NULL when that is 0); as for ds4hc_pre.
+ *            aligned (may be NULL when that is 0); as for ds4hc_pre. It holds parts of
+ *            sums of 512 row tiles, whatever the lengths, which the host does not know:
+ *            with d_latent 512 34 MB up to 32 rows (tokens x heads) a sequence on
+ *            average, 68 MB up to 64, 135 MB beyond.
  * Products are of the 16-bit inputs and sums, softmax statistics and the running
  * output float32; the softmax weights are rounded to the 16-bit type for the
  * second product, and divided by their sum as rounded (lse is of the sum before
@@ -436,6 +440,9 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
  * of the row's largest weight and weights below 2^-31 of it become 0; in bfloat16
  * there is no such end. Logits are float32: beyond 2^24 their last place is more
  * than a unit, and rows with logits beyond 2^30 (float16: 2^27) may become NaN.
+ * Every row goes through all of its sequence's cached tokens, also those that a
+ * chunk's early tokens do not see: a prompt without a context (q_len = kv_len = 4096,
+ * 128 heads: 5.9 ms) is for ds4hc_latent_prefill (0.76 ms, besides the projections).
  * scale > 0; heads 1..1024; N <= 2^24, N * heads <= 2^30.
  * Outputs may not overlap inputs or each other, as ranges from the first to the
  * last element; rows of out may not overlap one another.
