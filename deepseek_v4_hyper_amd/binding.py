@@ -30,12 +30,19 @@ DS4HC_FLAG_FORCE_TILE = 8
 DS4HC_ROPE_HALF = 1
 DS4HC_ROPE_INVERSE = 2
 DS4HC_ATTN_FULL = 1
+DS4HC_VERIFY_MAX_TOKENS = 1024
+DS4HC_PAGES_DONE = 0
+DS4HC_PAGES_SHORT = 1
+DS4HC_PAGES_INVALID = 2
 
 EXPORTED = ("ds4hc_pre", "ds4hc_sinkhorn", "ds4hc_post", "ds4hc_fused", "ds4hc_workspace_bytes",
             "ds4hc_post_pre", "ds4hc_post_pre_workspace_bytes", "ds4hc_post_pre_noalloc",
             "ds4hc_partials", "ds4hc_partials_workspace_bytes", "ds4hc_combine",
             "ds4hc_rope", "ds4hc_rope_frequencies", "ds4hc_latent_append", "ds4hc_latent_attn",
             "ds4hc_latent_attn_workspace_bytes", "ds4hc_latent_prefill",
+           "ds4hc_latent_append8", "ds4hc_latent_attn8", "ds4hc_latent_attn8_workspace_bytes",
+           "ds4hc_draft_verify", "ds4hc_draft_verify_workspace_bytes", "ds4hc_cache_compact", "ds4hc_pages_copy",
+           "ds4hc_pages_resize", "ds4hc_pages_fork", "ds4hc_pages_workspace_bytes",
             "ds4hc_status_string", "ds4hc_last_hip_error", "ds4hc_abi_version")
 
 
@@ -64,6 +71,19 @@ class PagedCache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p)]
+
+
+class PageStore(ctypes.Structure):
+    """ds4hc_page_store: the paged caches of all layers."""
+    _fields_ = [("layers", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+                ("row_bytes", ctypes.c_int64), ("layer_stride", ctypes.c_int64), ("data", ctypes.c_void_p)]
+
+
+class PagePool(ctypes.Structure):
+    """ds4hc_page_pool: which slot has which pages."""
+    _fields_ = [("page_size", ctypes.c_int32), ("n_slots", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("block_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("refs", ctypes.c_void_p)]
 
 
 def make_params(n_hc: int, d: int, rms_eps: float = 1e-6, sinkhorn_iters: int = 20,
@@ -99,11 +119,25 @@ def load(path: str = LIB_PATH):
     lib.ds4hc_rope_frequencies.argtypes = [i32, f64, f64, i64, f64, f64, vp, vp]
     lib.ds4hc_latent_append.argtypes = [C, i64, dt, vp, i64, vp, f32, vp, vp, f32, u32, vp, vp]
     lib.ds4hc_latent_attn.argtypes = [C, i64, i32, f32, vp, S, vp, S, vp, vp, i32, vp, S, vp, vp, sz, vp]
-    lib.ds4hc_latent_attn_workspace_bytes.argtypes = [C, i64, i32]
-    lib.ds4hc_latent_attn_workspace_bytes.restype = sz
+    lib.ds4hc_latent_append8.argtypes = lib.ds4hc_latent_append.argtypes
+    lib.ds4hc_latent_attn8.argtypes = lib.ds4hc_latent_attn.argtypes
+    for f in ("ds4hc_latent_attn_workspace_bytes", "ds4hc_latent_attn8_workspace_bytes"):
+        getattr(lib, f).argtypes = [C, i64, i32]
+        getattr(lib, f).restype = sz
+    PS, PP = ctypes.POINTER(PageStore), ctypes.POINTER(PagePool)
+    lib.ds4hc_draft_verify.argtypes = [i64, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.ds4hc_draft_verify_workspace_bytes.argtypes = [i32, i32]
+    lib.ds4hc_draft_verify_workspace_bytes.restype = sz
+    lib.ds4hc_cache_compact.argtypes = [PS, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.ds4hc_pages_copy.argtypes = [PS, i64, vp, vp]
+    lib.ds4hc_pages_resize.argtypes = [PP, i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.ds4hc_pages_fork.argtypes = [PP, i64, vp, vp, vp, vp, sz, vp]
+    lib.ds4hc_pages_workspace_bytes.argtypes = [PP, i64]
+    lib.ds4hc_pages_workspace_bytes.restype = sz
     lib.ds4hc_latent_prefill.argtypes = [i64, i64, i32, i32, dt, f32, u32, vp, vp, vp, i64, vp, vp, vp, vp, vp]
     for f in ("ds4hc_rope", "ds4hc_rope_frequencies", "ds4hc_latent_append", "ds4hc_latent_attn",
-              "ds4hc_latent_prefill"):
+              "ds4hc_latent_prefill", "ds4hc_latent_append8", "ds4hc_latent_attn8", "ds4hc_draft_verify",
+              "ds4hc_cache_compact", "ds4hc_pages_copy", "ds4hc_pages_resize", "ds4hc_pages_fork"):
         getattr(lib, f).restype = ctypes.c_int
     for f in ("ds4hc_pre", "ds4hc_sinkhorn", "ds4hc_post", "ds4hc_fused", "ds4hc_post_pre",
               "ds4hc_post_pre_noalloc", "ds4hc_partials", "ds4hc_combine"):
@@ -474,6 +508,23 @@ def ds4hc_latent_attn_raw(c, N, heads, scale, ql, ql_strides, qr, qr_strides, ca
                                     ws, int(ws_bytes), stream)
 
 
+def ds4hc_latent_append8_raw(c, *rest):
+    """As ds4hc_latent_append_raw."""
+    return load().ds4hc_latent_append8(ctypes.byref(c), *rest)
+
+
+def ds4hc_latent_attn8_raw(c, N, heads, scale, ql, ql_strides, qr, qr_strides, cache, tree_mask,
+                           mask_words, out, out_strides, lse, ws, ws_bytes, stream):
+    return load().ds4hc_latent_attn8(ctypes.byref(c), int(N), int(heads), float(scale), ql,
+                                     Strides(*ql_strides), qr, Strides(*qr_strides), cache,
+                                     tree_mask, int(mask_words), out, Strides(*out_strides), lse,
+                                     ws, int(ws_bytes), stream)
+
+
+def ds4hc_latent_attn8_workspace_bytes(c: PagedCache, N: int, heads: int) -> int:
+    return int(load().ds4hc_latent_attn8_workspace_bytes(ctypes.byref(c), int(N), int(heads)))
+
+
 def ds4hc_latent_attn_workspace_bytes(c: PagedCache, N: int, heads: int) -> int:
     return int(load().ds4hc_latent_attn_workspace_bytes(ctypes.byref(c), int(N), int(heads)))
 
@@ -593,21 +644,50 @@ def ds4hc_rope(x, positions, inv_freq, *, interleaved=True, inverse=False, ampli
     return out
 
 
-def _paged(cache, cu_q, kv_len, block_table, here=None):
+def _paged(cache, cu_q, kv_len, block_table, here=None, eight=None):
+    """`eight`: the 16-bit type of a cache of 8-bit latents, None: a cache of 16-bit ones."""
     torch = _torch()
     here = torch.cuda.current_device() if here is None else here
     shape, table = cache.shape, block_table.shape
     if len(shape) != 3 or kv_len.dim() != 1 or len(table) != 2:
-        raise ValueError("cache must be [pages, page_size, d_latent + 64], kv_len [B] and block_table [B, max_pages]")
+        raise ValueError("cache must be [pages, page_size, d_latent + %d], kv_len [B] and block_table [B, max_pages]"
+                         % (64 if eight is None else 144))
     pages, page_size, D = shape
     B = kv_len.shape[0]
     i32 = torch.int32
-    _dense(cache, shape, cache.dtype, "cache", here)
+    _dense(cache, shape, cache.dtype if eight is None else torch.uint8, "cache", here)
     _dense(cu_q, (B + 1,), i32, "cu_q", here)
     _dense(kv_len, (B,), i32, "kv_len", here)
     _dense(block_table, (B, table[1]), i32, "block_table", here)
-    return PagedCache(_any_code(cache, "cache", True), D - 64, 64, page_size, pages, B, table[1], cu_q.data_ptr(),
+    code = _any_code(cache, "cache", True) if eight is None else _codes().get(eight)
+    if code is None or code == DS4HC_F32:
+        raise TypeError(f"an 8-bit cache's rotated keys are bfloat16 or float16, not {eight}")
+    return PagedCache(code, D - (64 if eight is None else 144), 64, page_size, pages, B, table[1], cu_q.data_ptr(),
                       kv_len.data_ptr(), block_table.data_ptr())
+
+
+def _append(eight, kv, positions, inv_freq, cache, cu_q, kv_len, block_table, norm_weight, rms_eps, interleaved, amplitude,
+            stream):
+    """ds4hc_latent_append; `eight`: None, or the 16-bit type of an 8-bit cache's rotated keys."""
+    torch = _torch()
+    if not getattr(kv, "is_cuda", False):
+        _tensors(kv=kv)
+    here = _device(stream)
+    c = _paged(cache, cu_q, kv_len, block_table, here, eight)
+    src = _any_code(kv, "kv")
+    N, D = kv.shape[0], c.d_latent + 64
+    _rows(kv, (N, D), kv.dtype, "kv", here)
+    _dense(positions, (N,), torch.int64, "positions", here)
+    _dense(inv_freq, (32,), torch.float64, "inv_freq", here)
+    if norm_weight is not None:
+        _dense(norm_weight, (c.d_latent,), torch.float32, "norm_weight", here)
+    call = load().ds4hc_latent_append8 if eight else load().ds4hc_latent_append
+    st = call(ctypes.byref(c), N, src, kv.data_ptr(), kv.stride(0) if N > 1 else D,
+              None if norm_weight is None else norm_weight.data_ptr(), rms_eps, positions.data_ptr(), inv_freq.data_ptr(),
+              amplitude, 0 if interleaved else DS4HC_ROPE_HALF, cache.data_ptr(), _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_latent_append8" if eight else "ds4hc_latent_append")
+    return cache
 
 
 def ds4hc_latent_append(kv, positions, inv_freq, cache, cu_q, kv_len, block_table, *,
@@ -618,40 +698,27 @@ def ds4hc_latent_append(kv, positions, inv_freq, cache, cu_q, kv_len, block_tabl
     inv_freq [32] float64, cache [pages, page_size, d_latent + 64] bfloat16|float16,
     cu_q [B + 1], kv_len [B], block_table [B, max_pages] int32, norm_weight [d_latent]
     float32 or None (no norm). Returns cache."""
-    torch = _torch()
-    if not getattr(kv, "is_cuda", False):
-        _tensors(kv=kv)
-    here = _device(stream)
-    c = _paged(cache, cu_q, kv_len, block_table, here)
-    src = _any_code(kv, "kv")
-    N, D = kv.shape[0], cache.shape[2]
-    _rows(kv, (N, D), kv.dtype, "kv", here)
-    _dense(positions, (N,), torch.int64, "positions", here)
-    _dense(inv_freq, (32,), torch.float64, "inv_freq", here)
-    if norm_weight is not None:
-        _dense(norm_weight, (c.d_latent,), torch.float32, "norm_weight", here)
-    st = load().ds4hc_latent_append(ctypes.byref(c), N, src, kv.data_ptr(), kv.stride(0) if N > 1 else D,
-                                    None if norm_weight is None else norm_weight.data_ptr(), rms_eps,
-                                    positions.data_ptr(), inv_freq.data_ptr(), amplitude,
-                                    0 if interleaved else DS4HC_ROPE_HALF, cache.data_ptr(), _raw_stream(stream, here))
-    if st:
-        _check(st, "ds4hc_latent_append")
-    return cache
+    return _append(None, kv, positions, inv_freq, cache, cu_q, kv_len, block_table, norm_weight, rms_eps, interleaved,
+                   amplitude, stream)
 
 
-def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, scale, tree_mask=None,
-                      out=None, lse=None, workspace=None, stream=None, want_lse=False):
-    """Latent attention over the paged cache, absorbed form. q_latent [N, heads, d_latent]
-    and q_rope [N, heads, 64] (strided views are fine), cache and batch as in
-    ds4hc_latent_append, tree_mask [N, words] int64 or None (causal among the call's own
-    tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None), detached.
-    Rows behind the last sequence are left as they were."""
-    torch = _torch()
+def ds4hc_latent_append8(kv, positions, inv_freq, cache, cu_q, kv_len, block_table, *, dtype=None,
+                         norm_weight=None, rms_eps=1e-6, interleaved=True, amplitude=1.0, stream=None):
+    """ds4hc_latent_append into a cache of 8-bit latents: cache [pages, page_size, d_latent + 144] uint8 (layout in
+    include/ds4hc.h), dtype bfloat16 (the default) or float16: that of its rotated keys. Returns cache."""
+    return _append(_torch().bfloat16 if dtype is None else dtype, kv, positions, inv_freq, cache, cu_q, kv_len, block_table,
+                   norm_weight, rms_eps, interleaved, amplitude, stream)
+
+
+def _attn(eight, q_latent, q_rope, cache, cu_q, kv_len, block_table, scale, tree_mask, out, lse, workspace, stream,
+          want_lse):
+    """ds4hc_latent_attn; `eight`: of an 8-bit cache."""
+    torch, lib = _torch(), load()
     if not getattr(q_latent, "is_cuda", False):
         _tensors(q_latent=q_latent)
     here = _device(stream)
-    c = _paged(cache, cu_q, kv_len, block_table, here)
-    dtype = cache.dtype
+    dtype = q_latent.dtype if eight else cache.dtype
+    c = _paged(cache, cu_q, kv_len, block_table, here, dtype if eight else None)
     if q_latent.dim() != 3:
         raise ValueError(f"q_latent must be [N, heads, d_latent], got {tuple(q_latent.shape)}")
     N, heads, _ = q_latent.shape
@@ -677,18 +744,36 @@ def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, sca
             _tensors(workspace=workspace)
             if workspace.get_device() != here or not workspace.is_contiguous():
                 raise ValueError("workspace must be a dense array on the call's device")
-        workspace, ws_bytes = _scratch(load().ds4hc_latent_attn_workspace_bytes(ctypes.byref(c), N, heads), workspace,
-                                       cache.device)
+        need = lib.ds4hc_latent_attn8_workspace_bytes if eight else lib.ds4hc_latent_attn_workspace_bytes
+        workspace, ws_bytes = _scratch(need(ctypes.byref(c), N, heads), workspace, cache.device)
     ls, rs, os_ = q_latent.stride(), q_rope.stride(), out.stride()
-    st = load().ds4hc_latent_attn(ctypes.byref(c), N, heads, scale, q_latent.data_ptr(), _strides(ls[0], ls[1]),
-                                  q_rope.data_ptr(), _strides(rs[0], rs[1]), cache.data_ptr(),
-                                  None if tree_mask is None else tree_mask.data_ptr(), words, out.data_ptr(),
-                                  _strides(os_[0], os_[1]), None if lse is None else lse.data_ptr(),
-                                  None if workspace is None else workspace.data_ptr(), ws_bytes,
-                                  _raw_stream(stream, here))
+    call = lib.ds4hc_latent_attn8 if eight else lib.ds4hc_latent_attn
+    st = call(ctypes.byref(c), N, heads, scale, q_latent.data_ptr(), _strides(ls[0], ls[1]), q_rope.data_ptr(),
+              _strides(rs[0], rs[1]), cache.data_ptr(), None if tree_mask is None else tree_mask.data_ptr(), words,
+              out.data_ptr(), _strides(os_[0], os_[1]), None if lse is None else lse.data_ptr(),
+              None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream, here))
     if st:
-        _check(st, "ds4hc_latent_attn")
+        _check(st, "ds4hc_latent_attn8" if eight else "ds4hc_latent_attn")
     return out, lse
+
+
+def ds4hc_latent_attn(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, scale, tree_mask=None,
+                      out=None, lse=None, workspace=None, stream=None, want_lse=False):
+    """Latent attention over the paged cache, absorbed form. q_latent [N, heads, d_latent]
+    and q_rope [N, heads, 64] (strided views are fine), cache and batch as in
+    ds4hc_latent_append, tree_mask [N, words] int64 or None (causal among the call's own
+    tokens). Returns (out [N, heads, d_latent], lse [N, heads] float32 or None), detached.
+    Rows behind the last sequence are left as they were."""
+    return _attn(False, q_latent, q_rope, cache, cu_q, kv_len, block_table, scale, tree_mask, out, lse, workspace, stream,
+                 want_lse)
+
+
+def ds4hc_latent_attn8(q_latent, q_rope, cache, cu_q, kv_len, block_table, *, scale, tree_mask=None,
+                       out=None, lse=None, workspace=None, stream=None, want_lse=False):
+    """ds4hc_latent_attn over a cache of 8-bit latents, [pages, page_size, d_latent + 144] uint8 as
+    ds4hc_latent_append8 fills it. Its rotated keys are of the queries' type."""
+    return _attn(True, q_latent, q_rope, cache, cu_q, kv_len, block_table, scale, tree_mask, out, lse, workspace, stream,
+                 want_lse)
 
 
 def ds4hc_latent_prefill(q, kv, k_rope, cu_q, cu_k, *, scale, causal=True, out=None, lse=None,
@@ -727,3 +812,224 @@ def ds4hc_latent_prefill(q, kv, k_rope, cu_q, cu_k, *, scale, causal=True, out=N
     if st:
         _check(st, "ds4hc_latent_prefill")
     return out, lse
+
+
+# ------------------------------------------------------------------ around the attention of drafted tokens
+
+def ds4hc_draft_verify_raw(N, n_seqs, vocab, target, target_stride, draft, draft_stride, tokens, parents, cu_q, uniform,
+                           path, n_kept, next_token, ws, ws_bytes, stream):
+    return load().ds4hc_draft_verify(int(N), int(n_seqs), int(vocab), target, int(target_stride), draft,
+                                     int(draft_stride), tokens, parents, cu_q, uniform, path, n_kept, next_token, ws,
+                                     int(ws_bytes), stream)
+
+
+def ds4hc_draft_verify_workspace_bytes(n_seqs: int, vocab: int) -> int:
+    return int(load().ds4hc_draft_verify_workspace_bytes(int(n_seqs), int(vocab)))
+
+
+def ds4hc_cache_compact_raw(store, N, n_seqs, max_pages, cu_q, kv_len, block_table, keep, n_keep, stream):
+    return load().ds4hc_cache_compact(ctypes.byref(store), int(N), int(n_seqs), int(max_pages), cu_q, kv_len, block_table,
+                                      keep, n_keep, stream)
+
+
+def ds4hc_pages_copy_raw(store, n, pairs, stream):
+    return load().ds4hc_pages_copy(ctypes.byref(store), int(n), pairs, stream)
+
+
+def ds4hc_pages_resize_raw(pool, n, slots, lengths, copies, status, ws, ws_bytes, stream):
+    return load().ds4hc_pages_resize(ctypes.byref(pool), int(n), slots, lengths, copies, status, ws, int(ws_bytes), stream)
+
+
+def ds4hc_pages_fork_raw(pool, n, parents, children, status, ws, ws_bytes, stream):
+    return load().ds4hc_pages_fork(ctypes.byref(pool), int(n), parents, children, status, ws, int(ws_bytes), stream)
+
+
+def ds4hc_pages_workspace_bytes(pool: PagePool, n: int) -> int:
+    return int(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), int(n)))
+
+
+def _own_scratch(need, workspace, here):
+    """The caller's workspace looked at, or a fresh one."""
+    if workspace is not None:
+        _tensors(workspace=workspace)
+        if workspace.get_device() != here or not workspace.is_contiguous():
+            raise ValueError("workspace must be a dense array on the call's device")
+    return _scratch(need, workspace, f"cuda:{here}")
+
+
+def ds4hc_draft_verify(target, tokens, cu_q, uniform, *, draft=None, parents=None, path=None, n_kept=None,
+                       next_token=None, workspace=None, stream=None):
+    """Which drafted tokens are kept, and the token that follows them. target [N, vocab] float32 (row t: the distribution
+    of what follows token t; rows may be strided), tokens [N] int64, cu_q [B + 1] int32, uniform [N] float32; draft
+    [N, vocab] float32 or None: the distributions of drafted chains, parents [N] int32 or None: the trees' (a token's
+    parent among its sequence's tokens). Returns (path [N] int32: the kept tokens' indices among the sequence's, then -1;
+    n_kept [B] int32, the first token included; next_token [B] int64). Entries of path behind the last sequence are left
+    as they were."""
+    torch = _torch()
+    if not getattr(target, "is_cuda", False):
+        _tensors(target=target)
+    here, i32 = _device(stream), torch.int32
+    if target.dim() != 2 or cu_q.dim() != 1:
+        raise ValueError("target must be [N, vocab] and cu_q [B + 1]")
+    N, vocab = shape = target.shape
+    B = cu_q.shape[0] - 1
+    if B < 0:
+        raise ValueError("cu_q must be [B + 1]")
+    _rows(target, shape, torch.float32, "target", here)
+    _dense(tokens, (N,), torch.int64, "tokens", here)
+    _dense(cu_q, (B + 1,), i32, "cu_q", here)
+    _dense(uniform, (N,), torch.float32, "uniform", here)
+    if draft is not None:
+        _rows(draft, shape, torch.float32, "draft", here)
+        if not N:  # (has no address: would be taken for none)
+            draft = None
+    if parents is not None:
+        _dense(parents, (N,), i32, "parents", here)
+        if draft is not None:
+            raise ValueError("drafted trees are judged by the target alone: draft goes with chains")
+    with _on(stream):
+        if path is None:
+            path = _empty((N,), i32, target.device)
+        else:
+            _dense(path, (N,), i32, "path", here)
+        if n_kept is None:
+            n_kept = _empty((B,), i32, target.device)
+        else:
+            _dense(n_kept, (B,), i32, "n_kept", here)
+        if next_token is None:
+            next_token = _empty((B,), torch.int64, target.device)
+        else:
+            _dense(next_token, (B,), torch.int64, "next_token", here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_draft_verify_workspace_bytes(B, vocab), workspace, here)
+    row = lambda t: t.stride(0) if N > 1 else vocab  # noqa: E731
+    st = load().ds4hc_draft_verify(N, B, vocab, target.data_ptr(), row(target), None if draft is None else draft.data_ptr(),
+                                   0 if draft is None else row(draft), tokens.data_ptr(),
+                                   None if parents is None else parents.data_ptr(), cu_q.data_ptr(), uniform.data_ptr(),
+                                   path.data_ptr(), n_kept.data_ptr(), next_token.data_ptr(),
+                                   None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_draft_verify")
+    return path, n_kept, next_token
+
+
+def _store(cache, here):
+    """Caches [layers, pages, page_size, row] (or one, without the first) of any type, each layer dense."""
+    if cache.get_device() != here:
+        raise ValueError(f"cache is on {cache.device}, the call runs on the current device, cuda:{here}")
+    if cache.dim() not in (3, 4):
+        raise ValueError(f"cache must be [layers, pages, page_size, row] or [pages, page_size, row], got {tuple(cache.shape)}")
+    layers, size = (1 if cache.dim() == 3 else cache.shape[0]), cache.element_size()
+    if not layers or not (cache if cache.dim() == 3 else cache[0]).is_contiguous():
+        raise ValueError("the caches of single layers must be dense, and there must be one")
+    pages, page_size, row = cache.shape[-3:]
+    return PageStore(layers, page_size, pages, row * size, cache.stride(0) * size if layers > 1 else 0, cache.data_ptr())
+
+
+def ds4hc_cache_compact(cache, cu_q, kv_len, block_table, keep, n_keep, *, stream=None):
+    """Moves kept tokens behind their sequences' contexts, in all layers. cache [layers, pages, page_size, row] or
+    [pages, page_size, row] of any type (a row a multiple of 16 bytes), cu_q [B + 1], kv_len [B], block_table
+    [B, max_pages], keep [N] (entries cu_q[b] .. rising: indices among the sequence's tokens of the call, as
+    ds4hc_draft_verify's path), n_keep [B], all int32. kv_len is that of the attention (the call's tokens included); what is
+    kept then ends at kv_len - q_len + n_keep. Returns cache."""
+    torch = _torch()
+    if not getattr(cache, "is_cuda", False):
+        _tensors(cache=cache)
+    here, i32 = _device(stream), torch.int32
+    store = _store(cache, here)
+    if kv_len.dim() != 1 or block_table.dim() != 2 or keep.dim() != 1:
+        raise ValueError("kv_len must be [B], block_table [B, max_pages] and keep [N]")
+    B, N, most = kv_len.shape[0], keep.shape[0], block_table.shape[1]
+    _dense(cu_q, (B + 1,), i32, "cu_q", here)
+    _dense(kv_len, (B,), i32, "kv_len", here)
+    _dense(block_table, (B, most), i32, "block_table", here)
+    _dense(keep, (N,), i32, "keep", here)
+    _dense(n_keep, (B,), i32, "n_keep", here)
+    st = load().ds4hc_cache_compact(ctypes.byref(store), N, B, most, cu_q.data_ptr(), kv_len.data_ptr(),
+                                    block_table.data_ptr(), keep.data_ptr(), n_keep.data_ptr(), _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_cache_compact")
+    return cache
+
+
+def ds4hc_pages_copy(cache, pairs, *, stream=None):
+    """Copies whole pages in all layers: pairs [n, 2] int32, (from, to); pairs with an entry that is no page are passed
+    over. cache as for ds4hc_cache_compact. Returns cache."""
+    torch = _torch()
+    if not getattr(cache, "is_cuda", False):
+        _tensors(cache=cache)
+    here = _device(stream)
+    store = _store(cache, here)
+    if pairs.dim() != 2:
+        raise ValueError("pairs must be [n, 2]")
+    _dense(pairs, (pairs.shape[0], 2), torch.int32, "pairs", here)
+    st = load().ds4hc_pages_copy(ctypes.byref(store), pairs.shape[0], pairs.data_ptr(), _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_pages_copy")
+    return cache
+
+
+def _pool(block_table, kv_len, refs, page_size, here):
+    torch = _torch()
+    if block_table.dim() != 2 or refs.dim() != 1:
+        raise ValueError("block_table must be [slots, max_pages] and refs [pages]")
+    slots, most = shape = block_table.shape
+    i32 = torch.int32
+    _dense(block_table, shape, i32, "block_table", here)
+    _dense(kv_len, (slots,), i32, "kv_len", here)
+    _dense(refs, refs.shape, i32, "refs", here)
+    return PagePool(int(page_size), slots, most, refs.shape[0], block_table.data_ptr(), kv_len.data_ptr(), refs.data_ptr())
+
+
+def ds4hc_pages_resize(block_table, kv_len, refs, page_size, slots, lengths, *, copies=None, status=None, workspace=None,
+                       stream=None):
+    """New lengths for the given slots: takes free pages, or gives pages back. block_table [slots, max_pages], kv_len
+    [slots] and refs [pages] int32 are changed in place; slots [n] and lengths [n] int32. Returns (copies [n, 2] int32 for
+    ds4hc_pages_copy, to be run before anything else is written to the pages; status [n] int32: DS4HC_PAGES_*)."""
+    torch = _torch()
+    if not getattr(block_table, "is_cuda", False):
+        _tensors(block_table=block_table)
+    here, i32 = _device(stream), torch.int32
+    pool = _pool(block_table, kv_len, refs, page_size, here)
+    n = slots.shape[0] if slots.dim() else 0
+    _dense(slots, (n,), i32, "slots", here)
+    _dense(lengths, (n,), i32, "lengths", here)
+    with _on(stream):
+        if copies is None:
+            copies = _empty((n, 2), i32, refs.device)
+        else:
+            _dense(copies, (n, 2), i32, "copies", here)
+        if status is None:
+            status = _empty((n,), i32, refs.device)
+        else:
+            _dense(status, (n,), i32, "status", here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here)
+    st = load().ds4hc_pages_resize(ctypes.byref(pool), n, slots.data_ptr(), lengths.data_ptr(), copies.data_ptr(),
+                                   status.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes,
+                                   _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_pages_resize")
+    return copies, status
+
+
+def ds4hc_pages_fork(block_table, kv_len, refs, page_size, parents, children, *, status=None, workspace=None, stream=None):
+    """Slots children [n] become copies of slots parents [n] (int32) that share their pages; block_table, kv_len and refs
+    as for ds4hc_pages_resize, which gives a sequence its own last page once it grows. Returns status [n] int32."""
+    torch = _torch()
+    if not getattr(block_table, "is_cuda", False):
+        _tensors(block_table=block_table)
+    here, i32 = _device(stream), torch.int32
+    pool = _pool(block_table, kv_len, refs, page_size, here)
+    n = parents.shape[0] if parents.dim() else 0
+    _dense(parents, (n,), i32, "parents", here)
+    _dense(children, (n,), i32, "children", here)
+    with _on(stream):
+        if status is None:
+            status = _empty((n,), i32, refs.device)
+        else:
+            _dense(status, (n,), i32, "status", here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here)
+    st = load().ds4hc_pages_fork(ctypes.byref(pool), n, parents.data_ptr(), children.data_ptr(), status.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream, here))
+    if st:
+        _check(st, "ds4hc_pages_fork")
+    return status

@@ -16,8 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libds4hc.so")
-SOURCES = ["hc_kernels.hip", "rope_kernels.hip", "latent_attn.hip", "latent_prefill.hip", "ds4hc_api.cpp",
-           "latent_api.cpp"]
+SOURCES = ["hc_kernels.hip", "rope_kernels.hip", "latent_attn.hip", "latent_attn8.hip", "latent_prefill.hip",
+           "draft_kernels.hip", "page_kernels.hip", "ds4hc_api.cpp", "latent_api.cpp", "serve_api.cpp"]
 # the plain device copy bench.py measures beside the op (not part of the op's ABI)
 LIB_BW = os.path.join(PKG, "libds4hc_bw.so")
 SOURCES_BW = ["bw_copy.hip"]

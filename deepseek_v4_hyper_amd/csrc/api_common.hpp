@@ -1,5 +1,5 @@
-// api_common.hpp -- argument checks that the C ABI's two implementation files
-// (ds4hc_api.cpp, latent_api.cpp) share. Not installed; not part of the ABI.
+// api_common.hpp -- argument checks that the C ABI's implementation files
+// (ds4hc_api.cpp, latent_api.cpp, serve_api.cpp) share. Not installed; not part of the ABI.
 #pragma once
 
 #include "ds4hc.h"
@@ -23,6 +23,18 @@ inline bool overlap(Range a, Range b) {
     if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
     return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
+}
+
+// Whether any of the outputs overlaps another output or an input.
+template <int NI, int NO>
+bool clash(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int o = 0; o < NO; ++o) {
+        for (int i = 0; i < NI; ++i)
+            if (overlap(out[o], in[i])) return true;
+        for (int q = o + 1; q < NO; ++q)
+            if (overlap(out[o], out[q])) return true;
+    }
+    return false;
 }
 
 // Keeps the error's text for ds4hc_last_hip_error() on this thread.

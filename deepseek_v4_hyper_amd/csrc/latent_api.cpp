@@ -12,6 +12,7 @@
 namespace {
 
 using ds4hc::aligned;
+using ds4hc::clash;
 using ds4hc::MAX_T;
 using ds4hc::overlap;
 using ds4hc::Range;
@@ -72,8 +73,8 @@ bool batch_arrays_ok(const ds4hc_paged_cache *c) {
            aligned(c->block_table, 4);
 }
 
-uint64_t cache_bytes(const ds4hc_paged_cache *c) {
-    return (uint64_t)c->n_pages * c->page_size * (c->d_latent + c->d_rope) * 2;
+uint64_t cache_bytes(const ds4hc_paged_cache *c, bool eight) {
+    return (uint64_t)c->n_pages * c->page_size * (eight ? DS4HC_LATENT8_ROW_BYTES(c->d_latent) : (c->d_latent + c->d_rope) * 2);
 }
 
 ds4hc::Paged view(const ds4hc_paged_cache *c) {
@@ -83,16 +84,71 @@ ds4hc::Paged view(const ds4hc_paged_cache *c) {
 
 ds4hc_status done(hipError_t e) { return e == hipSuccess ? DS4HC_OK : ds4hc::hip_fail(e); }
 
-// Whether any of the outputs overlaps another output or an input.
-template <int NI, int NO>
-bool clash(const Range (&in)[NI], const Range (&out)[NO]) {
-    for (int o = 0; o < NO; ++o) {
-        for (int i = 0; i < NI; ++i)
-            if (overlap(out[o], in[i])) return true;
-        for (int q = o + 1; q < NO; ++q)
-            if (overlap(out[o], out[q])) return true;
-    }
-    return false;
+ds4hc_status append(bool eight, const ds4hc_paged_cache *c, int64_t N, ds4hc_dtype src_dtype,
+                                 const void *kv, int64_t kv_stride, const float *norm_weight,
+                                 float rms_eps, const int64_t *positions, const double *inv_freq,
+                                 float amplitude, uint32_t flags, void *cache, hipStream_t stream) {
+    const ds4hc_status st = check_cache(c, N);
+    if (st != DS4HC_OK) return st;
+    if (!any_type(src_dtype) || (flags & ~DS4HC_ROPE_HALF) || !isfinite(amplitude) || !(rms_eps >= 0.f) ||
+        !isfinite(rms_eps))
+        return DS4HC_ERR_INVALID_ARG;
+    const int D = c->d_latent + c->d_rope, eb = elem_bytes(src_dtype);
+    if (kv_stride < D || kv_stride > MAX_STRIDE || kv_stride * eb % 16) return DS4HC_ERR_INVALID_ARG;
+    if (N == 0 || c->n_seqs == 0) return DS4HC_OK;
+    if (!batch_arrays_ok(c) || !kv || !positions || !inv_freq || !cache) return DS4HC_ERR_INVALID_ARG;
+    if (!aligned(kv, 16) || !aligned(cache, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8) ||
+        (norm_weight && !aligned(norm_weight, 4)))
+        return DS4HC_ERR_INVALID_ARG;
+    const uint64_t B = (uint64_t)c->n_seqs;
+    const Range in[] = {{kv, ((uint64_t)(N - 1) * kv_stride + D) * eb}, {norm_weight, (uint64_t)c->d_latent * 4},
+                        {positions, (uint64_t)N * 8}, {inv_freq, (uint64_t)c->d_rope * 4},
+                        {c->cu_q, (B + 1) * 4}, {c->kv_len, B * 4}, {c->block_table, B * c->max_pages * 4}};
+    const Range out[] = {{cache, cache_bytes(c, eight)}};
+    if (clash(in, out)) return DS4HC_ERR_INVALID_ARG;
+    const ds4hc::AppendArgs a{view(c), (int)c->dtype, c->d_latent, (int)src_dtype, N, kv, kv_stride, norm_weight,
+                              rms_eps, positions, inv_freq, amplitude, (flags & DS4HC_ROPE_HALF) != 0, cache, eight};
+    return done(ds4hc::launch_append(a, stream));
+}
+
+ds4hc_status attn(bool eight, const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
+                               const void *q_latent, ds4hc_strides ls, const void *q_rope,
+                               ds4hc_strides rs, const void *cache, const uint64_t *tree_mask,
+                               int32_t mask_words, void *out, ds4hc_strides os, float *lse_opt,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    const ds4hc_status st = check_cache(c, N);
+    if (st != DS4HC_OK) return st;
+    if (heads < 1 || !(scale > 0.f) || !isfinite(scale) || !strides_ok(ls) || !strides_ok(rs) || !strides_ok(os))
+        return DS4HC_ERR_INVALID_ARG;
+    if (tree_mask && mask_words < 1) return DS4HC_ERR_INVALID_ARG;
+    if (heads > MAX_HEADS || N * heads > MAX_ROWS || (tree_mask && mask_words > MAX_MASK_WORDS))
+        return DS4HC_ERR_UNSUPPORTED;
+    if (N == 0 || c->n_seqs == 0) return DS4HC_OK;
+    if (!batch_arrays_ok(c) || !q_latent || !q_rope || !cache || !out) return DS4HC_ERR_INVALID_ARG;
+    if (!rows_aligned16(q_latent, N, heads, ls, 2) || !rows_aligned16(q_rope, N, heads, rs, 2) ||
+        !rows_aligned16(out, N, heads, os, 2) || !aligned(cache, 16) || (lse_opt && !aligned(lse_opt, 4)) ||
+        (tree_mask && !aligned(tree_mask, 8)) || (workspace && !aligned(workspace, 16)))
+        return DS4HC_ERR_INVALID_ARG;
+    if (!rows_apart(N, heads, c->d_latent, os)) return DS4HC_ERR_INVALID_ARG;
+    const ds4hc::Paged v = view(c);
+    const uint64_t need = (eight ? ds4hc::attn8_workspace_bytes : ds4hc::attn_workspace_bytes)(v, c->d_latent, heads, N);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return DS4HC_ERR_INVALID_ARG;
+    const uint64_t B = (uint64_t)c->n_seqs;
+    const Range in[] = {{q_latent, span(N, heads, c->d_latent, ls, 2)}, {q_rope, span(N, heads, c->d_rope, rs, 2)},
+                        {cache, cache_bytes(c, eight)}, {tree_mask, (uint64_t)N * (tree_mask ? mask_words : 0) * 8},
+                        {c->cu_q, (B + 1) * 4}, {c->kv_len, B * 4}, {c->block_table, B * c->max_pages * 4}};
+    const Range outs[] = {{out, span(N, heads, c->d_latent, os, 2)}, {lse_opt, (uint64_t)N * heads * 4},
+                          {need ? workspace : nullptr, need}};
+    if (clash(in, outs)) return DS4HC_ERR_INVALID_ARG;
+    const ds4hc::AttnArgs a{v, (int)c->dtype, c->d_latent, heads, N, scale, q_latent, ls.token, ls.head,
+                            q_rope, rs.token, rs.head, cache, tree_mask, tree_mask ? mask_words : 0, out, os.token,
+                            os.head, lse_opt, workspace, 0};
+    return done(eight ? ds4hc::launch_attn8(a, stream) : ds4hc::launch_attn(a, stream));
+}
+
+size_t attn_workspace(bool eight, const ds4hc_paged_cache *c, int64_t N, int32_t heads) {
+    if (check_cache(c, N) != DS4HC_OK || heads < 1 || heads > MAX_HEADS || N * heads > MAX_ROWS || N == 0 || c->n_seqs == 0) return 0;
+    return (size_t)(eight ? ds4hc::attn8_workspace_bytes : ds4hc::attn_workspace_bytes)(view(c), c->d_latent, heads, N);
 }
 
 }  // namespace
@@ -155,27 +211,14 @@ ds4hc_status ds4hc_latent_append(const ds4hc_paged_cache *c, int64_t N, ds4hc_dt
                                  const void *kv, int64_t kv_stride, const float *norm_weight,
                                  float rms_eps, const int64_t *positions, const double *inv_freq,
                                  float amplitude, uint32_t flags, void *cache, hipStream_t stream) {
-    const ds4hc_status st = check_cache(c, N);
-    if (st != DS4HC_OK) return st;
-    if (!any_type(src_dtype) || (flags & ~DS4HC_ROPE_HALF) || !isfinite(amplitude) || !(rms_eps >= 0.f) ||
-        !isfinite(rms_eps))
-        return DS4HC_ERR_INVALID_ARG;
-    const int D = c->d_latent + c->d_rope, eb = elem_bytes(src_dtype);
-    if (kv_stride < D || kv_stride > MAX_STRIDE || kv_stride * eb % 16) return DS4HC_ERR_INVALID_ARG;
-    if (N == 0 || c->n_seqs == 0) return DS4HC_OK;
-    if (!batch_arrays_ok(c) || !kv || !positions || !inv_freq || !cache) return DS4HC_ERR_INVALID_ARG;
-    if (!aligned(kv, 16) || !aligned(cache, 16) || !aligned(positions, 8) || !aligned(inv_freq, 8) ||
-        (norm_weight && !aligned(norm_weight, 4)))
-        return DS4HC_ERR_INVALID_ARG;
-    const uint64_t B = (uint64_t)c->n_seqs;
-    const Range in[] = {{kv, ((uint64_t)(N - 1) * kv_stride + D) * eb}, {norm_weight, (uint64_t)c->d_latent * 4},
-                        {positions, (uint64_t)N * 8}, {inv_freq, (uint64_t)c->d_rope * 4},
-                        {c->cu_q, (B + 1) * 4}, {c->kv_len, B * 4}, {c->block_table, B * c->max_pages * 4}};
-    const Range out[] = {{cache, cache_bytes(c)}};
-    if (clash(in, out)) return DS4HC_ERR_INVALID_ARG;
-    const ds4hc::AppendArgs a{view(c), (int)c->dtype, c->d_latent, (int)src_dtype, N, kv, kv_stride, norm_weight,
-                              rms_eps, positions, inv_freq, amplitude, (flags & DS4HC_ROPE_HALF) != 0, cache};
-    return done(ds4hc::launch_append(a, stream));
+    return append(false, c, N, src_dtype, kv, kv_stride, norm_weight, rms_eps, positions, inv_freq, amplitude, flags, cache, stream);
+}
+
+ds4hc_status ds4hc_latent_append8(const ds4hc_paged_cache *c, int64_t N, ds4hc_dtype src_dtype,
+                                 const void *kv, int64_t kv_stride, const float *norm_weight,
+                                 float rms_eps, const int64_t *positions, const double *inv_freq,
+                                 float amplitude, uint32_t flags, void *cache, hipStream_t stream) {
+    return append(true, c, N, src_dtype, kv, kv_stride, norm_weight, rms_eps, positions, inv_freq, amplitude, flags, cache, stream);
 }
 
 ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
@@ -183,39 +226,25 @@ ds4hc_status ds4hc_latent_attn(const ds4hc_paged_cache *c, int64_t N, int32_t he
                                ds4hc_strides rs, const void *cache, const uint64_t *tree_mask,
                                int32_t mask_words, void *out, ds4hc_strides os, float *lse_opt,
                                void *workspace, size_t workspace_bytes, hipStream_t stream) {
-    const ds4hc_status st = check_cache(c, N);
-    if (st != DS4HC_OK) return st;
-    if (heads < 1 || !(scale > 0.f) || !isfinite(scale) || !strides_ok(ls) || !strides_ok(rs) || !strides_ok(os))
-        return DS4HC_ERR_INVALID_ARG;
-    if (tree_mask && mask_words < 1) return DS4HC_ERR_INVALID_ARG;
-    if (heads > MAX_HEADS || N * heads > MAX_ROWS || (tree_mask && mask_words > MAX_MASK_WORDS))
-        return DS4HC_ERR_UNSUPPORTED;
-    if (N == 0 || c->n_seqs == 0) return DS4HC_OK;
-    if (!batch_arrays_ok(c) || !q_latent || !q_rope || !cache || !out) return DS4HC_ERR_INVALID_ARG;
-    if (!rows_aligned16(q_latent, N, heads, ls, 2) || !rows_aligned16(q_rope, N, heads, rs, 2) ||
-        !rows_aligned16(out, N, heads, os, 2) || !aligned(cache, 16) || (lse_opt && !aligned(lse_opt, 4)) ||
-        (tree_mask && !aligned(tree_mask, 8)) || (workspace && !aligned(workspace, 16)))
-        return DS4HC_ERR_INVALID_ARG;
-    if (!rows_apart(N, heads, c->d_latent, os)) return DS4HC_ERR_INVALID_ARG;
-    const ds4hc::Paged v = view(c);
-    const uint64_t need = ds4hc::attn_workspace_bytes(v, c->d_latent, heads, N);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return DS4HC_ERR_INVALID_ARG;
-    const uint64_t B = (uint64_t)c->n_seqs;
-    const Range in[] = {{q_latent, span(N, heads, c->d_latent, ls, 2)}, {q_rope, span(N, heads, c->d_rope, rs, 2)},
-                        {cache, cache_bytes(c)}, {tree_mask, (uint64_t)N * (tree_mask ? mask_words : 0) * 8},
-                        {c->cu_q, (B + 1) * 4}, {c->kv_len, B * 4}, {c->block_table, B * c->max_pages * 4}};
-    const Range outs[] = {{out, span(N, heads, c->d_latent, os, 2)}, {lse_opt, (uint64_t)N * heads * 4},
-                          {need ? workspace : nullptr, need}};
-    if (clash(in, outs)) return DS4HC_ERR_INVALID_ARG;
-    const ds4hc::AttnArgs a{v, (int)c->dtype, c->d_latent, heads, N, scale, q_latent, ls.token, ls.head,
-                            q_rope, rs.token, rs.head, cache, tree_mask, tree_mask ? mask_words : 0, out, os.token,
-                            os.head, lse_opt, workspace, 0};
-    return done(ds4hc::launch_attn(a, stream));
+    return attn(false, c, N, heads, scale, q_latent, ls, q_rope, rs, cache, tree_mask, mask_words, out, os, lse_opt, workspace,
+                workspace_bytes, stream);
+}
+
+ds4hc_status ds4hc_latent_attn8(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
+                               const void *q_latent, ds4hc_strides ls, const void *q_rope,
+                               ds4hc_strides rs, const void *cache, const uint64_t *tree_mask,
+                               int32_t mask_words, void *out, ds4hc_strides os, float *lse_opt,
+                               void *workspace, size_t workspace_bytes, hipStream_t stream) {
+    return attn(true, c, N, heads, scale, q_latent, ls, q_rope, rs, cache, tree_mask, mask_words, out, os, lse_opt, workspace,
+                workspace_bytes, stream);
 }
 
 size_t ds4hc_latent_attn_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, int32_t heads) {
-    if (check_cache(c, N) != DS4HC_OK || heads < 1 || heads > MAX_HEADS || N * heads > MAX_ROWS || N == 0 || c->n_seqs == 0) return 0;
-    return (size_t)ds4hc::attn_workspace_bytes(view(c), c->d_latent, heads, N);
+    return attn_workspace(false, c, N, heads);
+}
+
+size_t ds4hc_latent_attn8_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, int32_t heads) {
+    return attn_workspace(true, c, N, heads);
 }
 
 ds4hc_status ds4hc_latent_prefill(int64_t N, int64_t S, int32_t n_seqs, int32_t heads,

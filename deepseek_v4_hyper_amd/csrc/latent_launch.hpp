@@ -1,6 +1,6 @@
 // latent_launch.hpp -- internal interface between the C ABI (latent_api.cpp)
 // and the kernels of an attention site (rope_kernels.hip, latent_attn.hip,
-// latent_prefill.hip). Arguments have been validated. Not part of the ABI.
+// latent_attn8.hip, latent_prefill.hip). Arguments have been validated. Not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -47,6 +47,7 @@ struct AppendArgs {
     float amplitude;
     bool half;
     void *cache;
+    bool eight;  // a cache of 8-bit latents
 };
 hipError_t launch_append(const AppendArgs &a, hipStream_t s);
 
@@ -68,6 +69,8 @@ struct AttnArgs {
     void *ws;
     int members;  // workgroups of a cluster: launch_attn sets it
 };
+uint64_t attn8_workspace_bytes(const Paged &c, int latent, int heads, int64_t N);
+hipError_t launch_attn8(const AttnArgs &a, hipStream_t s);  // cache rows of 8-bit latents
 uint64_t attn_workspace_bytes(const Paged &c, int latent, int heads, int64_t N);
 hipError_t launch_attn(const AttnArgs &a, hipStream_t s);
 

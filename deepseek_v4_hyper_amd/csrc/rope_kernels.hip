@@ -115,12 +115,34 @@ __device__ __forceinline__ int sequence_by_wave(const int32_t *cu, int n_seqs, i
     return found;
 }
 
+// A wave's row of E values a lane over its power of 2, the smallest that brings all of them to 448 at most, e4m3's
+// largest number; returns the scale byte. A row that holds a value that is not finite: NaN, and 255.
+template <int E> __device__ __forceinline__ int to_eight(float (&v)[E]) {
+    float top = 0.f;
+    bool finite = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        top = fmaxf(top, fabsf(v[e]));
+        finite &= isfinite(v[e]);
+    }
+    for (int m = 32; m; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+    const bool all_finite = __all(finite);
+    const uint32_t bits = __float_as_uint(top);  // 448 = 1.75 x 2^8
+    const int exponent = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0), scale = min(max(exponent, -117), 119);
+    const float inverse = __uint_as_float((uint32_t)(127 - scale) << 23);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = all_finite ? fminf(fmaxf(v[e] * inverse, -448.f), 448.f) : NAN;
+    return all_finite ? scale + 127 : 255;
+}
+
 // Bound by memory, and in small calls by the chain of loads (sequence, length, page) before the
 // first store, beside which the row's own loads run: 32 tokens 3.4 us; 4096 float32 rows of 576
 // 5.5 us (16 MB, 2.9 TB/s).
 // A wave a token: LATENT / 64 consecutive elements a lane, and a pair of the rope key for each
 // of the first 32 lanes. The row is read once, kept in registers over the sum of its squares.
-template <int SRC, int DT, int LATENT>
+// EIGHT: into a cache of 8-bit latents, where the row's largest magnitude, one more exchange over the
+// wave, gives its scale.
+template <int SRC, int DT, int LATENT, bool EIGHT>
 __global__ __launch_bounds__(64) void append_kernel(AppendArgs a) {
     constexpr int E = LATENT / 64, D = LATENT + LATENT_ROPE;
     const int t = blockIdx.x, lane = threadIdx.x, n = (int)a.N;
@@ -155,7 +177,7 @@ __global__ __launch_bounds__(64) void append_kernel(AppendArgs a) {
     if (j < 0) return;
     const int64_t row = cache_row(a.c, b, j);
     if (row < 0) return;
-    elem_t<DT> *y = static_cast<elem_t<DT> *>(a.cache) + row * D;
+    char *stored = static_cast<char *>(a.cache) + row * (EIGHT ? LATENT + LATENT_ROPE * 2 + 16 : D * 2);
     if (a.norm_weight) {
         float ss = 0.f;
 #pragma unroll
@@ -165,7 +187,20 @@ __global__ __launch_bounds__(64) void append_kernel(AppendArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] *= inv * w[e];
     }
-    if constexpr (E == 8) {
+    elem_t<DT> *y = reinterpret_cast<elem_t<DT> *>(stored), *rope = EIGHT ? reinterpret_cast<elem_t<DT> *>(stored + LATENT) : y + LATENT;
+    if constexpr (EIGHT) {
+        const int scale = to_eight<E>(v);
+        uint32_t w[(E + 3) / 4] = {};
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            if (e % 4 == 0) w[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(v[e], v[e + 1], w[e / 4], false);
+            else w[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(v[e], v[e + 1], w[e / 4], true);
+        }
+        if constexpr (E == 8) *reinterpret_cast<u32x2_t *>(stored + lane * E) = u32x2_t{w[0], w[1]};
+        else if constexpr (E == 4) *reinterpret_cast<uint32_t *>(stored + lane * E) = w[0];
+        else *reinterpret_cast<uint16_t *>(stored + lane * E) = (uint16_t)w[0];
+        if (lane == 63) *reinterpret_cast<u32x4_t *>(stored + LATENT + LATENT_ROPE * 2) = u32x4_t{(uint32_t)scale, 0, 0, 0};
+    } else if constexpr (E == 8) {
         Vec<DT> o;
 #pragma unroll
         for (int e = 0; e < E; ++e) o.f[e] = v[e];
@@ -179,10 +214,10 @@ __global__ __launch_bounds__(64) void append_kernel(AppendArgs a) {
         rope_angle(position, inv_freq, a.amplitude, c, s);
         turn<DT>(x0, x1, c, s);
         if (a.half) {
-            y[LATENT + i0] = elem_round<DT>(x0);
-            y[LATENT + i1] = elem_round<DT>(x1);
+            rope[i0] = elem_round<DT>(x0);
+            rope[i1] = elem_round<DT>(x1);
         } else {
-            *reinterpret_cast<uint32_t *>(y + LATENT + i0) = pack2<DT>(x0, x1);
+            *reinterpret_cast<uint32_t *>(rope + i0) = pack2<DT>(x0, x1);
         }
     }
 }
@@ -209,20 +244,20 @@ template <int DT> hipError_t launch_rope_of(const RopeArgs &a, hipStream_t s) {
                   : launch_kernel(rope_kernel<DT, false, false>, grid, dim3(THREADS), s, a);
 }
 
-template <int SRC, int DT> hipError_t launch_append_of(const AppendArgs &a, hipStream_t s) {
+template <int SRC, int DT, bool EIGHT> hipError_t launch_append_of(const AppendArgs &a, hipStream_t s) {
     const dim3 grid((unsigned)a.N);
     switch (a.latent) {
-    case 128: return launch_kernel(append_kernel<SRC, DT, 128>, grid, dim3(64), s, a);
-    case 256: return launch_kernel(append_kernel<SRC, DT, 256>, grid, dim3(64), s, a);
-    default: return launch_kernel(append_kernel<SRC, DT, 512>, grid, dim3(64), s, a);
+    case 128: return launch_kernel(append_kernel<SRC, DT, 128, EIGHT>, grid, dim3(64), s, a);
+    case 256: return launch_kernel(append_kernel<SRC, DT, 256, EIGHT>, grid, dim3(64), s, a);
+    default: return launch_kernel(append_kernel<SRC, DT, 512, EIGHT>, grid, dim3(64), s, a);
     }
 }
 
-template <int DT> hipError_t launch_append_to(const AppendArgs &a, hipStream_t s) {
+template <int DT, bool EIGHT> hipError_t launch_append_to(const AppendArgs &a, hipStream_t s) {
     switch (a.src_dt) {
-    case DT_F32: return launch_append_of<DT_F32, DT>(a, s);
-    case DT_BF16: return launch_append_of<DT_BF16, DT>(a, s);
-    default: return launch_append_of<DT_F16, DT>(a, s);
+    case DT_F32: return launch_append_of<DT_F32, DT, EIGHT>(a, s);
+    case DT_BF16: return launch_append_of<DT_BF16, DT, EIGHT>(a, s);
+    default: return launch_append_of<DT_F16, DT, EIGHT>(a, s);
     }
 }
 
@@ -237,7 +272,8 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_append(const AppendArgs &a, hipStream_t s) {
-    return a.dt == DT_BF16 ? launch_append_to<DT_BF16>(a, s) : launch_append_to<DT_F16>(a, s);
+    if (a.eight) return a.dt == DT_BF16 ? launch_append_to<DT_BF16, true>(a, s) : launch_append_to<DT_F16, true>(a, s);
+    return a.dt == DT_BF16 ? launch_append_to<DT_BF16, false>(a, s) : launch_append_to<DT_F16, false>(a, s);
 }
 
 }  // namespace ds4hc

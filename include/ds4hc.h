@@ -486,6 +486,195 @@ ds4hc_status ds4hc_latent_prefill(int64_t N, int64_t S, int32_t n_seqs, int32_t 
                                   const int32_t *cu_q, const int32_t *cu_k, void *out,
                                   float *lse_opt, hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The same cache with its latents in 8 bits (0.57 of the bytes at d_latent 512).
+ * It is [n_pages, page_size, DS4HC_LATENT8_ROW_BYTES(d_latent)] bytes, dense, on a 16-byte
+ * boundary; a token's row is
+ *   d_latent   e4m3 values c8 (sign, 4 bits of exponent, 3 of fraction; 0x7F and 0xFF are
+ *              NaN, there are no infinities)
+ *   64         rotated key, c->dtype (its values are few and larger than the latent's, and
+ *              rounding them to 8 bits would cost more than it saves)
+ *   1 byte s   the scale of this block of one token: its latent is c8 * 2^(s - 127)
+ *   15 bytes   zeros
+ * A block of several tokens would have to be rounded again whenever a later token of it is
+ * larger. The scale is a power of 2: finer ones gain nothing over e4m3's own exponents, and
+ * these leave every value exact in bfloat16. The descriptor is the same; its dtype is that
+ * of the rotated keys, the queries and the output.
+ */
+#define DS4HC_LATENT8_ROW_BYTES(d_latent) ((d_latent) + 144)
+
+/*
+ * ds4hc_latent_append8 -- ds4hc_latent_append into an 8-bit cache. With the normed latent c'
+ * in float32 and m its largest magnitude, e is the smallest integer with m <= 448 * 2^e,
+ * held to [-117, 119], c8 = c' * 2^-e rounded to nearest even (at most 448) and s = e + 127.
+ * A latent with a value that is not finite becomes NaN whole, with s = 255.
+ * All else as for ds4hc_latent_append.
+ */
+ds4hc_status ds4hc_latent_append8(const ds4hc_paged_cache *c, int64_t N, ds4hc_dtype src_dtype,
+                                  const void *kv, int64_t kv_stride, const float *norm_weight,
+                                  float rms_eps, const int64_t *positions, const double *inv_freq,
+                                  float amplitude, uint32_t flags, void *cache, hipStream_t stream);
+
+/*
+ * ds4hc_latent_attn8 -- ds4hc_latent_attn over an 8-bit cache: the same formulas, masks,
+ * lengths, workspace and limits, with c_j = c8 * 2^(s - 127). Scale bytes outside 10..246 are
+ * taken as the nearest of these, and 255 as a token that is NaN; a token with a NaN makes
+ * the rows that see it not finite, in some of their elements at least.
+ * Products are of 16-bit values (float16: as far as its range goes) and sums float32. The weight
+ * times the token's power of 2 is rounded to 16 bits for the second product.
+ */
+ds4hc_status ds4hc_latent_attn8(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
+                                const void *q_latent, ds4hc_strides q_latent_strides,
+                                const void *q_rope, ds4hc_strides q_rope_strides, const void *cache,
+                                const uint64_t *tree_mask, int32_t mask_words, void *out,
+                                ds4hc_strides out_strides, float *lse_opt, void *workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+size_t ds4hc_latent_attn8_workspace_bytes(const ds4hc_paged_cache *c, int64_t N, int32_t heads);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the attention of drafted tokens: which of them stay, where they lie, and the
+ * pages that hold them. One step of a serving program with drafts is
+ *   ds4hc_pages_resize (room for the drafts), per layer an append and an attention,
+ *   ds4hc_draft_verify, ds4hc_cache_compact (trees), ds4hc_pages_resize (what was accepted),
+ * all on one stream and without a look at the results on the host. What device arrays hold
+ * is checked in the kernels, as above: no value in them makes a kernel read or write outside
+ * the arrays given.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Tokens of a sequence that ds4hc_draft_verify looks at: those behind are not accepted. */
+#define DS4HC_VERIFY_MAX_TOKENS 1024
+
+/*
+ * ds4hc_draft_verify -- speculative sampling: which drafted tokens are kept, and the token that
+ * follows them, so that the tokens are distributed as if drawn from the target one by one.
+ * Sequence b has tokens cu_q[b] .. cu_q[b + 1] - 1 of the call's N. Its first is the root, a
+ * token that is accepted already; the others are drafted, each the child of an earlier one.
+ * Row t of `target` is the target's distribution p of the token that follows token t.
+ *   chain (parents NULL): the child of token i is token i + 1. With `draft`, row t of which is
+ *     the distribution q that token t + 1 was drawn from, token x is accepted if
+ *     u * q(x) < p(x); the first that is not ends the path, and the next token is drawn from
+ *     max(p - q, 0) of the row before it; if all are accepted, from p of the last row.
+ *   trees, and chains without draft: the children of an accepted token are tried in their order;
+ *     one with token x is accepted if u * (1 - sum) < p(x), where sum is of the p of those tried
+ *     before it. If none is, the next token is drawn from p without the tokens tried.
+ *     (Right for any drafted tokens, drawn or chosen. A token tried before, again among the
+ *     children of one token, is not accepted.)
+ * u is uniform[t] of the drafted token t; uniform[t] of the root draws the next token: the smallest
+ * x whose sum of weights up to and with x is above uniform[t] * their total. If all weights are
+ * 0 (the two distributions are equal but for rounding), they are p's of that row.
+ * Products, sums and comparisons are of 64 bits, in a fixed order. Rows need not sum to 1
+ * exactly; weights that are negative or not finite count as 0, and a token outside [0, vocab) is
+ * not accepted. Random numbers are in [0, 1); others are taken as the nearest of these (NaN: 0).
+ *   target   [N, vocab] float32, target_stride elements between rows (read: the rows that are
+ *            reached, and of the others single elements)
+ *   draft    [N, vocab] float32, draft_stride between rows, or NULL (with parents: must be NULL)
+ *   tokens   [N] int64, parents [N] int32 or NULL: index of the parent among the sequence's
+ *            tokens, smaller than the token's own (others: never accepted; the root's is not read)
+ *   cu_q     [n_seqs + 1] int32, uniform [N] float32 (read)
+ *   path     [N] int32 (written): entries cu_q[b] .. : the accepted tokens' indices among the
+ *            sequence's, the root's 0 first, then -1. As `keep` for ds4hc_cache_compact.
+ *   n_kept   [n_seqs] int32 (written): their number, the root's included (0: no token)
+ *   next     [n_seqs] int64 (written): the token that follows the last of them (-1: no token, or
+ *            a row without a weight)
+ *   workspace of ds4hc_draft_verify_workspace_bytes(n_seqs, vocab) bytes, 16-byte aligned
+ * vocab 1..2^24, N <= 2^24, n_seqs <= 65535.
+ */
+ds4hc_status ds4hc_draft_verify(int64_t N, int32_t n_seqs, int32_t vocab, const float *target,
+                                int64_t target_stride, const float *draft, int64_t draft_stride,
+                                const int64_t *tokens, const int32_t *parents, const int32_t *cu_q,
+                                const float *uniform, int32_t *path, int32_t *n_kept, int64_t *next,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream);
+size_t ds4hc_draft_verify_workspace_bytes(int32_t n_seqs, int32_t vocab);
+
+/* Paged caches of all layers, of any kind: layer l's is at data + l * layer_stride, dense
+ * [n_pages, page_size] rows of row_bytes bytes. */
+typedef struct {
+    int32_t layers;       /* 1..65535 */
+    int32_t page_size;    /* tokens a page: a power of two, 1..65536 */
+    int64_t n_pages;      /* >= 1; n_pages * page_size < 2^31 */
+    int64_t row_bytes;    /* a multiple of 16, 16..65536 */
+    int64_t layer_stride; /* bytes, a multiple of 16, not less than a layer's (one layer: any) */
+    void *data;           /* 16-byte aligned */
+} ds4hc_page_store;
+
+/*
+ * ds4hc_cache_compact -- moves accepted tokens to their places: in every layer, for sequence b
+ * and i < n_keep[b], the row of the call's token keep[cu_q[b] + i] of b goes to the place of the
+ * call's token i of b (token i of the call's q_len for b is token kv_len[b] - q_len + i of b).
+ * keep[cu_q[b]] .. must rise strictly; entries outside [0, q_len) and places that are not in the
+ * cache are passed over. Sequences whose pages are written may share none of them.
+ *   cu_q [n_seqs + 1], kv_len [n_seqs], block_table [n_seqs, max_pages], keep [N],
+ *   n_keep [n_seqs] int32 (read). N <= 2^24, n_seqs <= 65535, max_pages as for ds4hc_paged_cache.
+ */
+ds4hc_status ds4hc_cache_compact(const ds4hc_page_store *s, int64_t N, int32_t n_seqs,
+                                 int32_t max_pages, const int32_t *cu_q, const int32_t *kv_len,
+                                 const int32_t *block_table, const int32_t *keep,
+                                 const int32_t *n_keep, hipStream_t stream);
+
+/*
+ * ds4hc_pages_copy -- copies whole pages, in every layer: pairs[i] = (from, to), for i < n. Pairs
+ * with an entry outside [0, n_pages) are passed over, as those that ds4hc_pages_resize gives where
+ * nothing is to be copied. No page may be written twice, or written and read.
+ *   pairs [n, 2] int32 (read), n <= 2^20.
+ */
+ds4hc_status ds4hc_pages_copy(const ds4hc_page_store *s, int64_t n, const int32_t *pairs,
+                              hipStream_t stream);
+
+/* Who has which page: sequences in slots, with a row of the block table and a length each, and
+ * for every page the number of entries that name it (0: free). All three are the caller's; to
+ * begin with, refs and kv_len are 0 and the table's entries -1. */
+typedef struct {
+    int32_t page_size;    /* tokens a page: a power of two, 1..65536 */
+    int32_t n_slots;      /* >= 1, <= 2^20 */
+    int32_t max_pages;    /* >= 1; max_pages * page_size <= 2^30 */
+    int32_t n_pages;      /* >= 1, <= 2^28 */
+    int32_t *block_table; /* [n_slots, max_pages] */
+    int32_t *kv_len;      /* [n_slots] */
+    int32_t *refs;        /* [n_pages] */
+} ds4hc_page_pool;
+
+/* What became of an item: */
+#define DS4HC_PAGES_DONE 0
+#define DS4HC_PAGES_SHORT 1   /* too few free pages: left as it was */
+#define DS4HC_PAGES_INVALID 2 /* left as it was: see there */
+
+/*
+ * ds4hc_pages_resize -- new lengths for n of the slots. A slot that needs fewer pages gives those
+ * behind up: their entries become -1 and their counts fall by one. One that needs more takes free
+ * pages. Where it grows and its last page is filled in part and counted more than once, so that
+ * the tokens to come would be written into a page that others have too, it gets a page of its
+ * own in that one's place, and copies[i] = (that page, the new one) for ds4hc_pages_copy, which is to
+ * run before anything else is written to the pool (copies[i] = (-1, -1): nothing to copy).
+ * Free pages are those whose count is 0 when the call begins, and are taken in ascending order, by
+ * the items in their order. Items that would need more than there are when all before them had got
+ * theirs are DS4HC_PAGES_SHORT. DS4HC_PAGES_INVALID: a slot outside [0, n_slots), one that an
+ * earlier item has, a length outside [0, max_pages * page_size].
+ *   slots [n], lengths [n] int32 (read), copies [n, 2], status [n] int32 (written)
+ *   workspace of ds4hc_pages_workspace_bytes(p, n) bytes, 16-byte aligned. n <= 2^20.
+ */
+ds4hc_status ds4hc_pages_resize(const ds4hc_page_pool *p, int64_t n, const int32_t *slots,
+                                const int32_t *lengths, int32_t *copies, int32_t *status,
+                                void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * ds4hc_pages_fork -- slot children[i] becomes a copy of slot parents[i]: its length and entries,
+ * the counts of whose pages rise by one. No page is copied: the next ds4hc_pages_resize that grows
+ * one of them finds the shared last page. DS4HC_PAGES_INVALID: a slot outside [0, n_slots), a child
+ * that is its parent, that an earlier item has, or whose length is not 0. Lengths are those when
+ * the call begins.
+ *   parents [n], children [n] int32 (read), status [n] int32 (written), workspace as above.
+ */
+ds4hc_status ds4hc_pages_fork(const ds4hc_page_pool *p, int64_t n, const int32_t *parents,
+                              const int32_t *children, int32_t *status, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* Workspace bytes of ds4hc_pages_resize and ds4hc_pages_fork. Looks at the host fields alone; 0
+ * for invalid arguments and n = 0. */
+size_t ds4hc_pages_workspace_bytes(const ds4hc_page_pool *p, int64_t n);
+
 /* Static, human-readable name of a status code. */
 const char *ds4hc_status_string(ds4hc_status s);
 
