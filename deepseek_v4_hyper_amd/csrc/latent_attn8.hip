@@ -16,22 +16,29 @@ namespace {
 
 template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape8 {
     static constexpr int LATENT = LATENT_, ROW_WAVES = ROW_WAVES_, SETS = SETS_;
-    static constexpr int TOKENS = 64, BUFS = 2, STEPS = TOKENS / SETS / 32;
+    static constexpr int TOKENS = 64, BUFS = 3, STEPS = TOKENS / SETS / 32;
     static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int ROWS = ROW_WAVES * 32;
     static constexpr int ROW_BYTES = LATENT, CHUNKS = ROW_BYTES / 16;  // a token's latent in LDS
+    // a wave loads the tokens of its GROUPS groups of 16, which lie in one page each unless pages are smaller
+    static constexpr int OWN = TOKENS / WAVES, GROUPS = OWN / 16;
     static constexpr int ROPE_AT = TOKENS * ROW_BYTES, SCALE_AT = ROPE_AT + TOKENS * LATENT_ROPE * 2;
-    static constexpr int TILE_BYTES = SCALE_AT + TOKENS * 16;
+    static constexpr int TILE_BYTES = SCALE_AT + TOKENS * 64;  // (scales: a group's 16 bytes a token, 1024 bytes on)
     static constexpr int ROWS_A_LOAD = 1024 / ROW_BYTES;
-    static constexpr int OWN_LATENT = TOKENS / ROWS_A_LOAD / WAVES, OWN_ROPE = TOKENS / 8 / WAVES;
-    static constexpr int LOADS = OWN_LATENT + OWN_ROPE + 1;  // of a wave and tile; the last, of the scales, is one wave's
+    static constexpr int LOADS_LATENT = 16 / ROWS_A_LOAD, LOADS_GROUP = LOADS_LATENT + 2 + 1, LOADS = GROUPS * LOADS_GROUP;  // of a wave and tile
     static constexpr int KLATENT = LATENT / 16, KSTEPS = KLATENT + LATENT_ROPE / 16, DBLOCKS = LATENT / 32;
     // of the output, that a wave finishes, and what it takes to store them (with two sets: to give them away)
     static constexpr int BLOCKS = DBLOCKS / SETS, BLOCK_BYTES = 16 * 64 * 4;
     static constexpr int END_BYTES = SETS == 1 ? WAVES * 32 * BLOCKS * 64 : WAVES * (BLOCKS * BLOCK_BYTES + 384);
     static constexpr int RING_BYTES = BUFS * TILE_BYTES > END_BYTES ? BUFS * TILE_BYTES : END_BYTES;
-    static_assert(OWN_LATENT * ROWS_A_LOAD * WAVES == TOKENS && OWN_ROPE * 8 * WAVES == TOKENS, "the waves load alike");
+    static_assert(GROUPS * 16 * WAVES == TOKENS && LOADS_LATENT * ROWS_A_LOAD == 16, "the waves load alike");
 };
+
+// f(0) .. f(N - 1), each with its number as a constant.
+template <int... I, class F> __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F &&f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F> __device__ __forceinline__ void for_each(F &&f) { each_of(std::make_integer_sequence<int, N>{}, f); }
 
 // Swizzle: 16-byte chunk c of token row r lies at chunk c ^ swz8(r) of the row's place in LDS. A read of the
 // first product takes the same chunk of 16 rows, 256 bytes: swz8 takes 16 values over 16 rows (rows of 128
@@ -81,16 +88,77 @@ __device__ __forceinline__ u32x2_t lds_read_tr8(const DS4HC_LDS char *p) {
     return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr8_b64_v2i32((DS4HC_LDS i32x2_t *)p));
 }
 
+// 16 bytes a lane, at `voffset` + `soffset` from a buffer's base, to LDS byte lds + 16 * lane; zeros behind the buffer's
+// end. Counted like load_to_lds16, of which it saves the address arithmetic of 64 bits. Wait states: one after
+// a write of m0.
+typedef uint32_t buffer_t __attribute__((ext_vector_type(4)));
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void buffer_to_lds16(uint32_t voffset, buffer_t buffer, int soffset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(lds), "v"(voffset), "s"(buffer), "s"(soffset)
+                 : "m0", "memory");
+}
+#pragma clang diagnostic pop
+
+// LDS byte of token r's scale word in a tile.
+template <class S> __device__ __forceinline__ uint32_t scale_at(int r) { return S::SCALE_AT + (r >> 4) * 1024 + (r & 15) * 16; }
+
 // Not 0 if one of 16 e4m3 values is NaN (all bits but the sign set; there are no infinities).
 __device__ __forceinline__ uint32_t nan_bits8(u32x4_t w) {
     constexpr uint32_t REST = 0x7F7F7F7Fu, ONE = 0x01010101u;
     return (((w.x & REST) + ONE) | ((w.y & REST) + ONE) | ((w.z & REST) + ONE) | ((w.w & REST) + ONE)) & ~REST;
 }
 
-template <int DT, class S>
+// ------------------------------------------------------------------ products of 8-bit values
+//
+// C[32 x 32] += A[32 x 64] B[64 x 32] of e4m3 values at twice the rate of 16-bit ones, each block of 32 along k
+// times a power of 2 of its row (A) or column (B). Lane l holds row or column l % 32; its bytes 0 .. 15 are of the
+// first block, whose power is that of the lane below 32, its bytes 16 .. 31 of the second, lanes from 32.
+// What a bfloat16 number has, 8 bits, two e4m3 numbers have together: x = hi + lo, where lo is hi's rounding error
+// exactly, if it is given a scale 2^-4 of hi's. So queries and weights go in as two numbers, at the rate of one
+// 16-bit product, and the cache's values as they are. Of a product's 64 terms those below 2^-13 of the largest
+// are cut off there by the matrix unit (measured: 2^-18 of the sum of magnitudes on average over normal values).
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef short s16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+
+// With C in vector registers, as mfma32_v; the wait for its results is that of the last instruction of a chain.
+__device__ __forceinline__ void mfma64_first_v(i32x8_t a, i32x8_t b, acc16_t &c, int scale_a, int scale_b) {
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]" : "=&v"(c) : "v"(a), "v"(b), "v"(scale_a), "v"(scale_b));
+}
+__device__ __forceinline__ void mfma64_v(i32x8_t a, i32x8_t b, acc16_t &c, int scale_a, int scale_b) {
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]" : "+&v"(c) : "v"(a), "v"(b), "v"(scale_a), "v"(scale_b));
+}
+__device__ __forceinline__ acc16_t mfma64(i32x8_t a, i32x8_t b, acc16_t c, int scale_a, int scale_b) {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, scale_a, 0, scale_b);
+}
+__device__ __forceinline__ i32x8_t join8(u32x4_t a, u32x4_t b) { return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w}; }
+
+// Scale byte that brings magnitudes up to `top` below 256 (with one 4 lower for what the rounding leaves), and its power.
+__device__ __forceinline__ int split_scale(float top) { return min(max((int)(__float_as_uint(top) >> 23) - 7, 5), 254); }
+__device__ __forceinline__ float power_of(int scale) { return __uint_as_float((uint32_t)scale << 23); }
+
+// Four numbers as hi and lo, a word each.
+__device__ __forceinline__ void split4(float a, float b, float c, float d, int scale, uint32_t &hi, uint32_t &lo) {
+    const float up = power_of(scale), down = power_of(scale - 4);
+    s16x2_t h = {0, 0}, l = {0, 0};
+    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, a, b, up, false);
+    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, c, d, up, true);
+    hi = __builtin_bit_cast(uint32_t, h);
+    const f32x2_t ab = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, up, false), cd = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, up, true);
+    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, a - ab.x, b - ab.y, down, false);
+    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, c - cd.x, d - cd.y, down, true);
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+
+// SMALL: pages of fewer than 16 tokens, whose rows are looked up one by one.
+template <int DT, class S, bool SMALL>
 __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
     __shared__ __align__(256) char ring[S::RING_BYTES];
     __shared__ uint32_t not_finite[2];
+    __shared__ __align__(16) u32x4_t rope_queries[S::WAVES][LATENT_ROPE / 16][64];  // (no registers are left for them)
     __shared__ __align__(16) float units[S::WAVES][S::TOKENS];  // the tile's powers of 2, each wave's own copy
     __shared__ __align__(16) float powers[DT == DT_F16 ? S::WAVES : 1][S::TOKENS];  // their exponents
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
@@ -148,16 +216,48 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         // steps 2 j and 2 j + 1, the others those behind: what a read of 16 bytes of a cached row gives.
         const int row0 = row_tile * S::ROWS + row_wave * 32;
         const int tok = min(row0 + (lane & 31), n_rows - 1) / a.heads;  // rows behind the last repeat it
-        u32x4_t q[S::KSTEPS];
+        // (8-bit products: lanes below 32 hold channels 64 k .. 64 k + 31 of step k as hi (q[4 k], q[4 k + 1]) and lo.)
+        constexpr bool EIGHT = DT == DT_BF16;
+        u32x4_t q[S::KLATENT];
+        int scale_hi = 0, scale_lo = 0;
         auto load_queries = [&]() {
             const int head = min(row0 + (lane & 31), n_rows - 1) - tok * a.heads;
             const elem_t<DT> *ql = static_cast<const elem_t<DT> *>(a.ql) + (int64_t)(q0 + tok) * a.ql_token + head * a.ql_head + (lane >> 5) * 16;
             const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head + (lane >> 5) * 8;
 #pragma unroll
-            for (int k = 0; k < S::KSTEPS; ++k)
-                q[k] = *reinterpret_cast<const u32x4_t *>(k < S::KLATENT ? ql + (k >> 1) * 32 + (k & 1) * 8 : qr + (k - S::KLATENT) * 16);
+            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane] = *reinterpret_cast<const u32x4_t *>(qr + k * 16);
 #pragma unroll
-            for (int k = 0; k < S::KSTEPS; ++k) loaded(q[k]);
+            for (int k = 0; k < S::KLATENT; ++k)
+                q[k] = *reinterpret_cast<const u32x4_t *>(EIGHT ? ql + (lane >> 5) * 16 + (k >> 2) * 64 + (k & 3) * 8 : ql + (k >> 1) * 32 + (k & 1) * 8);
+#pragma unroll
+            for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);
+            if constexpr (EIGHT) {
+                float most = 0.f;
+#pragma unroll
+                for (int k = 0; k < S::KLATENT; ++k)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(bf16_lo(q[k][i])), fabsf(bf16_hi(q[k][i]))));
+#pragma unroll
+                for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);  // (as new: the numbers above are not kept for what follows)
+                scale_hi = split_scale(max_halves(most));
+                scale_lo = scale_hi - 4;
+#pragma unroll
+                for (int k = 0; k < S::KLATENT; k += 4) {
+                    u32x4_t hi[2], lo[2];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t w0 = q[k + i / 2][2 * (i & 1)], w1 = q[k + i / 2][2 * (i & 1) + 1];
+                        uint32_t h, l;
+                        split4(bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1), scale_hi, h, l);
+                        hi[i / 4][i & 3] = h;
+                        lo[i / 4][i & 3] = l;
+                    }
+                    q[k] = hi[0];
+                    q[k + 1] = hi[1];
+                    q[k + 2] = lo[0];
+                    q[k + 3] = lo[1];
+                }
+            }
         };
         float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
         float sum = 0.f;                    // of the weights
@@ -172,9 +272,16 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         // block table is read once for many tiles and its latency is not a tile's.
         const int e_shift = max(__builtin_ctz(S::TOKENS) - a.c.page_shift, 0);
         int pages = -1, pages_from = t_first - 64;
-        // Cache rows of a tile's tokens, lane r that of token r (-1: not in the cache, or behind the end).
+        // Where a tile's tokens lie, and which of them are in the cache. A token that is not there takes a place in the
+        // cache all the same (of its page, if that is there, else of page 0), whose bytes do not count.
+        struct Where {
+            int row;            // SMALL: of the lane's token
+            int first[S::GROUPS];  // else: of the wave's groups
+            uint64_t ok;
+        };
         auto look_up = [&](int tile) {
-            if (tile >= t_first + n) return -1;
+            Where w = {};
+            if (tile >= t_first + n) return w;
             if (tile - pages_from >= 64 >> e_shift) {
                 pages_from = tile;
                 const int e = lane_here(), in_tile = e >> e_shift;
@@ -184,120 +291,233 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 if (pages >= a.c.n_pages) pages = -1;
                 loaded(pages);
             }
-            const int r = lane_here() & (S::TOKENS - 1), j = tile * S::TOKENS + r;
-            const int page = from_lane(pages, ((tile - pages_from) << e_shift) + (e_shift ? r >> a.c.page_shift : 0));
-            return page < 0 || j >= sq.len ? -1 : (page << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
-        };
-        // Tokens that are not there get the data of one that is (their places may hold anything, also NaN, which a
-        // weight of 0 would not hide). Which tokens are there, a bit each:
-        auto present = [&](int &rows) -> uint64_t {
-            const uint64_t ok = __ballot(rows >= 0);
-            const int one = __builtin_amdgcn_readlane(rows, __builtin_ctzll(ok | 1ull << 63));
-            rows = rows >= 0 ? rows : one >= 0 ? one : 0;  // (none is there: row 0; nothing sees it)
-            return ok;
-        };
-        // The wave's load number i of the tile to `buf`; lane r of `rows` has token r's cache row.
-        auto load = [&](int i, int rows, uint32_t l, uint32_t buf, uint64_t lanes) {
-            auto of_row = [&](int r) { return cache + (uint64_t)(uint32_t)from_lane(rows, r) * STRIDE; };
-            if (i < S::OWN_LATENT) {
-                const int r0 = (wave * S::OWN_LATENT + i) * S::ROWS_A_LOAD, r = r0 + l / S::CHUNKS, c = l % S::CHUNKS;
-                load_to_lds16(of_row(r) + ((c ^ swz8<S::CHUNKS>(r)) << 4), buf + r0 * S::ROW_BYTES, lanes);
-            } else if (i < S::OWN_LATENT + S::OWN_ROPE) {
-                const int r0 = (wave * S::OWN_ROPE + i - S::OWN_LATENT) * 8, r = r0 + l / 8, c = l % 8;
-                load_to_lds16(of_row(r) + S::LATENT + ((c ^ swz8_rope(r)) << 4), buf + S::ROPE_AT + r0 * 128, lanes);
+            const int e0 = (tile - pages_from) << e_shift, in_page = (1 << a.c.page_shift) - 1, left_over = sq.len - tile * S::TOKENS;
+            if constexpr (SMALL) {
+                const int r = lane_here(), page = from_lane(pages, e0 + (r >> a.c.page_shift));
+                w.row = (max(page, 0) << a.c.page_shift) + (r & in_page);
+                w.ok = __ballot(page >= 0 && r < left_over);
             } else {
-                load_to_lds16(of_row(l) + S::LATENT + LATENT_ROPE * 2, buf + S::SCALE_AT, (uint64_t)uniform((int64_t)(wave == 0 ? lanes : 0)));
+#pragma unroll
+                for (int g = 0; g < S::GROUPS; ++g) {
+                    const int o = wave * S::OWN + g * 16;
+                    const int page = __builtin_amdgcn_readlane(pages, e0 + (e_shift ? o >> a.c.page_shift : 0));
+                    w.first[g] = (max(page, 0) << a.c.page_shift) + ((tile * S::TOKENS + o) & in_page);
+                }
+                w.ok = ~0ull;
+                const uint64_t there = __ballot(pages >= 0) >> e0;
+                const int entries = 1 << e_shift, each = S::TOKENS >> e_shift;
+                for (int k = 0; k < entries; ++k)
+                    if (!((there >> k) & 1)) w.ok &= ~((~0ull >> (64 - each)) << (k * each));
+                if (left_over < 64) w.ok &= (1ull << max(left_over, 0)) - 1;
+            }
+            return w;
+        };
+        // What a lane's places in the loads have alike: the chunk, swizzled, and the row, of the latents and of the rotated keys.
+        struct Place {
+            uint32_t chunk, row, rope_chunk, rope_row, scale;
+            uint32_t to, to_rope, to_scale;  // the wave's places in LDS
+        };
+        auto place = [&](uint32_t buf) {
+            const uint32_t l = lane_here();
+            uint32_t to = buf + wave * (S::OWN * S::ROW_BYTES), to_rope = buf + S::ROPE_AT + wave * (S::OWN * 128), to_scale = buf + S::SCALE_AT + wave * (S::OWN * 64);
+            asm volatile("" : "+s"(to), "+s"(to_rope), "+s"(to_scale));  // (not one register for every load)
+            return Place{((l % S::CHUNKS) ^ swz8<S::CHUNKS>(l / S::CHUNKS)) << 4, l / S::CHUNKS * STRIDE, ((l % 8) ^ swz8_rope(l / 8)) << 4, l / 8 * STRIDE,
+                         (l & 15) * STRIDE, to, to_rope, to_scale};
+        };
+        // The wave's load number i of the tile to LDS at `buf`. Rows of a group lie one behind another.
+        auto load = [&](int i, const Where &w, const buffer_t (&buffers)[S::GROUPS], const Place &x) {
+            const int g = i / S::LOADS_GROUP, k = i % S::LOADS_GROUP, r0 = wave * S::OWN + g * 16;
+            const uint32_t to = k < S::LOADS_LATENT ? x.to + (g * 16 + k * S::ROWS_A_LOAD) * S::ROW_BYTES
+                              : k < S::LOADS_LATENT + 2 ? x.to_rope + (g * 16 + (k - S::LOADS_LATENT) * 8) * 128 : x.to_scale + g * 1024;
+            if constexpr (SMALL) {
+                const uint32_t l = lane_here();
+                auto of_row = [&](int r) { return cache + (uint64_t)(uint32_t)from_lane(w.row, r) * STRIDE; };
+                if (k < S::LOADS_LATENT) {
+                    const int r = r0 + k * S::ROWS_A_LOAD + l / S::CHUNKS, c = l % S::CHUNKS;
+                    load_to_lds16(of_row(r) + ((c ^ swz8<S::CHUNKS>(r)) << 4), to, ~0ull);
+                } else if (k < S::LOADS_LATENT + 2) {
+                    const int at = r0 + (k - S::LOADS_LATENT) * 8, r = at + l / 8, c = l % 8;
+                    load_to_lds16(of_row(r) + S::LATENT + ((c ^ swz8_rope(r)) << 4), to, ~0ull);
+                } else {
+                    load_to_lds16(of_row(r0 + (l & 15)) + S::LATENT + LATENT_ROPE * 2, to, ~0ull);
+                }
+            } else if (k < S::LOADS_LATENT) {
+                buffer_to_lds16((x.chunk ^ (swz8<S::CHUNKS>(k * S::ROWS_A_LOAD) << 4)) + x.row, buffers[g], k * S::ROWS_A_LOAD * STRIDE, to);
+            } else if (k < S::LOADS_LATENT + 2) {
+                const int half = k - S::LOADS_LATENT;
+                buffer_to_lds16((x.rope_chunk ^ (swz8_rope(half * 8) << 4)) + x.rope_row, buffers[g], half * 8 * STRIDE + S::LATENT, to);
+            } else {
+                buffer_to_lds16(x.scale, buffers[g], S::LATENT + LATENT_ROPE * 2, to);
+            }
+        };
+        // The groups' rows as buffers; without an end where there is no tile to load.
+        auto buffers_of = [&](const Where &w, bool any, buffer_t (&buffers)[S::GROUPS]) {
+#pragma unroll
+            for (int g = 0; g < S::GROUPS; ++g) {
+                const uint64_t at = (uint64_t)cache + (uint64_t)(uint32_t)w.first[g] * STRIDE;
+                buffers[g] = {(uint32_t)uniform((int)(uint32_t)at), (uint32_t)uniform((int)(at >> 32)), (uint32_t)uniform(any ? 16 * STRIDE : 0), 0x00020000u};
+                // (a load may read scalar registers 5 wait states after the vector unit wrote them)
+                asm volatile("s_nop 4" : "+s"(buffers[g]));
             }
         };
 
-        // Tile t (tokens `ok`) in LDS at `at`, and the loads of the next one, if there is one, beside it.
-        auto tile = [&](int t, uint64_t ok, uint32_t at, int rows, uint32_t at_next) {
+        // Tile t (tokens `ok`) in LDS at `at`, and the loads of the one BUFS - 1 further on, if there is one, beside it.
+        auto tile = [&](int t, uint64_t ok, uint32_t at, const Where &next, uint32_t at_next) {
             DS4HC_LDS char *buf = (DS4HC_LDS char *)(uintptr_t)at;
-            DS4HC_LDS uint32_t *scales = (DS4HC_LDS uint32_t *)(uintptr_t)(at + S::SCALE_AT);  // (token r's: element 4 r, its lowest byte)
+            auto scale_of_token = [&](int r) -> DS4HC_LDS uint32_t & { return *(DS4HC_LDS uint32_t *)(buf + scale_at<S>(r)); };
             const int j0 = t * S::TOKENS;
             const bool masked = ok != ~0ull || j0 + S::TOKENS > (a.tree_mask ? context : context + 1);
             uint64_t bad = 0;  // tokens that hold a value that is not finite
             if (masked) {  // the same in all waves
-                // Only what some rows see and others do not has to be looked at: the call's own tokens,
-                // and the copies in place of tokens that are not there, if it is one of those they copy. (A
-                // copy of a context token is seen, as that token, by all.) If none of the tile's tokens is
-                // there, they copy the cache's first row, which may be nobody's and is seen by none.
-                const int own = ok ? context - j0 : 0, copied = ok ? __builtin_ctzll(ok) : 0;
-                const int lo = copied >= own ? 0 : own, hi = copied >= own ? S::TOKENS : min(S::TOKENS, sq.len - j0);
+                // Tokens that are not there become zeros, so that what lies in their places meets no weight of 0. Of
+                // the others only what some rows see and others do not has to be looked at: the call's own tokens.
+                const int lo = max(context - j0, 0), hi = min(S::TOKENS, sq.len - j0);
+                auto clear = [&](int i) {
+                    const uint32_t zero = here(0);
+                    *reinterpret_cast<DS4HC_LDS u32x4_t *>(buf + i * 16) = u32x4_t{zero, zero, zero, zero};
+                    if (i % S::CHUNKS == 0) scale_of_token(i / S::CHUNKS) = 127;
+                };
                 if (threadIdx.x < 2) not_finite[threadIdx.x] = 0;
                 wait_and_barrier<63>();
+                if (~ok)
+                    for (int i = threadIdx.x; i < S::TOKENS * S::CHUNKS; i += S::THREADS)
+                        if (!((ok >> (i / S::CHUNKS)) & 1)) clear(i);
                 for (int i = lo * S::CHUNKS + threadIdx.x; i < hi * S::CHUNKS; i += S::THREADS)
-                    if (nan_bits8(lds_read16(buf + i * 16)) || scale_is_nan(scales[i / S::CHUNKS * 4]))
+                    if (((ok >> (i / S::CHUNKS)) & 1) && (nan_bits8(lds_read16(buf + i * 16)) || scale_is_nan(scale_of_token(i / S::CHUNKS))))
                         atomicOr(&not_finite[(i / S::CHUNKS) >> 5], 1u << ((i / S::CHUNKS) & 31));
                 wait_and_barrier<63>();
                 bad = ((uint64_t)uniform((int)not_finite[1]) << 32) | (uint32_t)uniform((int)not_finite[0]);
-                if (bad) {  // zero in LDS, so that they meet no weight of 0; the rows that see them get NaN weights
+                if (bad) {  // zeros, too; the rows that see them get NaN weights
                     for (int i = threadIdx.x; i < S::TOKENS * S::CHUNKS; i += S::THREADS)
-                        if ((bad >> (i / S::CHUNKS)) & 1) {
-                            const uint32_t zero = here(0);
-                            *reinterpret_cast<DS4HC_LDS u32x4_t *>(buf + i * 16) = u32x4_t{zero, zero, zero, zero};
-                            scales[i / S::CHUNKS * 4] = 127;
-                        }
+                        if ((bad >> (i / S::CHUNKS)) & 1) clear(i);
                     wait_and_barrier<63>();
                 }
             }
             const int l = lane_here(), lr = l & 31, lh = l >> 5;
-            units[wave][l] = scale_of<DT>(scales[l * 4]);
-            if constexpr (DT == DT_F16) powers[wave][l] = scale_is_nan(scales[l * 4]) ? NAN : (float)(scale_byte<DT>(scales[l * 4]) - 127);
+            const uint32_t own_scale = scale_of_token(l);
+            units[wave][l] = scale_of<DT>(own_scale);
+            if constexpr (DT == DT_F16) powers[wave][l] = scale_is_nan(own_scale) ? NAN : (float)(scale_byte<DT>(own_scale) - 127);
             // LDS offsets of this lane's reads for the first k step, rope step and block of the
             // output; the others' chunks differ in higher bits, which an xor reaches. Made anew for
             // every tile: there are no registers to keep them.
             const int t0 = set * S::STEPS * 32;  // first token of the wave
-            const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + ((lh ^ swz8<S::CHUNKS>(lr)) << 4);
+            const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + (((EIGHT ? 2 * lh : lh) ^ swz8<S::CHUNKS>(lr)) << 4);
             const uint32_t r0 = S::ROPE_AT + (t0 + lr) * 128 + ((lh ^ swz8_rope(lr)) << 4);
             const int vr = lh * 4 + ((l >> 1) & 3) + (l & 8);
             const uint32_t v0 = (t0 + vr) * S::ROW_BYTES + ((((l >> 4) & 1) ^ swz8<S::CHUNKS>(vr)) << 4) + (l & 1) * 8;
 
-            // X^T = K Q^T of 32 tokens, the operands of the next products on their way; `between`
-            // gives other work to the vector unit while the matrix unit is busy
+            // X^T = K Q^T of 32 tokens. A chain's first operands are read before it begins (begin_k), the others while it
+            // runs; `between` gives other work to the vector unit while the matrix unit is busy.
+            constexpr int ROPE_STEPS = LATENT_ROPE / 16;
+            constexpr int SLOTS_K = EIGHT ? S::LATENT / 32 + ROPE_STEPS : S::KSTEPS, SLOTS_V = EIGHT ? S::DBLOCKS : S::DBLOCKS * 2;  // matrix instructions
+            constexpr int KREADS = S::LATENT / 32, KAHEAD = KREADS < 4 ? KREADS : 4;  // reads of 16 bytes a lane
+            u32x4_t kx[KAHEAD];
+            uint32_t scale_word;
+            auto read_k = [&](int step, int i) {
+                const uint32_t at = EIGHT ? (k0 ^ ((i & 6) << 5) ^ ((i & 1) << 4)) : (k0 ^ ((i & 7) << 5));
+                return lds_read16(buf + at + (i >> 3) * 256 + step * 32 * S::ROW_BYTES);
+            };
+            auto begin_k = [&](int step) {
+                scale_word = scale_of_token(t0 + step * 32 + lr);
+#pragma unroll
+                for (int i = 0; i < KAHEAD; ++i) kx[i] = read_k(step, i);
+            };
             auto products_k = [&](int step, acc16_t &s, auto &&between) {
-                const float unit_k = scale_of<DT>(scales[(t0 + step * 32 + lr) * 4]);
-                auto read = [&](int j) { return lds_read16(buf + (k0 ^ ((j & 7) << 5)) + (j >> 3) * 256 + step * 32 * S::ROW_BYTES); };
-                auto read_rope = [&](int j) { return lds_read16(buf + (r0 ^ (j << 5)) + step * 32 * 128); };
-                constexpr int ROPE_STEPS = LATENT_ROPE / 16;
-                u32x4_t x[2] = {read(0), read(1)}, r[ROPE_STEPS];
-#pragma unroll
-                for (int j = 0; j < S::KLATENT / 2; ++j) {
-                    const u32x4_t now = x[j & 1];
-                    if (j + 2 < S::KLATENT / 2) x[j & 1] = read(j + 2);
-                    if (j >= S::KLATENT / 2 - ROPE_STEPS) r[j - S::KLATENT / 2 + ROPE_STEPS] = read_rope(j - S::KLATENT / 2 + ROPE_STEPS);
-                    const u32x4_t w0 = widen8<DT>(now.x, now.y, unit_k), w1 = widen8<DT>(now.z, now.w, unit_k);
-                    if (j == 0) mfma32_first_v<DT>(w0, q[0], s);
-                    else mfma32_v<DT>(w0, q[2 * j], s);
-                    between(2 * j);
-                    mfma32_v<DT>(w1, q[2 * j + 1], s);
-                    between(2 * j + 1);
-                    __builtin_amdgcn_sched_barrier(0);
+                u32x4_t r[2], rq[2];
+                auto read_rope = [&](int j) {
+                    r[j & 1] = lds_read16(buf + (r0 ^ (j << 5)) + step * 32 * 128);
+                    rq[j & 1] = rope_queries[wave][j][l];
+                };
+                if constexpr (EIGHT) {
+                    const int scale = scale_is_nan(scale_word) ? SCALE_NAN : scale_byte<DT>(scale_word);
+                    for_each<KREADS / 2>([&](auto nth) {
+                        constexpr int k = nth;
+                        const i32x8_t now = join8(kx[2 * k % KAHEAD], kx[(2 * k + 1) % KAHEAD]);
+                        if (k == 0) mfma64_first_v(now, join8(q[0], q[1]), s, scale, scale_hi);
+                        else mfma64_v(now, join8(q[4 * k], q[4 * k + 1]), s, scale, scale_hi);
+                        between(2 * k);
+                        __builtin_amdgcn_sched_barrier(0);
+                        mfma64_v(now, join8(q[4 * k + 2], q[4 * k + 3]), s, scale, scale_lo);
+                        if (2 * k + KAHEAD < KREADS) {
+                            kx[2 * k % KAHEAD] = read_k(step, 2 * k + KAHEAD);
+                            kx[(2 * k + 1) % KAHEAD] = read_k(step, 2 * k + 1 + KAHEAD);
+                        }
+                        if (k == KREADS / 2 - 1) read_rope(0), read_rope(1);
+                        between(2 * k + 1);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                } else {
+                    const float unit_k = scale_of<DT>(scale_word);
+                    for_each<KREADS>([&](auto nth) {
+                        constexpr int i = nth;
+                        const u32x4_t now = kx[i % KAHEAD];
+                        if (i + KAHEAD < KREADS) kx[i % KAHEAD] = read_k(step, i + KAHEAD);
+                        if (i == KREADS - 1) read_rope(0), read_rope(1);
+                        const u32x4_t w0 = widen8<DT>(now.x, now.y, unit_k), w1 = widen8<DT>(now.z, now.w, unit_k);
+                        if (i == 0) mfma32_first_v<DT>(w0, q[0], s);
+                        else mfma32_v<DT>(w0, q[2 * i], s);
+                        between(2 * i);
+                        mfma32_v<DT>(w1, q[2 * i + 1], s);
+                        between(2 * i + 1);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
                 }
-#pragma unroll
-                for (int j = 0; j < ROPE_STEPS; ++j) {
-                    mfma32_v<DT>(r[j], q[S::KLATENT + j], s);
-                    between(S::KLATENT + j);
+                for_each<ROPE_STEPS>([&](auto nth) {
+                    constexpr int j = nth;
+                    mfma32_v<DT>(r[j & 1], rq[j & 1], s);
+                    if (j + 2 < ROPE_STEPS) read_rope(j + 2);
+                    between(SLOTS_K - ROPE_STEPS + j);
                     __builtin_amdgcn_sched_barrier(0);
+                });
+            };
+            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of X^T's rows, for both operands. 8-bit
+            // products: the weights' hi in the first block of k, their lo in the second, the values in both.
+            constexpr int VREADS = S::DBLOCKS * 2, VAHEAD = VREADS < 4 ? VREADS : 4;
+            u32x2_t vx[VAHEAD], again[VAHEAD];  // (8-bit products: read twice, in place of copies in the vector unit)
+            struct Weights {
+                u32x4_t p[2];
+                int scale;  // 8-bit products: of the lane's block
+            };
+            const uint32_t v0_again = here(v0);  // (an address that the compiler does not take for the same)
+            auto read_v = [&](int step, int i, uint32_t v0) {  // block i / 2, tokens 16 (i % 2) .. + 15
+                const int d = i / 2;
+                return lds_read_tr8(buf + (v0 ^ ((d & 7) << 5)) + (d >> 3) * 256 + (step * 32 + (i & 1) * 16) * S::ROW_BYTES);
+            };
+            auto begin_v = [&](int step) {
+#pragma unroll
+                for (int i = 0; i < VAHEAD; ++i) {
+                    vx[i] = read_v(step, i, v0);
+                    if constexpr (EIGHT) again[i] = read_v(step, i, v0_again);
                 }
             };
-            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of X^T's rows, for both operands
-            constexpr int VAHEAD = 4;
-            auto products_v = [&](int step, const u32x4_t (&p)[2], auto &&between) {
-                auto read = [&](int i) {  // block i / 2, tokens 16 (i % 2) .. + 15
-                    const int d = i / 2;
-                    return lds_read_tr8(buf + (v0 ^ ((d & 7) << 5)) + (d >> 3) * 256 + (step * 32 + (i & 1) * 16) * S::ROW_BYTES);
-                };
-                u32x2_t v[VAHEAD];
-#pragma unroll
-                for (int i = 0; i < VAHEAD; ++i) v[i] = read(i);
-#pragma unroll
-                for (int i = 0; i < S::DBLOCKS * 2; ++i) {
-                    const u32x4_t w = widen8<DT>(v[i % VAHEAD].x, v[i % VAHEAD].y, 1.f);
-                    acc[i / 2] = mfma32<DT>(w, p[i & 1], acc[i / 2]);
-                    if (i + VAHEAD < S::DBLOCKS * 2) v[i % VAHEAD] = read(i + VAHEAD);
-                    between(i);
-                    __builtin_amdgcn_sched_barrier(0);
+            auto products_v = [&](int step, const Weights &w, auto &&between) {
+                if constexpr (EIGHT) {
+                    const i32x8_t p = join8(w.p[0], w.p[1]);
+                    int one = 127;
+                    asm("" : "+v"(one));
+                    for_each<S::DBLOCKS>([&](auto nth) {
+                        constexpr int d = nth;
+                        constexpr int x = 2 * d % VAHEAD, y = (2 * d + 1) % VAHEAD;
+                        acc[d] = mfma64(join8(u32x4_t{vx[x].x, vx[x].y, vx[y].x, vx[y].y}, u32x4_t{again[x].x, again[x].y, again[y].x, again[y].y}), p,
+                                        acc[d], one, w.scale);
+                        if (2 * d + VAHEAD < VREADS) {
+                            vx[x] = read_v(step, 2 * d + VAHEAD, v0);
+                            vx[y] = read_v(step, 2 * d + 1 + VAHEAD, v0);
+                            again[x] = read_v(step, 2 * d + VAHEAD, v0_again);
+                            again[y] = read_v(step, 2 * d + 1 + VAHEAD, v0_again);
+                        }
+                        between(d);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                } else {
+                    for_each<VREADS>([&](auto nth) {
+                        constexpr int i = nth;
+                        const u32x4_t a = widen8<DT>(vx[i % VAHEAD].x, vx[i % VAHEAD].y, 1.f);
+                        acc[i / 2] = mfma32<DT>(a, w.p[i & 1], acc[i / 2]);
+                        if (i + VAHEAD < VREADS) vx[i % VAHEAD] = read_v(step, i + VAHEAD, v0);
+                        between(i);
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
                 }
             };
             // Softmax of a step, in pieces. The mask, and the largest logit (of the lane's row).
@@ -341,83 +561,127 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 }
                 return keep;
             };
-            // Weights 2 i and 2 i + 1 times their tokens' powers of 2, rounded to the type that the second product takes.
-            auto weight2 = [&](int step, const acc16_t &s, int i, u32x4_t (&p)[2]) {
-                const float *u = &units[wave][at_token + step * 32 + 8 * (i / 2) + 2 * (i & 1)];
-                if constexpr (DT == DT_F16) {
-                    const float e0 = exp2_fast(s[2 * i] - from), e1 = exp2_fast(s[2 * i + 1] - from);
-                    auto inverse = [](float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); };
-                    sum = fmaf(e0, inverse(u[0]), sum);
-                    sum = fmaf(e1, inverse(u[1]), sum);
-                    p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+            // Weights times their tokens' powers of 2, as the second product takes them, in pieces: 8 of two weights,
+            // then (8-bit products) the scale and four words.
+            constexpr int PIECES = EIGHT ? 13 : 8;
+            int scale_p = 0;
+            acc4_t powers2[2];  // read ahead
+            auto read_powers = [&](int step, int k) { powers2[k & 1] = *reinterpret_cast<const acc4_t *>(&units[wave][at_token + step * 32 + 8 * k]); };
+            auto weigh = [&](int step, acc16_t &s, int i, Weights &w) {
+                if (i < 8) {
+                    const float u[2] = {powers2[i / 2 & 1][2 * (i & 1)], powers2[i / 2 & 1][2 * (i & 1) + 1]};
+                    if ((i & 1) && i / 2 + 2 < 4) read_powers(step, i / 2 + 2);
+                    if constexpr (DT == DT_F16) {
+                        const float e0 = exp2_fast(s[2 * i] - from), e1 = exp2_fast(s[2 * i + 1] - from);
+                        auto inverse = [](float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); };
+                        sum = fmaf(e0, inverse(u[0]), sum);
+                        sum = fmaf(e1, inverse(u[1]), sum);
+                        w.p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+                    } else {
+                        const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
+                        sum += e0;
+                        sum += e1;
+                        if constexpr (EIGHT) s[2 * i] = e0 * u[0], s[2 * i + 1] = e1 * u[1];
+                        else w.p[i >> 2][i & 3] = pack2<DT>(e0 * u[0], e1 * u[1]);
+                    }
+                } else if (i == 8) {
+                    scale_p = split_scale(max_halves(max16(s)));
+                    w.scale = lane_here() < 32 ? scale_p : scale_p - 4;
                 } else {
-                    const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
-                    sum += e0;
-                    sum += e1;
-                    p[i >> 2][i & 3] = pack2<DT>(e0 * u[0], e1 * u[1]);
+                    const int k = i - 9;
+                    uint32_t hi, lo;
+                    split4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3], scale_p, hi, lo);
+                    w.p[0][k] = hi;
+                    w.p[1][k] = lo;
                 }
             };
-            constexpr int SLOTS = S::KSTEPS * S::STEPS + S::DBLOCKS * 2, LOAD_EVERY = SLOTS / S::LOADS;
+            constexpr int SLOTS = SLOTS_K * S::STEPS + SLOTS_V, LOAD_EVERY = SLOTS / S::LOADS;
             static_assert(LOAD_EVERY >= 1, "a place for each load");
-            const uint64_t lanes = (uint64_t)uniform((int64_t)(t + 1 < t_first + n ? -1 : 0));
+            buffer_t buffers[S::GROUPS];
+            buffers_of(next, t + S::BUFS - 1 < t_first + n, buffers);
+            const Place places = place(at_next);
             auto load_some = [&](int i) {
-                if (i % LOAD_EVERY == 0 && i / LOAD_EVERY < S::LOADS) load(i / LOAD_EVERY, rows, lane_here(), at_next, lanes);
+                if (i % LOAD_EVERY == 0 && i / LOAD_EVERY < S::LOADS) load(i / LOAD_EVERY, next, buffers, places);
             };
             acc16_t s;
-            u32x4_t p[2];
-            products_k(0, s, load_some);
+            Weights w;
+            begin_k(0);
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int LATE = SLOTS_K - ROPE_STEPS;  // the chain's latents have been read
             if constexpr (S::STEPS == 1) {
+                products_k(0, s, [&](int i) {
+                    load_some(i);
+                    if (i == LATE) begin_v(0);
+                    if (i == LATE + 1) read_powers(0, 0), read_powers(0, 1);
+                });
                 mfma_results(s);
                 const float high = largest(0, s);
                 if (__any(too_high(high))) raise(high);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) weight2(0, s, i, p);
-                products_v(0, p, [&](int i) { load_some(S::KSTEPS + i); });
+                for (int i = 0; i < PIECES; ++i) weigh(0, s, i, w);
+                products_v(0, w, [&](int i) { load_some(SLOTS_K + i); });
             } else {  // two steps, the softmax of each beside the products of the other, as far as can be
                 acc16_t s1;
-                u32x4_t p1[2];
+                Weights w1;
+                products_k(0, s, [&](int i) {
+                    load_some(i);
+                    if (i == LATE) begin_k(1);
+                    if (i == LATE + 1) read_powers(0, 0), read_powers(0, 1);
+                });
                 mfma_results(s);
                 float high = largest(0, s);
                 if (__any(too_high(high))) raise(high);
                 products_k(1, s1, [&](int i) {
-                    constexpr int EVERY = S::KSTEPS / 8;
-                    load_some(S::KSTEPS + i);
-                    if (i % EVERY == EVERY - 1 && i / EVERY < 8) weight2(0, s, i / EVERY, p);
+                    load_some(SLOTS_K + i);
+#pragma unroll
+                    for (int k = i * PIECES / SLOTS_K; k < (i + 1) * PIECES / SLOTS_K; ++k) weigh(0, s, k, w);
+                    if (i == LATE) begin_v(0);
+                    if (i == SLOTS_K - 1) read_powers(1, 0), read_powers(1, 1);
                 });
                 mfma_results(s1);
                 high = largest(1, s1);
                 if (__any(too_high(high))) {
-                    const float keep = raise(high);
+                    const float was = top, keep = raise(high);
+                    if constexpr (EIGHT) w.scale = max(w.scale + (int)fmaxf(was - top, -300.f), 1);
+                    else
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
+                        for (int i = 0; i < 8; ++i) w.p[i >> 2][i & 3] = scale2_words<DT>(w.p[i >> 2][i & 3], keep);
                 }
-                products_v(0, p, [&](int i) {
-                    constexpr int EVERY = S::DBLOCKS / 4;
-                    load_some(2 * S::KSTEPS + i);
-                    if (i % EVERY == EVERY - 1) weight2(1, s1, i / EVERY, p1);
+                products_v(0, w, [&](int i) {
+                    load_some(2 * SLOTS_K + i);
+#pragma unroll
+                    for (int k = i * PIECES / SLOTS_V; k < (i + 1) * PIECES / SLOTS_V; ++k) weigh(1, s1, k, w1);
                 });
-                products_v(1, p1, [](int) {});
+                begin_v(1);
+                products_v(1, w1, [](int) {});
             }
         };
 
-        // ---- tiles: the next one's loads run beside this one's products. All waves are done with
-        // tile t - 1 when they meet at the barrier of tile t, so its buffer takes tile t + 1.
+        // ---- tiles: the loads of the next two run beside this one's products. All waves are done with
+        // tile t - 1 when they meet at the barrier of tile t, so its buffer takes tile t + 2.
+        static_assert(S::BUFS == 3, "two tiles on their way");
         wait_and_barrier<63>();  // the last part's reads of the ring
         const uint32_t ring_at = lds_address(ring);
-        int rows = look_up(t_first);
-        uint64_t ok = present(rows);
+        Where now = look_up(t_first), next = look_up(t_first + 1);
+        buffer_t buffers[S::GROUPS];
+        buffers_of(now, true, buffers);
 #pragma unroll
-        for (int i = 0; i < S::LOADS; ++i) load(i, rows, lane_here(), ring_at, ~0ull);
+        for (int i = 0; i < S::LOADS; ++i) load(i, now, buffers, place(ring_at));
         load_queries();  // (waits for the first tile, too)
-        int next = look_up(t_first + 1);
+        buffers_of(next, n > 1, buffers);
+#pragma unroll
+        for (int i = 0; i < S::LOADS; ++i) load(i, next, buffers, place(ring_at + S::TILE_BYTES));
+        uint64_t ok = now.ok, ok_next = next.ok;
+        uint32_t at = 0;
         for (int i = 0; i < n; ++i) {
-            wait_and_barrier<0>();
-            rows = next;
-            const uint64_t ok_next = present(rows);
-            next = look_up(t_first + i + 2);
-            tile(t_first + i, ok, ring_at + (i & 1) * S::TILE_BYTES, rows, ring_at + ((i + 1) & 1) * S::TILE_BYTES);
+            wait_and_barrier<S::LOADS>();  // only the next tile's loads are on their way
+            const Where behind = look_up(t_first + i + 2);
+            tile(t_first + i, ok, ring_at + at, behind, ring_at + (at >= S::TILE_BYTES ? at - S::TILE_BYTES : at + 2 * S::TILE_BYTES));
+            at = at == 2 * S::TILE_BYTES ? 0 : at + S::TILE_BYTES;
             ok = ok_next;
+            ok_next = behind.ok;
         }
+        wait_and_barrier<0>();  // (those behind the last tile write zeros to LDS)
 
         // ---- the part's result
 #pragma unroll
@@ -524,7 +788,8 @@ Plan8 plan8(const Paged &c, int heads, int64_t N) {
 }
 
 template <int DT, class S> hipError_t run8(const AttnArgs &a, hipStream_t s) {
-    const hipError_t e = launch_kernel(attn8_kernel<DT, S>, dim3(WORKGROUPS), dim3(S::THREADS), s, a);
+    const dim3 grid(WORKGROUPS), block(S::THREADS);
+    const hipError_t e = a.c.page_shift >= 4 ? launch_kernel(attn8_kernel<DT, S, false>, grid, block, s, a) : launch_kernel(attn8_kernel<DT, S, true>, grid, block, s, a);
     if (e != hipSuccess) return e;
     return launch_kernel(attn_join_kernel<DT, S>, dim3(WORKGROUPS / a.members - 1, a.members), dim3(JOIN_WAVES * 64), s, a);
 }
