@@ -12,11 +12,11 @@ namespace ds4hc {
 namespace {
 
 constexpr int NODES = 1024;  // tokens of a sequence that are looked at
-constexpr int WIDE = 256, LAST = 1024;  // threads of a workgroup: of the sums, of the choice
-constexpr int CHUNK_STEP = 1024, CHUNK_MOST = 16 * LAST;
+constexpr int WIDE = 256, WAVES = WIDE / 64, LAST = 1024;  // threads of a workgroup: of the sums, of the choice
+constexpr int CHUNK_STEP = 1024, CHUNK_MOST = 16384;       // elements of a workgroup, a quarter of them a wave
 constexpr int GOAL = 1024;   // workgroups that sum
 
-// What the first kernel leaves for the second: of each sequence, then of each (sequence, chunk).
+// What the first kernel leaves for the second: of each sequence, then of each (sequence, wave's part of the row).
 struct Reached {
     int node;    // last token kept, -1: the sequence has none
     int ends;    // its children have all been rejected, or (chain with draft) its child: weights are what is left
@@ -70,7 +70,7 @@ __device__ __forceinline__ double left_of(float p, float q, bool less) {
     return less ? fmax((double)weight(p) - (double)weight(q), 0.0) : (double)weight(p);
 }
 
-// Grid (chunks, sequences). Every workgroup of a sequence finds its path by itself, from single elements
+// Grid (chunks, sequences). 64 chains of up to 5 tokens over 100003: @@SUMS@@. Every workgroup of a sequence finds its path by itself, from single elements
 // of the rows, and sums its chunk of the row that the path ends at; the first one writes the path.
 __global__ __launch_bounds__(WIDE) void verify_sums_kernel(VerifyArgs a) {
     __shared__ int parent[NODES], on_path[NODES];
@@ -78,7 +78,6 @@ __global__ __launch_bounds__(WIDE) void verify_sums_kernel(VerifyArgs a) {
     __shared__ int64_t token_of[NODES];
     __shared__ uint32_t marks[CHUNK_MOST / 32];
     __shared__ int shared_node, shared_kept;
-    __shared__ double partial[2][WIDE / 64];
     const int b = blockIdx.y, chunk = blockIdx.x, n = (int)a.N, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int t0 = cu_at(a.cu_q, b, n), all_tokens = max(cu_at(a.cu_q, b + 1, n) - t0, 0), few = min(all_tokens, NODES);
     if (few == 0) {
@@ -180,33 +179,38 @@ __global__ __launch_bounds__(WIDE) void verify_sums_kernel(VerifyArgs a) {
     const bool marked = !a.draft && mark_rejected<WIDE>(a, t0, few, node, first, count, marks);
     const float *p = a.target + (int64_t)(t0 + node) * a.target_stride + first;
     const float *q = less ? a.draft + (int64_t)(t0 + node) * a.draft_stride + first : p;
+    // a wave a quarter of the chunk, 8 loads of each row in flight
+    const int part = a.chunk / WAVES, end = min((wave + 1) * part, count);
     double left = 0.0, all = 0.0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < count; i += WIDE) {
-        const float w = p[i];
-        const double l = left_of(w, less ? q[i] : 0.f, less);
-        all += (double)weight(w);
-        left += marked && (marks[i >> 5] >> (i & 31)) & 1 ? 0.0 : l;
+    constexpr int AT_ONCE = 8;
+    for (int i0 = wave * part + lane; i0 < end; i0 += 64 * AT_ONCE) {
+        float w[AT_ONCE], v[AT_ONCE];
+#pragma unroll
+        for (int e = 0; e < AT_ONCE; ++e) {
+            const int i = min(i0 + e * 64, end - 1);
+            w[e] = p[i];
+            v[e] = less ? q[i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < AT_ONCE; ++e) {
+            const int i = i0 + e * 64;
+            if (i < end) {
+                all += (double)weight(w[e]);
+                left += marked && (marks[i >> 5] >> (i & 31)) & 1 ? 0.0 : left_of(w[e], v[e], less);
+            }
+        }
     }
     left = wave_sum(left);
     all = wave_sum(all);
-    if (lane == 0) {
-        partial[0][wave] = left;
-        partial[1][wave] = all;
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        Sums s = {0.0, 0.0};
-        for (int w = 0; w < WIDE / 64; ++w) s = {s.left + partial[0][w], s.all + partial[1][w]};
-        sums_at(a)[(int64_t)b * gridDim.x + chunk] = s;
-    }
+    if (lane == 0) sums_at(a)[((int64_t)b * gridDim.x + chunk) * WAVES + wave] = {left, all};
 }
 
-// A workgroup a sequence: the chunk in which the sum passes the number, then the element.
-__global__ __launch_bounds__(LAST) void verify_choose_kernel(VerifyArgs a, int chunks) {
-    __shared__ uint32_t marks[CHUNK_MOST / 32];
+// A workgroup a sequence: the part in which the sum passes the number, then the element.
+__global__ __launch_bounds__(LAST) void verify_choose_kernel(VerifyArgs a, int parts) {
+    constexpr int PART_MOST = CHUNK_MOST / WAVES;
+    __shared__ uint32_t marks[PART_MOST / 32];
     __shared__ double before[LAST / 64 + 1], goal, base;
-    __shared__ int chosen, in_chunk, least, use_all;
+    __shared__ int chosen, in_part, least, use_all;
     const int b = blockIdx.x, n = (int)a.N, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const Reached r = reached_at(a)[b];
     if (r.node < 0) {
@@ -214,41 +218,62 @@ __global__ __launch_bounds__(LAST) void verify_choose_kernel(VerifyArgs a, int c
         return;
     }
     const int t0 = cu_at(a.cu_q, b, n), few = min(cu_at(a.cu_q, b + 1, n) - t0, NODES);
-    const Sums *sums = sums_at(a) + (int64_t)b * chunks;
-    if (threadIdx.x == 0) {
-        double left = 0.0, all = 0.0;
-        for (int c = 0; c < chunks; ++c) left += sums[c].left, all += sums[c].all;
-        use_all = !(left > 0.0);
-        goal = number(a.uniform[t0]) * (use_all ? all : left);
-        // the first chunk whose end is above the goal; if rounding leaves none, the last that has any weight
-        double sum = 0.0;
-        in_chunk = -1;
-        base = 0.0;
-        for (int c = 0; c < chunks; ++c) {
-            const double s = use_all ? sums[c].all : sums[c].left;
-            if (s > 0.0) {
-                in_chunk = c;
-                base = sum;
-                if (sum + s > goal) break;
+    if (wave == 0) {
+        const Sums *sums = sums_at(a) + (int64_t)b * parts;
+        const float u = a.uniform[t0];
+        // lane by lane, 64 parts at a time; `left` and `all` are the sums before them
+        auto upto = [&](double v) {
+            for (int m = 1; m < 64; m <<= 1) {
+                const double o = __shfl_up(v, m);
+                if (lane >= m) v += o;
             }
-            sum += s;
+            return v;
+        };
+        double left = 0.0, all = 0.0;
+        for (int c0 = 0; c0 < parts; c0 += 64) {
+            const Sums s = c0 + lane < parts ? sums[c0 + lane] : Sums{0.0, 0.0};
+            left += __shfl(upto(s.left), 63);
+            all += __shfl(upto(s.all), 63);
         }
-        chosen = INT_MAX;
-        least = -1;
+        const bool every = !(left > 0.0);
+        const double to = number(u) * (every ? all : left);
+        // the first part whose end is above the goal; if rounding leaves none, the last that has any weight
+        int found = -1;
+        double sum = 0.0, at = 0.0;
+        for (int c0 = 0; c0 < parts; c0 += 64) {
+            const Sums s = c0 + lane < parts ? sums[c0 + lane] : Sums{0.0, 0.0};
+            const double v = every ? s.all : s.left, end = sum + upto(v);
+            const uint64_t some = __ballot(v > 0.0), over = __ballot(v > 0.0 && end > to);
+            if (some) {
+                const int who = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
+                found = c0 + who;
+                at = __shfl(end, who) - __shfl(v, who);
+            }
+            if (over) break;
+            sum = __shfl(end, 63);
+        }
+        if (lane == 0) {
+            use_all = every;
+            goal = to;
+            in_part = found;
+            base = at;
+            chosen = INT_MAX;
+            least = -1;
+        }
     }
     __syncthreads();
-    if (in_chunk < 0) {  // no weight at all
+    if (in_part < 0) {  // no weight at all
         if (threadIdx.x == 0) a.next[b] = -1;
         return;
     }
-    const int first = in_chunk * a.chunk, count = min(a.chunk, a.vocab - first);
+    const int part = a.chunk / WAVES, first = in_part / WAVES * a.chunk + in_part % WAVES * part, count = min(part, a.vocab - first);
     const bool less = r.ends && !use_all;
     const bool marked = !a.draft && !use_all && mark_rejected<LAST>(a, t0, few, r.node, first, count, marks);
     const float *p = a.target + (int64_t)(t0 + r.node) * a.target_stride + first;
     const float *q = less ? a.draft + (int64_t)(t0 + r.node) * a.draft_stride + first : p;
     // a thread some elements one behind another
-    constexpr int MOST = CHUNK_MOST / LAST;
-    const int each = (a.chunk + LAST - 1) / LAST, i0 = threadIdx.x * each;
+    constexpr int MOST = PART_MOST / LAST;
+    const int each = (part + LAST - 1) / LAST, i0 = threadIdx.x * each;
     double w[MOST], mine = 0.0;
 #pragma unroll
     for (int e = 0; e < MOST; ++e) {
@@ -281,7 +306,7 @@ __global__ __launch_bounds__(LAST) void verify_choose_kernel(VerifyArgs a, int c
     const uint64_t hits = __ballot(hit != INT_MAX);
     if (hits && lane == __builtin_ctzll(hits)) atomicMin(&chosen, hit);
     __syncthreads();
-    if (chosen == INT_MAX && last >= 0) atomicMax(&least, last);  // (rounding left none: the chunk's last)
+    if (chosen == INT_MAX && last >= 0) atomicMax(&least, last);  // (rounding left none: the part's last)
     __syncthreads();
     if (threadIdx.x == 0) a.next[b] = first + (chosen != INT_MAX ? chosen : least);
 }
@@ -289,7 +314,7 @@ __global__ __launch_bounds__(LAST) void verify_choose_kernel(VerifyArgs a, int c
 }  // namespace
 
 uint64_t verify_workspace_bytes(int n_seqs, int vocab) {
-    return (uint64_t)n_seqs * (sizeof(Reached) + (uint64_t)chunks_of(vocab, chunk_of(n_seqs, vocab)) * sizeof(Sums));
+    return (uint64_t)n_seqs * (sizeof(Reached) + (uint64_t)chunks_of(vocab, chunk_of(n_seqs, vocab)) * WAVES * sizeof(Sums));
 }
 
 hipError_t launch_verify(const VerifyArgs &args, hipStream_t s) {
@@ -298,7 +323,7 @@ hipError_t launch_verify(const VerifyArgs &args, hipStream_t s) {
     const int chunks = chunks_of(a.vocab, a.chunk);
     const hipError_t e = launch_kernel(verify_sums_kernel, dim3((unsigned)chunks, (unsigned)a.n_seqs), dim3(WIDE), s, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(verify_choose_kernel, dim3((unsigned)a.n_seqs), dim3(LAST), s, a, chunks);
+    return launch_kernel(verify_choose_kernel, dim3((unsigned)a.n_seqs), dim3(LAST), s, a, chunks * WAVES);
 }
 
 }  // namespace ds4hc

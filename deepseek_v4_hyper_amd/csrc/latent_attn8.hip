@@ -17,6 +17,9 @@ namespace {
 template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape8 {
     static constexpr int LATENT = LATENT_, ROW_WAVES = ROW_WAVES_, SETS = SETS_;
     static constexpr int TOKENS = 64, BUFS = 3, STEPS = TOKENS / SETS / 32;
+    // (4, 6, 8, 10: 128 sequences of up to 8192 tokens x 16 heads 116, 106, 105, 105 us; calls of fewer than 32 tiles a
+    // workgroup, where a quarter of them is what counts, the same within 1 %)
+    static constexpr int EXTRA = 8;
     static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int ROWS = ROW_WAVES * 32;
     static constexpr int ROW_BYTES = LATENT, CHUNKS = ROW_BYTES / 16;  // a token's latent in LDS
@@ -220,23 +223,31 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         constexpr bool EIGHT = DT == DT_BF16;
         u32x4_t q[S::KLATENT];
         int scale_hi = 0, scale_lo = 0;
-        auto load_queries = [&]() {
+        u32x4_t rope[LATENT_ROPE / 16];
+        auto load_queries = [&]() {  // (they are there once the block table's entries are, before the first tile's loads)
             const int head = min(row0 + (lane & 31), n_rows - 1) - tok * a.heads;
             const elem_t<DT> *ql = static_cast<const elem_t<DT> *>(a.ql) + (int64_t)(q0 + tok) * a.ql_token + head * a.ql_head + (lane >> 5) * 16;
             const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head + (lane >> 5) * 8;
 #pragma unroll
-            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane] = *reinterpret_cast<const u32x4_t *>(qr + k * 16);
-#pragma unroll
             for (int k = 0; k < S::KLATENT; ++k)
                 q[k] = *reinterpret_cast<const u32x4_t *>(EIGHT ? ql + (lane >> 5) * 16 + (k >> 2) * 64 + (k & 3) * 8 : ql + (k >> 1) * 32 + (k & 1) * 8);
 #pragma unroll
+            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope[k] = *reinterpret_cast<const u32x4_t *>(qr + k * 16);
+        };
+        auto split_queries = [&]() {
+#pragma unroll
             for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);
+#pragma unroll
+            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane_here()] = rope[k];
             if constexpr (EIGHT) {
-                float most = 0.f;
+                // largest magnitude: bfloat16 bits without the sign are in the numbers' order (NaN last)
+                typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+                u16x2_t most2 = {0, 0};
 #pragma unroll
                 for (int k = 0; k < S::KLATENT; ++k)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) most = fmaxf(most, fmaxf(fabsf(bf16_lo(q[k][i])), fabsf(bf16_hi(q[k][i]))));
+                    for (int i = 0; i < 4; ++i) most2 = __builtin_elementwise_max(most2, __builtin_bit_cast(u16x2_t, q[k][i] & 0x7FFF7FFFu));
+                const float most = __uint_as_float((uint32_t)(most2.x > most2.y ? most2.x : most2.y) << 16);
 #pragma unroll
                 for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);  // (as new: the numbers above are not kept for what follows)
                 scale_hi = split_scale(max_halves(most));
@@ -662,15 +673,16 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         static_assert(S::BUFS == 3, "two tiles on their way");
         wait_and_barrier<63>();  // the last part's reads of the ring
         const uint32_t ring_at = lds_address(ring);
+        load_queries();
         Where now = look_up(t_first), next = look_up(t_first + 1);
         buffer_t buffers[S::GROUPS];
         buffers_of(now, true, buffers);
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i) load(i, now, buffers, place(ring_at));
-        load_queries();  // (waits for the first tile, too)
         buffers_of(next, n > 1, buffers);
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i) load(i, next, buffers, place(ring_at + S::TILE_BYTES));
+        split_queries();
         uint64_t ok = now.ok, ok_next = next.ok;
         uint32_t at = 0;
         for (int i = 0; i < n; ++i) {

@@ -1,6 +1,7 @@
 // latent_split.hpp -- how attention over a paged latent cache is split over workgroups, and the
 // joining of what is cut: shared by the kernels of the 16-bit (latent_attn.hip) and of the 8-bit
-// cache (latent_attn8.hip). S is a kernel's tile shape: S::ROWS query rows by S::TOKENS tokens, S::LATENT.
+// cache (latent_attn8.hip). S is a kernel's tile shape: S::ROWS query rows by S::TOKENS tokens, S::LATENT, and S::EXTRA, the
+// tiles that a batch's queries and results cost as much as.
 #pragma once
 
 #include "latent_device.hpp"
@@ -11,9 +12,6 @@ namespace {
 
 constexpr int WORKGROUPS = 256;  // one a CU: the ring of tiles fills most of its LDS
 constexpr int XCDS = 8;          // workgroup i runs on XCD i % 8
-// tiles that a batch's queries and results cost as much as (0, 4, 8: 64 sequences of up to 8192 x 128
-// heads 158, 143, 136 us; 24 chains over up to 4096 166, 110, 119; trees 89, 76, 78)
-constexpr int EXTRA = 4;
 
 // ------------------------------------------------------------------ the split of the work
 //
@@ -92,7 +90,7 @@ __device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, 
         }
     }
     const int clusters = WORKGROUPS / a.members;
-    extra = (int)min(wave_sum(tiles) / clusters / 4, (int64_t)EXTRA);  // (none where a share is a few tiles)
+    extra = (int)min(wave_sum(tiles) / clusters / 4, (int64_t)S::EXTRA);  // (none where a share is a few tiles)
     const int64_t mine = tiles + batches * extra, upto = wave_prefix(mine, lane), total = __shfl(upto, 63);
     share = (total + clusters - 1) / clusters;
     if (share < 1) share = 1;

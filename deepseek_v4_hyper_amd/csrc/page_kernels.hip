@@ -125,20 +125,50 @@ __device__ __forceinline__ int64_t block_prefix(int64_t v, int64_t *shared, int6
     return before + upto - v;
 }
 
-// The first item of each slot that the items name.
-__device__ __forceinline__ void find_owners(const PoolArgs &a, int *owner) {
-    for (int i = threadIdx.x; i < a.n; i += DECIDE) {
-        const int s = a.slots[i];
-        if (s >= 0 && s < a.n_slots) __hip_atomic_store(&owner[s], INT_MAX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// Whether item i is the first that names slot `s`. Of up to DECIDE items the slots stand in a table in LDS, each at the first
+// free place from its hash on; of more each slot's first item in the workspace. (Through the workspace a call waits for
+// three round trips more.)
+constexpr int PLACES = 2 * DECIDE;
+struct First {
+    int slot[PLACES], item[PLACES];
+};
+__device__ __forceinline__ int place_of(int s) { return (int)((uint32_t)s * 2654435769u >> 21); }
+static_assert(PLACES == 1 << 11, "the hash's bits");
+
+__device__ __forceinline__ void find_firsts(const PoolArgs &a, int *owner, First &f) {
+    if (a.n <= DECIDE) {
+        for (int i = threadIdx.x; i < PLACES; i += DECIDE) {
+            f.slot[i] = -1;
+            f.item[i] = INT_MAX;
+        }
+        __syncthreads();
+        const int i = threadIdx.x, s = i < a.n ? a.slots[i] : -1;
+        if (s >= 0 && s < a.n_slots)
+            for (int at = place_of(s);; at = (at + 1) % PLACES) {  // (at most DECIDE of the places are taken)
+                const int was = atomicCAS(&f.slot[at], -1, s);
+                if (was == -1 || was == s) {
+                    atomicMin(&f.item[at], i);
+                    break;
+                }
+            }
+    } else {
+        for (int i = threadIdx.x; i < a.n; i += DECIDE) {
+            const int s = a.slots[i];
+            if (s >= 0 && s < a.n_slots) __hip_atomic_store(&owner[s], INT_MAX, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.n; i += DECIDE) {
+            const int s = a.slots[i];
+            if (s >= 0 && s < a.n_slots) atomicMin(&owner[s], i);
+        }
     }
-    __threadfence();
     __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += DECIDE) {
-        const int s = a.slots[i];
-        if (s >= 0 && s < a.n_slots) atomicMin(&owner[s], i);
-    }
-    __threadfence();
-    __syncthreads();
+}
+__device__ __forceinline__ bool is_first(const PoolArgs &a, const int *owner, const First &f, int s, int i) {
+    if (a.n > DECIDE) return load_fresh(&owner[s]) == i;
+    int at = place_of(s);
+    while (f.slot[at] != s) at = (at + 1) % PLACES;
+    return f.item[at] == i;
 }
 
 __device__ __forceinline__ int length_at(const PoolArgs &a, int slot) {
@@ -148,8 +178,9 @@ __device__ __forceinline__ int pages_of(const PoolArgs &a, int length) { return 
 
 __global__ __launch_bounds__(DECIDE) void resize_decide_kernel(PoolArgs a) {
     __shared__ int64_t shared[WAVES];
+    __shared__ First firsts;
     const Space ws = space(a);
-    find_owners(a, ws.owner);
+    find_firsts(a, ws.owner, firsts);
     int64_t need = 0;  // of all items so far
     for (int i0 = 0; i0 < a.n; i0 += DECIDE) {
         const int i = i0 + threadIdx.x;
@@ -157,7 +188,7 @@ __global__ __launch_bounds__(DECIDE) void resize_decide_kernel(PoolArgs a) {
         int mine = 0;
         if (i < a.n) {
             const int s = a.slots[i], length = a.lengths[i];
-            if (s >= 0 && s < a.n_slots && length >= 0 && length <= a.max_pages << a.page_shift && load_fresh(&ws.owner[s]) == i) {
+            if (s >= 0 && s < a.n_slots && length >= 0 && length <= a.max_pages << a.page_shift && is_first(a, ws.owner, firsts, s, i)) {
                 const int old = length_at(a, s);
                 item.had = pages_of(a, old);
                 item.has = pages_of(a, length);
@@ -241,12 +272,13 @@ __global__ __launch_bounds__(THREADS) void resize_apply_kernel(PoolArgs a) {
 }
 
 __global__ __launch_bounds__(DECIDE) void fork_decide_kernel(PoolArgs a) {
+    __shared__ First firsts;
     const Space ws = space(a);
-    find_owners(a, ws.owner);
+    find_firsts(a, ws.owner, firsts);
     for (int i = threadIdx.x; i < a.n; i += DECIDE) {
         const int child = a.slots[i], parent = a.lengths[i];
         Item item = {0, -1, 0, 0};
-        if (child >= 0 && child < a.n_slots && parent >= 0 && parent < a.n_slots && child != parent && load_fresh(&ws.owner[child]) == i &&
+        if (child >= 0 && child < a.n_slots && parent >= 0 && parent < a.n_slots && child != parent && is_first(a, ws.owner, firsts, child, i) &&
             a.kv_len[child] == 0) {
             item.had = length_at(a, parent);
             item.has = pages_of(a, item.had);
