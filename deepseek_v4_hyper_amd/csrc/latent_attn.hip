@@ -31,7 +31,7 @@ template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape {
     static constexpr int TOKENS = 64, BUFS = 2, STEPS = TOKENS / SETS / 32;
     // (0, 4, 8: 64 sequences of up to 8192 x 128 heads 158, 143, 136 us; 24 chains over up to 4096 166, 110, 119;
     // trees 89, 76, 78)
-    static constexpr int EXTRA = 4;
+    static constexpr int EXTRA = 4, EXTRA_OF = 4;
     static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int D = LATENT + LATENT_ROPE;
     static constexpr int ROWS = ROW_WAVES * 32;

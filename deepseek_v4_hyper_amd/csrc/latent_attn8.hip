@@ -17,9 +17,10 @@ namespace {
 template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape8 {
     static constexpr int LATENT = LATENT_, ROW_WAVES = ROW_WAVES_, SETS = SETS_;
     static constexpr int TOKENS = 64, BUFS = 3, STEPS = TOKENS / SETS / 32;
-    // (4, 6, 8, 10: 128 sequences of up to 8192 tokens x 16 heads 116, 106, 105, 105 us; calls of fewer than 32 tiles a
-    // workgroup, where a quarter of them is what counts, the same within 1 %)
-    static constexpr int EXTRA = 8;
+    // (EXTRA and the share that it may take: 8 and a quarter, 6 and a half, 8 and a half, all: 128 sequences of up to 8192 tokens
+    // x 16 heads 105, 106, 105, 105 us; 64 x 128 heads 122, 114, 114, 114; 24 chains over up to 4096 98, 91, 91, 93; trees
+    // 79, 73, 73, 72, float16 78, 80, 80, 84; latent 128 54.6, 56.8, 56.3, 56.0)
+    static constexpr int EXTRA = 6, EXTRA_OF = 2;
     static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int ROWS = ROW_WAVES * 32;
     static constexpr int ROW_BYTES = LATENT, CHUNKS = ROW_BYTES / 16;  // a token's latent in LDS
@@ -128,11 +129,16 @@ typedef short s16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
 // With C in vector registers, as mfma32_v; the wait for its results is that of the last instruction of a chain.
-__device__ __forceinline__ void mfma64_first_v(i32x8_t a, i32x8_t b, acc16_t &c, int scale_a, int scale_b) {
-    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %3, %4 op_sel_hi:[0,0,0]" : "=&v"(c) : "v"(a), "v"(b), "v"(scale_a), "v"(scale_b));
+// A times hi, then lo, of B.
+__device__ __forceinline__ void mfma64_first_v(i32x8_t a, i32x8_t hi, i32x8_t lo, acc16_t &c, int scale_a, int scale_hi, int scale_lo) {
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %4, %5 op_sel_hi:[0,0,0]\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %3, %0, %4, %6 op_sel_hi:[0,0,0]"
+        : "=&v"(c)
+        : "v"(a), "v"(hi), "v"(lo), "v"(scale_a), "v"(scale_hi), "v"(scale_lo));
 }
-__device__ __forceinline__ void mfma64_v(i32x8_t a, i32x8_t b, acc16_t &c, int scale_a, int scale_b) {
-    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[0,0,0]" : "+&v"(c) : "v"(a), "v"(b), "v"(scale_a), "v"(scale_b));
+__device__ __forceinline__ void mfma64_v(i32x8_t a, i32x8_t hi, i32x8_t lo, acc16_t &c, int scale_a, int scale_hi, int scale_lo) {
+    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %4, %5 op_sel_hi:[0,0,0]\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %3, %0, %4, %6 op_sel_hi:[0,0,0]"
+        : "+&v"(c)
+        : "v"(a), "v"(hi), "v"(lo), "v"(scale_a), "v"(scale_hi), "v"(scale_lo));
 }
 __device__ __forceinline__ acc16_t mfma64(i32x8_t a, i32x8_t b, acc16_t c, int scale_a, int scale_b) {
     return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, scale_a, 0, scale_b);
@@ -183,7 +189,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         Start at = {b, 0, 0, 0};
         if (b >= 0) {
             const int each = sq.kv_tiles + extra;
-            at.batch = (int)(off / each);
+            at.batch = (int)quotient(off, each);
             at.tile = max((int)(off - (int64_t)at.batch * each) - extra, 0);
         }
         head->start[cluster] = at;
@@ -204,7 +210,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             continue;
         }
         const int q0 = sq.q0;
-        const int batch = (int)(off / each), u0 = (int)(off - (int64_t)batch * each), u1 = u0 + (int)min((int64_t)(each - u0), left);
+        const int batch = (int)quotient(off, each), u0 = (int)(off - (int64_t)batch * each), u1 = u0 + (int)min((int64_t)(each - u0), left);
         const int t_first = max(u0 - extra, 0), n = max(u1 - extra, 0) - t_first;
         const int row_tile = batch * a.members + member;
         const bool part_of_first = first_part && t_first > 0;
@@ -420,7 +426,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             // X^T = K Q^T of 32 tokens. A chain's first operands are read before it begins (begin_k), the others while it
             // runs; `between` gives other work to the vector unit while the matrix unit is busy.
             constexpr int ROPE_STEPS = LATENT_ROPE / 16;
-            constexpr int SLOTS_K = EIGHT ? S::LATENT / 32 + ROPE_STEPS : S::KSTEPS, SLOTS_V = EIGHT ? S::DBLOCKS : S::DBLOCKS * 2;  // matrix instructions
+            constexpr int SLOTS_K = EIGHT ? S::LATENT / 64 + ROPE_STEPS : S::KSTEPS, SLOTS_V = EIGHT ? S::DBLOCKS : S::DBLOCKS * 2;  // places for other work
             constexpr int KREADS = S::LATENT / 32, KAHEAD = KREADS < 4 ? KREADS : 4;  // reads of 16 bytes a lane
             u32x4_t kx[KAHEAD];
             uint32_t scale_word;
@@ -444,17 +450,14 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                     for_each<KREADS / 2>([&](auto nth) {
                         constexpr int k = nth;
                         const i32x8_t now = join8(kx[2 * k % KAHEAD], kx[(2 * k + 1) % KAHEAD]);
-                        if (k == 0) mfma64_first_v(now, join8(q[0], q[1]), s, scale, scale_hi);
-                        else mfma64_v(now, join8(q[4 * k], q[4 * k + 1]), s, scale, scale_hi);
-                        between(2 * k);
-                        __builtin_amdgcn_sched_barrier(0);
-                        mfma64_v(now, join8(q[4 * k + 2], q[4 * k + 3]), s, scale, scale_lo);
+                        if (k == 0) mfma64_first_v(now, join8(q[0], q[1]), join8(q[2], q[3]), s, scale, scale_hi, scale_lo);
+                        else mfma64_v(now, join8(q[4 * k], q[4 * k + 1]), join8(q[4 * k + 2], q[4 * k + 3]), s, scale, scale_hi, scale_lo);
                         if (2 * k + KAHEAD < KREADS) {
                             kx[2 * k % KAHEAD] = read_k(step, 2 * k + KAHEAD);
                             kx[(2 * k + 1) % KAHEAD] = read_k(step, 2 * k + 1 + KAHEAD);
                         }
                         if (k == KREADS / 2 - 1) read_rope(0), read_rope(1);
-                        between(2 * k + 1);
+                        between(k);
                         __builtin_amdgcn_sched_barrier(0);
                     });
                 } else {
@@ -606,13 +609,15 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                     w.p[1][k] = lo;
                 }
             };
-            constexpr int SLOTS = SLOTS_K * S::STEPS + SLOTS_V, LOAD_EVERY = SLOTS / S::LOADS;
-            static_assert(LOAD_EVERY >= 1, "a place for each load");
+            constexpr int SLOTS = SLOTS_K * S::STEPS + SLOTS_V, LOAD_EVERY = SLOTS > S::LOADS ? SLOTS / S::LOADS : 1, LOADS_A_SLOT = (S::LOADS + SLOTS - 1) / SLOTS;
             buffer_t buffers[S::GROUPS];
             buffers_of(next, t + S::BUFS - 1 < t_first + n, buffers);
             const Place places = place(at_next);
             auto load_some = [&](int i) {
-                if (i % LOAD_EVERY == 0 && i / LOAD_EVERY < S::LOADS) load(i / LOAD_EVERY, next, buffers, places);
+                if (i % LOAD_EVERY) return;
+#pragma unroll
+                for (int k = i / LOAD_EVERY * LOADS_A_SLOT; k < (i / LOAD_EVERY + 1) * LOADS_A_SLOT; ++k)
+                    if (k < S::LOADS) load(k, next, buffers, places);
             };
             acc16_t s;
             Weights w;

@@ -1,7 +1,7 @@
 // latent_split.hpp -- how attention over a paged latent cache is split over workgroups, and the
 // joining of what is cut: shared by the kernels of the 16-bit (latent_attn.hip) and of the 8-bit
-// cache (latent_attn8.hip). S is a kernel's tile shape: S::ROWS query rows by S::TOKENS tokens, S::LATENT, and S::EXTRA, the
-// tiles that a batch's queries and results cost as much as.
+// cache (latent_attn8.hip). S is a kernel's tile shape: S::ROWS query rows by S::TOKENS tokens, S::LATENT, and
+// S::EXTRA, the tiles that a batch's queries and results cost as much as, but at most 1 / S::EXTRA_OF of a share.
 #pragma once
 
 #include "latent_device.hpp"
@@ -37,6 +37,11 @@ struct Header {
     int64_t share, pad;
     Start start[WORKGROUPS];
 };
+
+// a / b, of which a hardly ever needs 64 bits (the same in all lanes).
+__device__ __forceinline__ int64_t quotient(int64_t a, int b) {
+    return (uint64_t)a >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 struct Seq {
     int q0, few, len;    // first token of the call, tokens of the call, cached tokens
@@ -89,10 +94,10 @@ __device__ __forceinline__ int64_t find_unit(const AttnArgs &a, int64_t &share, 
             tiles += (int64_t)s.batches(a.members) * s.kv_tiles;
         }
     }
-    const int clusters = WORKGROUPS / a.members;
-    extra = (int)min(wave_sum(tiles) / clusters / 4, (int64_t)S::EXTRA);  // (none where a share is a few tiles)
+    const int clusters = WORKGROUPS / a.members, shift = __builtin_ctz(clusters);  // (a power of 2: 64-bit divisions take their time)
+    extra = (int)min((wave_sum(tiles) >> shift) / S::EXTRA_OF, (int64_t)S::EXTRA);  // (none where a share is a few tiles)
     const int64_t mine = tiles + batches * extra, upto = wave_prefix(mine, lane), total = __shfl(upto, 63);
-    share = (total + clusters - 1) / clusters;
+    share = (total + clusters - 1) >> shift;
     if (share < 1) share = 1;
     const int64_t at = cluster * share;
     b_out = -1;
