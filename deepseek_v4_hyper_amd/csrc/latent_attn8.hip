@@ -115,53 +115,6 @@ __device__ __forceinline__ uint32_t nan_bits8(u32x4_t w) {
     return (((w.x & REST) + ONE) | ((w.y & REST) + ONE) | ((w.z & REST) + ONE) | ((w.w & REST) + ONE)) & ~REST;
 }
 
-// ------------------------------------------------------------------ products of 8-bit values
-//
-// C[32 x 32] += A[32 x 64] B[64 x 32] of e4m3 values at twice the rate of 16-bit ones, each block of 32 along k
-// times a power of 2 of its row (A) or column (B). Lane l holds row or column l % 32; its bytes 0 .. 15 are of the
-// first block, whose power is that of the lane below 32, its bytes 16 .. 31 of the second, lanes from 32.
-// What a bfloat16 number has, 8 bits, two e4m3 numbers have together: x = hi + lo, where lo is hi's rounding error
-// exactly, if it is given a scale 2^-4 of hi's. So queries and weights go in as two numbers, at the rate of one
-// 16-bit product, and the cache's values as they are. Of a product's 64 terms those below 2^-13 of the largest
-// are cut off there by the matrix unit (measured: 2^-18 of the sum of magnitudes on average over normal values).
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef short s16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-
-// With C in vector registers, as mfma32_v; the wait for its results is that of the last instruction of a chain.
-// A times hi, then lo, of B.
-__device__ __forceinline__ void mfma64_first_v(i32x8_t a, i32x8_t hi, i32x8_t lo, acc16_t &c, int scale_a, int scale_hi, int scale_lo) {
-    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, 0, %4, %5 op_sel_hi:[0,0,0]\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %3, %0, %4, %6 op_sel_hi:[0,0,0]"
-        : "=&v"(c)
-        : "v"(a), "v"(hi), "v"(lo), "v"(scale_a), "v"(scale_hi), "v"(scale_lo));
-}
-__device__ __forceinline__ void mfma64_v(i32x8_t a, i32x8_t hi, i32x8_t lo, acc16_t &c, int scale_a, int scale_hi, int scale_lo) {
-    asm("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %4, %5 op_sel_hi:[0,0,0]\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %3, %0, %4, %6 op_sel_hi:[0,0,0]"
-        : "+&v"(c)
-        : "v"(a), "v"(hi), "v"(lo), "v"(scale_a), "v"(scale_hi), "v"(scale_lo));
-}
-__device__ __forceinline__ acc16_t mfma64(i32x8_t a, i32x8_t b, acc16_t c, int scale_a, int scale_b) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, scale_a, 0, scale_b);
-}
-__device__ __forceinline__ i32x8_t join8(u32x4_t a, u32x4_t b) { return i32x8_t{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w}; }
-
-// Scale byte that brings magnitudes up to `top` below 256 (with one 4 lower for what the rounding leaves), and its power.
-__device__ __forceinline__ int split_scale(float top) { return min(max((int)(__float_as_uint(top) >> 23) - 7, 5), 254); }
-__device__ __forceinline__ float power_of(int scale) { return __uint_as_float((uint32_t)scale << 23); }
-
-// Four numbers as hi and lo, a word each.
-__device__ __forceinline__ void split4(float a, float b, float c, float d, int scale, uint32_t &hi, uint32_t &lo) {
-    const float up = power_of(scale), down = power_of(scale - 4);
-    s16x2_t h = {0, 0}, l = {0, 0};
-    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, a, b, up, false);
-    h = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(h, c, d, up, true);
-    hi = __builtin_bit_cast(uint32_t, h);
-    const f32x2_t ab = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, up, false), cd = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, up, true);
-    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, a - ab.x, b - ab.y, down, false);
-    l = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(l, c - cd.x, d - cd.y, down, true);
-    lo = __builtin_bit_cast(uint32_t, l);
-}
-
 // SMALL: pages of fewer than 16 tokens, whose rows are looked up one by one.
 template <int DT, class S, bool SMALL>
 __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
@@ -225,10 +178,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         // steps 2 j and 2 j + 1, the others those behind: what a read of 16 bytes of a cached row gives.
         const int row0 = row_tile * S::ROWS + row_wave * 32;
         const int tok = min(row0 + (lane & 31), n_rows - 1) / a.heads;  // rows behind the last repeat it
-        // (8-bit products: lanes below 32 hold channels 64 k .. 64 k + 31 of step k as hi (q[4 k], q[4 k + 1]) and lo.)
-        constexpr bool EIGHT = DT == DT_BF16;
         u32x4_t q[S::KLATENT];
-        int scale_hi = 0, scale_lo = 0;
         u32x4_t rope[LATENT_ROPE / 16];
         auto load_queries = [&]() {  // (they are there once the block table's entries are, before the first tile's loads)
             const int head = min(row0 + (lane & 31), n_rows - 1) - tok * a.heads;
@@ -236,45 +186,15 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head + (lane >> 5) * 8;
 #pragma unroll
             for (int k = 0; k < S::KLATENT; ++k)
-                q[k] = *reinterpret_cast<const u32x4_t *>(EIGHT ? ql + (lane >> 5) * 16 + (k >> 2) * 64 + (k & 3) * 8 : ql + (k >> 1) * 32 + (k & 1) * 8);
+                q[k] = *reinterpret_cast<const u32x4_t *>(ql + (k >> 1) * 32 + (k & 1) * 8);
 #pragma unroll
             for (int k = 0; k < LATENT_ROPE / 16; ++k) rope[k] = *reinterpret_cast<const u32x4_t *>(qr + k * 16);
         };
-        auto split_queries = [&]() {
+        auto queries_loaded = [&]() {
 #pragma unroll
             for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);
 #pragma unroll
             for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane_here()] = rope[k];
-            if constexpr (EIGHT) {
-                // largest magnitude: bfloat16 bits without the sign are in the numbers' order (NaN last)
-                typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-                u16x2_t most2 = {0, 0};
-#pragma unroll
-                for (int k = 0; k < S::KLATENT; ++k)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) most2 = __builtin_elementwise_max(most2, __builtin_bit_cast(u16x2_t, q[k][i] & 0x7FFF7FFFu));
-                const float most = __uint_as_float((uint32_t)(most2.x > most2.y ? most2.x : most2.y) << 16);
-#pragma unroll
-                for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);  // (as new: the numbers above are not kept for what follows)
-                scale_hi = split_scale(max_halves(most));
-                scale_lo = scale_hi - 4;
-#pragma unroll
-                for (int k = 0; k < S::KLATENT; k += 4) {
-                    u32x4_t hi[2], lo[2];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w0 = q[k + i / 2][2 * (i & 1)], w1 = q[k + i / 2][2 * (i & 1) + 1];
-                        uint32_t h, l;
-                        split4(bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1), scale_hi, h, l);
-                        hi[i / 4][i & 3] = h;
-                        lo[i / 4][i & 3] = l;
-                    }
-                    q[k] = hi[0];
-                    q[k + 1] = hi[1];
-                    q[k + 2] = lo[0];
-                    q[k + 3] = lo[1];
-                }
-            }
         };
         float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
         float sum = 0.f;                    // of the weights
@@ -418,7 +338,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             // output; the others' chunks differ in higher bits, which an xor reaches. Made anew for
             // every tile: there are no registers to keep them.
             const int t0 = set * S::STEPS * 32;  // first token of the wave
-            const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + (((EIGHT ? 2 * lh : lh) ^ swz8<S::CHUNKS>(lr)) << 4);
+            const uint32_t k0 = (t0 + lr) * S::ROW_BYTES + ((lh ^ swz8<S::CHUNKS>(lr)) << 4);
             const uint32_t r0 = S::ROPE_AT + (t0 + lr) * 128 + ((lh ^ swz8_rope(lr)) << 4);
             const int vr = lh * 4 + ((l >> 1) & 3) + (l & 8);
             const uint32_t v0 = (t0 + vr) * S::ROW_BYTES + ((((l >> 4) & 1) ^ swz8<S::CHUNKS>(vr)) << 4) + (l & 1) * 8;
@@ -426,13 +346,12 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             // X^T = K Q^T of 32 tokens. A chain's first operands are read before it begins (begin_k), the others while it
             // runs; `between` gives other work to the vector unit while the matrix unit is busy.
             constexpr int ROPE_STEPS = LATENT_ROPE / 16;
-            constexpr int SLOTS_K = EIGHT ? S::LATENT / 64 + ROPE_STEPS : S::KSTEPS, SLOTS_V = EIGHT ? S::DBLOCKS : S::DBLOCKS * 2;  // places for other work
+            constexpr int SLOTS_K = S::KSTEPS, SLOTS_V = S::DBLOCKS * 2;  // places for other work
             constexpr int KREADS = S::LATENT / 32, KAHEAD = KREADS < 4 ? KREADS : 4;  // reads of 16 bytes a lane
             u32x4_t kx[KAHEAD];
             uint32_t scale_word;
             auto read_k = [&](int step, int i) {
-                const uint32_t at = EIGHT ? (k0 ^ ((i & 6) << 5) ^ ((i & 1) << 4)) : (k0 ^ ((i & 7) << 5));
-                return lds_read16(buf + at + (i >> 3) * 256 + step * 32 * S::ROW_BYTES);
+                return lds_read16(buf + (k0 ^ ((i & 7) << 5)) + (i >> 3) * 256 + step * 32 * S::ROW_BYTES);
             };
             auto begin_k = [&](int step) {
                 scale_word = scale_of_token(t0 + step * 32 + lr);
@@ -445,37 +364,20 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                     r[j & 1] = lds_read16(buf + (r0 ^ (j << 5)) + step * 32 * 128);
                     rq[j & 1] = rope_queries[wave][j][l];
                 };
-                if constexpr (EIGHT) {
-                    const int scale = scale_is_nan(scale_word) ? SCALE_NAN : scale_byte<DT>(scale_word);
-                    for_each<KREADS / 2>([&](auto nth) {
-                        constexpr int k = nth;
-                        const i32x8_t now = join8(kx[2 * k % KAHEAD], kx[(2 * k + 1) % KAHEAD]);
-                        if (k == 0) mfma64_first_v(now, join8(q[0], q[1]), join8(q[2], q[3]), s, scale, scale_hi, scale_lo);
-                        else mfma64_v(now, join8(q[4 * k], q[4 * k + 1]), join8(q[4 * k + 2], q[4 * k + 3]), s, scale, scale_hi, scale_lo);
-                        if (2 * k + KAHEAD < KREADS) {
-                            kx[2 * k % KAHEAD] = read_k(step, 2 * k + KAHEAD);
-                            kx[(2 * k + 1) % KAHEAD] = read_k(step, 2 * k + 1 + KAHEAD);
-                        }
-                        if (k == KREADS / 2 - 1) read_rope(0), read_rope(1);
-                        between(k);
-                        __builtin_amdgcn_sched_barrier(0);
-                    });
-                } else {
-                    const float unit_k = scale_of<DT>(scale_word);
-                    for_each<KREADS>([&](auto nth) {
-                        constexpr int i = nth;
-                        const u32x4_t now = kx[i % KAHEAD];
-                        if (i + KAHEAD < KREADS) kx[i % KAHEAD] = read_k(step, i + KAHEAD);
-                        if (i == KREADS - 1) read_rope(0), read_rope(1);
-                        const u32x4_t w0 = widen8<DT>(now.x, now.y, unit_k), w1 = widen8<DT>(now.z, now.w, unit_k);
-                        if (i == 0) mfma32_first_v<DT>(w0, q[0], s);
-                        else mfma32_v<DT>(w0, q[2 * i], s);
-                        between(2 * i);
-                        mfma32_v<DT>(w1, q[2 * i + 1], s);
-                        between(2 * i + 1);
-                        __builtin_amdgcn_sched_barrier(0);
-                    });
-                }
+                const float unit_k = scale_of<DT>(scale_word);
+                for_each<KREADS>([&](auto nth) {
+                    constexpr int i = nth;
+                    const u32x4_t now = kx[i % KAHEAD];
+                    if (i + KAHEAD < KREADS) kx[i % KAHEAD] = read_k(step, i + KAHEAD);
+                    if (i == KREADS - 1) read_rope(0), read_rope(1);
+                    const u32x4_t w0 = widen8<DT>(now.x, now.y, unit_k), w1 = widen8<DT>(now.z, now.w, unit_k);
+                    if (i == 0) mfma32_first_v<DT>(w0, q[0], s);
+                    else mfma32_v<DT>(w0, q[2 * i], s);
+                    between(2 * i);
+                    mfma32_v<DT>(w1, q[2 * i + 1], s);
+                    between(2 * i + 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
                 for_each<ROPE_STEPS>([&](auto nth) {
                     constexpr int j = nth;
                     mfma32_v<DT>(r[j & 1], rq[j & 1], s);
@@ -484,55 +386,26 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                     __builtin_amdgcn_sched_barrier(0);
                 });
             };
-            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of X^T's rows, for both operands. 8-bit
-            // products: the weights' hi in the first block of k, their lo in the second, the values in both.
+            // O^T += V^T P^T of 32 tokens; the order of the tokens is that of X^T's rows, for both operands
             constexpr int VREADS = S::DBLOCKS * 2, VAHEAD = VREADS < 4 ? VREADS : 4;
-            u32x2_t vx[VAHEAD], again[VAHEAD];  // (8-bit products: read twice, in place of copies in the vector unit)
-            struct Weights {
-                u32x4_t p[2];
-                int scale;  // 8-bit products: of the lane's block
-            };
-            const uint32_t v0_again = here(v0);  // (an address that the compiler does not take for the same)
-            auto read_v = [&](int step, int i, uint32_t v0) {  // block i / 2, tokens 16 (i % 2) .. + 15
+            u32x2_t vx[VAHEAD];
+            auto read_v = [&](int step, int i) {  // block i / 2, tokens 16 (i % 2) .. + 15
                 const int d = i / 2;
                 return lds_read_tr8(buf + (v0 ^ ((d & 7) << 5)) + (d >> 3) * 256 + (step * 32 + (i & 1) * 16) * S::ROW_BYTES);
             };
             auto begin_v = [&](int step) {
 #pragma unroll
-                for (int i = 0; i < VAHEAD; ++i) {
-                    vx[i] = read_v(step, i, v0);
-                    if constexpr (EIGHT) again[i] = read_v(step, i, v0_again);
-                }
+                for (int i = 0; i < VAHEAD; ++i) vx[i] = read_v(step, i);
             };
-            auto products_v = [&](int step, const Weights &w, auto &&between) {
-                if constexpr (EIGHT) {
-                    const i32x8_t p = join8(w.p[0], w.p[1]);
-                    int one = 127;
-                    asm("" : "+v"(one));
-                    for_each<S::DBLOCKS>([&](auto nth) {
-                        constexpr int d = nth;
-                        constexpr int x = 2 * d % VAHEAD, y = (2 * d + 1) % VAHEAD;
-                        acc[d] = mfma64(join8(u32x4_t{vx[x].x, vx[x].y, vx[y].x, vx[y].y}, u32x4_t{again[x].x, again[x].y, again[y].x, again[y].y}), p,
-                                        acc[d], one, w.scale);
-                        if (2 * d + VAHEAD < VREADS) {
-                            vx[x] = read_v(step, 2 * d + VAHEAD, v0);
-                            vx[y] = read_v(step, 2 * d + 1 + VAHEAD, v0);
-                            again[x] = read_v(step, 2 * d + VAHEAD, v0_again);
-                            again[y] = read_v(step, 2 * d + 1 + VAHEAD, v0_again);
-                        }
-                        between(d);
-                        __builtin_amdgcn_sched_barrier(0);
-                    });
-                } else {
-                    for_each<VREADS>([&](auto nth) {
-                        constexpr int i = nth;
-                        const u32x4_t a = widen8<DT>(vx[i % VAHEAD].x, vx[i % VAHEAD].y, 1.f);
-                        acc[i / 2] = mfma32<DT>(a, w.p[i & 1], acc[i / 2]);
-                        if (i + VAHEAD < VREADS) vx[i % VAHEAD] = read_v(step, i + VAHEAD, v0);
-                        between(i);
-                        __builtin_amdgcn_sched_barrier(0);
-                    });
-                }
+            auto products_v = [&](int step, const u32x4_t (&p)[2], auto &&between) {
+                for_each<VREADS>([&](auto nth) {
+                    constexpr int i = nth;
+                    const u32x4_t a = widen8<DT>(vx[i % VAHEAD].x, vx[i % VAHEAD].y, 1.f);
+                    acc[i / 2] = mfma32<DT>(a, p[i & 1], acc[i / 2]);
+                    if (i + VAHEAD < VREADS) vx[i % VAHEAD] = read_v(step, i + VAHEAD);
+                    between(i);
+                    __builtin_amdgcn_sched_barrier(0);
+                });
             };
             // Softmax of a step, in pieces. The mask, and the largest logit (of the lane's row).
             uint64_t sees = ~0ull;
@@ -575,38 +448,27 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 }
                 return keep;
             };
-            // Weights times their tokens' powers of 2, as the second product takes them, in pieces: 8 of two weights,
-            // then (8-bit products) the scale and four words.
-            constexpr int PIECES = EIGHT ? 13 : 8;
-            int scale_p = 0;
+            // Weights 2 i and 2 i + 1 times their tokens' powers of 2, rounded to the type that the second product takes. (The
+            // sum is that of the weights before the rounding: a rounded weight's share of it would have to be found
+            // from its product with the power, at 6 instructions for two, and an error of 1.25 times that of
+            // float32 weights would become 1.0.)
+            constexpr int PIECES = 8;
             acc4_t powers2[2];  // read ahead
             auto read_powers = [&](int step, int k) { powers2[k & 1] = *reinterpret_cast<const acc4_t *>(&units[wave][at_token + step * 32 + 8 * k]); };
-            auto weigh = [&](int step, acc16_t &s, int i, Weights &w) {
-                if (i < 8) {
-                    const float u[2] = {powers2[i / 2 & 1][2 * (i & 1)], powers2[i / 2 & 1][2 * (i & 1) + 1]};
-                    if ((i & 1) && i / 2 + 2 < 4) read_powers(step, i / 2 + 2);
-                    if constexpr (DT == DT_F16) {
-                        const float e0 = exp2_fast(s[2 * i] - from), e1 = exp2_fast(s[2 * i + 1] - from);
-                        auto inverse = [](float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); };
-                        sum = fmaf(e0, inverse(u[0]), sum);
-                        sum = fmaf(e1, inverse(u[1]), sum);
-                        w.p[i >> 2][i & 3] = pack2<DT>(e0, e1);
-                    } else {
-                        const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
-                        sum += e0;
-                        sum += e1;
-                        if constexpr (EIGHT) s[2 * i] = e0 * u[0], s[2 * i + 1] = e1 * u[1];
-                        else w.p[i >> 2][i & 3] = pack2<DT>(e0 * u[0], e1 * u[1]);
-                    }
-                } else if (i == 8) {
-                    scale_p = split_scale(max_halves(max16(s)));
-                    w.scale = lane_here() < 32 ? scale_p : scale_p - 4;
+            auto weigh = [&](int step, const acc16_t &s, int i, u32x4_t (&p)[2]) {
+                const float u[2] = {powers2[i / 2 & 1][2 * (i & 1)], powers2[i / 2 & 1][2 * (i & 1) + 1]};
+                if ((i & 1) && i / 2 + 2 < 4) read_powers(step, i / 2 + 2);
+                if constexpr (DT == DT_F16) {
+                    const float e0 = exp2_fast(s[2 * i] - from), e1 = exp2_fast(s[2 * i + 1] - from);
+                    auto inverse = [](float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); };
+                    sum = fmaf(e0, inverse(u[0]), sum);
+                    sum = fmaf(e1, inverse(u[1]), sum);
+                    p[i >> 2][i & 3] = pack2<DT>(e0, e1);
                 } else {
-                    const int k = i - 9;
-                    uint32_t hi, lo;
-                    split4(s[4 * k], s[4 * k + 1], s[4 * k + 2], s[4 * k + 3], scale_p, hi, lo);
-                    w.p[0][k] = hi;
-                    w.p[1][k] = lo;
+                    const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
+                    sum += e0;
+                    sum += e1;
+                    p[i >> 2][i & 3] = pack2<DT>(e0 * u[0], e1 * u[1]);
                 }
             };
             constexpr int SLOTS = SLOTS_K * S::STEPS + SLOTS_V, LOAD_EVERY = SLOTS > S::LOADS ? SLOTS / S::LOADS : 1, LOADS_A_SLOT = (S::LOADS + SLOTS - 1) / SLOTS;
@@ -620,7 +482,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                     if (k < S::LOADS) load(k, next, buffers, places);
             };
             acc16_t s;
-            Weights w;
+            u32x4_t p[2];
             begin_k(0);
             __builtin_amdgcn_sched_barrier(0);
             constexpr int LATE = SLOTS_K - ROPE_STEPS;  // the chain's latents have been read
@@ -634,11 +496,11 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 const float high = largest(0, s);
                 if (__any(too_high(high))) raise(high);
 #pragma unroll
-                for (int i = 0; i < PIECES; ++i) weigh(0, s, i, w);
-                products_v(0, w, [&](int i) { load_some(SLOTS_K + i); });
+                for (int i = 0; i < PIECES; ++i) weigh(0, s, i, p);
+                products_v(0, p, [&](int i) { load_some(SLOTS_K + i); });
             } else {  // two steps, the softmax of each beside the products of the other, as far as can be
                 acc16_t s1;
-                Weights w1;
+                u32x4_t p1[2];
                 products_k(0, s, [&](int i) {
                     load_some(i);
                     if (i == LATE) begin_k(1);
@@ -650,26 +512,24 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 products_k(1, s1, [&](int i) {
                     load_some(SLOTS_K + i);
 #pragma unroll
-                    for (int k = i * PIECES / SLOTS_K; k < (i + 1) * PIECES / SLOTS_K; ++k) weigh(0, s, k, w);
+                    for (int k = i * PIECES / SLOTS_K; k < (i + 1) * PIECES / SLOTS_K; ++k) weigh(0, s, k, p);
                     if (i == LATE) begin_v(0);
                     if (i == SLOTS_K - 1) read_powers(1, 0), read_powers(1, 1);
                 });
                 mfma_results(s1);
                 high = largest(1, s1);
                 if (__any(too_high(high))) {
-                    const float was = top, keep = raise(high);
-                    if constexpr (EIGHT) w.scale = max(w.scale + (int)fmaxf(was - top, -300.f), 1);
-                    else
+                    const float keep = raise(high);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) w.p[i >> 2][i & 3] = scale2_words<DT>(w.p[i >> 2][i & 3], keep);
+                    for (int i = 0; i < 8; ++i) p[i >> 2][i & 3] = scale2_words<DT>(p[i >> 2][i & 3], keep);
                 }
-                products_v(0, w, [&](int i) {
+                products_v(0, p, [&](int i) {
                     load_some(2 * SLOTS_K + i);
 #pragma unroll
-                    for (int k = i * PIECES / SLOTS_V; k < (i + 1) * PIECES / SLOTS_V; ++k) weigh(1, s1, k, w1);
+                    for (int k = i * PIECES / SLOTS_V; k < (i + 1) * PIECES / SLOTS_V; ++k) weigh(1, s1, k, p1);
                 });
                 begin_v(1);
-                products_v(1, w1, [](int) {});
+                products_v(1, p1, [](int) {});
             }
         };
 
@@ -687,7 +547,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         buffers_of(next, n > 1, buffers);
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i) load(i, next, buffers, place(ring_at + S::TILE_BYTES));
-        split_queries();
+        queries_loaded();
         uint64_t ok = now.ok, ok_next = next.ok;
         uint32_t at = 0;
         for (int i = 0; i < n; ++i) {
