@@ -848,13 +848,13 @@ def ds4hc_pages_workspace_bytes(pool: PagePool, n: int) -> int:
     return int(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), int(n)))
 
 
-def _own_scratch(need, workspace, here):
+def _own_scratch(need, workspace, here, device):
     """The caller's workspace looked at, or a fresh one."""
     if workspace is not None:
         _tensors(workspace=workspace)
         if workspace.get_device() != here or not workspace.is_contiguous():
             raise ValueError("workspace must be a dense array on the call's device")
-    return _scratch(need, workspace, f"cuda:{here}")
+    return _scratch(need, workspace, device)
 
 
 def ds4hc_draft_verify(target, tokens, cu_q, uniform, *, draft=None, parents=None, path=None, n_kept=None,
@@ -900,7 +900,7 @@ def ds4hc_draft_verify(target, tokens, cu_q, uniform, *, draft=None, parents=Non
             next_token = _empty((B,), torch.int64, target.device)
         else:
             _dense(next_token, (B,), torch.int64, "next_token", here)
-        workspace, ws_bytes = _own_scratch(load().ds4hc_draft_verify_workspace_bytes(B, vocab), workspace, here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_draft_verify_workspace_bytes(B, vocab), workspace, here, target.device)
     row = lambda t: t.stride(0) if N > 1 else vocab  # noqa: E731
     st = load().ds4hc_draft_verify(N, B, vocab, target.data_ptr(), row(target), None if draft is None else draft.data_ptr(),
                                    0 if draft is None else row(draft), tokens.data_ptr(),
@@ -1002,7 +1002,7 @@ def ds4hc_pages_resize(block_table, kv_len, refs, page_size, slots, lengths, *, 
             status = _empty((n,), i32, refs.device)
         else:
             _dense(status, (n,), i32, "status", here)
-        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here, refs.device)
     st = load().ds4hc_pages_resize(ctypes.byref(pool), n, slots.data_ptr(), lengths.data_ptr(), copies.data_ptr(),
                                    status.data_ptr(), None if workspace is None else workspace.data_ptr(), ws_bytes,
                                    _raw_stream(stream, here))
@@ -1027,7 +1027,7 @@ def ds4hc_pages_fork(block_table, kv_len, refs, page_size, parents, children, *,
             status = _empty((n,), i32, refs.device)
         else:
             _dense(status, (n,), i32, "status", here)
-        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here)
+        workspace, ws_bytes = _own_scratch(load().ds4hc_pages_workspace_bytes(ctypes.byref(pool), n), workspace, here, refs.device)
     st = load().ds4hc_pages_fork(ctypes.byref(pool), n, parents.data_ptr(), children.data_ptr(), status.data_ptr(),
                                  None if workspace is None else workspace.data_ptr(), ws_bytes, _raw_stream(stream, here))
     if st:
