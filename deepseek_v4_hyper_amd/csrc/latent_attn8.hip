@@ -122,7 +122,8 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
     __shared__ uint32_t not_finite[2];
     __shared__ __align__(16) u32x4_t rope_queries[S::WAVES][LATENT_ROPE / 16][64];  // (no registers are left for them)
     __shared__ __align__(16) float units[S::WAVES][S::TOKENS];  // the tile's powers of 2, each wave's own copy
-    __shared__ __align__(16) float powers[DT == DT_F16 ? S::WAVES : 1][S::TOKENS];  // their exponents
+    __shared__ __align__(16) float powers[DT == DT_F16 ? S::WAVES : 1][S::TOKENS];  // float16: their exponents
+    __shared__ __align__(16) uint16_t inverses[DT == DT_BF16 ? S::WAVES : 1][S::TOKENS];  // bfloat16: one over them
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int row_wave = wave % S::ROW_WAVES, set = wave / S::ROW_WAVES;
     // clusters in the order of the work run on one XCD
@@ -197,7 +198,8 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane_here()] = rope[k];
         };
         float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
-        float sum = 0.f;                    // of the weights
+        float sum = 0.f, used = 0.f;        // of the weights, and of the weights as they were rounded
+        int least = 255, most = 0;          // float16: scale bytes so far
         acc16_t acc[S::DBLOCKS];
 #pragma unroll
         for (int d = 0; d < S::DBLOCKS; ++d) {
@@ -333,7 +335,21 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             const int l = lane_here(), lr = l & 31, lh = l >> 5;
             const uint32_t own_scale = scale_of_token(l);
             units[wave][l] = scale_of<DT>(own_scale);
-            if constexpr (DT == DT_F16) powers[wave][l] = scale_is_nan(own_scale) ? NAN : (float)(scale_byte<DT>(own_scale) - 127);
+            if constexpr (DT == DT_BF16) inverses[wave][l] = (uint16_t)((254 - scale_byte<DT>(own_scale)) << 7);
+            if constexpr (DT == DT_F16) {
+                powers[wave][l] = scale_is_nan(own_scale) ? NAN : (float)(scale_byte<DT>(own_scale) - 127);
+                const int byte = scale_byte<DT>(own_scale);
+                const bool counts = (ok >> l) & 1 && !scale_is_nan(own_scale);
+                if (__ballot(counts && (byte < least || byte > most))) {
+                    int lo = counts ? byte : 255, hi = counts ? byte : 0;
+                    for (int m = 32; m; m >>= 1) {
+                        lo = min(lo, __shfl_xor(lo, m));
+                        hi = max(hi, __shfl_xor(hi, m));
+                    }
+                    least = uniform(min(least, lo));
+                    most = uniform(max(most, hi));
+                }
+            }
             // LDS offsets of this lane's reads for the first k step, rope step and block of the
             // output; the others' chunks differ in higher bits, which an xor reaches. Made anew for
             // every tile: there are no registers to keep them.
@@ -438,6 +454,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 from = top == -INFINITY ? 0.f : top;
                 const float keep = was == -INFINITY ? 0.f : exp2_fast(was - top);
                 sum *= keep;
+                used *= keep;
                 if (__any(was != -INFINITY)) {  // (the first maximum: the sums are 0)
 #pragma unroll
                     for (int d = 0; d < S::DBLOCKS; ++d) {
@@ -448,27 +465,38 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
                 }
                 return keep;
             };
-            // Weights 2 i and 2 i + 1 times their tokens' powers of 2, rounded to the type that the second product takes. (The
-            // sum is that of the weights before the rounding: a rounded weight's share of it would have to be found
-            // from its product with the power, at 6 instructions for two, and an error of 1.25 times that of
-            // float32 weights would become 1.0.)
+            // Weights 2 i and 2 i + 1 times their tokens' powers of 2, rounded to the type that the second product takes, and
+            // what is left of the weights themselves after that: a row is divided by their sum.
             constexpr int PIECES = 8;
-            acc4_t powers2[2];  // read ahead
-            auto read_powers = [&](int step, int k) { powers2[k & 1] = *reinterpret_cast<const acc4_t *>(&units[wave][at_token + step * 32 + 8 * k]); };
+            acc4_t powers2[2];  // read ahead, and in bfloat16 one over them
+            u32x2_t over[2];
+            auto read_powers = [&](int step, int k) {
+                powers2[k & 1] = *reinterpret_cast<const acc4_t *>(&units[wave][at_token + step * 32 + 8 * k]);
+                if constexpr (DT == DT_BF16) over[k & 1] = *reinterpret_cast<const u32x2_t *>(&inverses[wave][at_token + step * 32 + 8 * k]);
+            };
             auto weigh = [&](int step, const acc16_t &s, int i, u32x4_t (&p)[2]) {
                 const float u[2] = {powers2[i / 2 & 1][2 * (i & 1)], powers2[i / 2 & 1][2 * (i & 1) + 1]};
+                const uint32_t over2 = DT == DT_BF16 ? over[i / 2 & 1][i & 1] : 0;
                 if ((i & 1) && i / 2 + 2 < 4) read_powers(step, i / 2 + 2);
                 if constexpr (DT == DT_F16) {
                     const float e0 = exp2_fast(s[2 * i] - from), e1 = exp2_fast(s[2 * i + 1] - from);
                     auto inverse = [](float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); };
-                    sum = fmaf(e0, inverse(u[0]), sum);
-                    sum = fmaf(e1, inverse(u[1]), sum);
-                    p[i >> 2][i & 3] = pack2<DT>(e0, e1);
+                    const float o0 = inverse(u[0]), o1 = inverse(u[1]);
+                    sum = fmaf(e0, o0, sum);
+                    sum = fmaf(e1, o1, sum);
+                    const uint32_t both = pack2<DT>(e0, e1);
+                    asm("v_fma_mix_f32 %0, %1, %2, %0 op_sel_hi:[1,0,0]\n\tv_fma_mix_f32 %0, %1, %3, %0 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+                        : "+&v"(used)
+                        : "v"(both), "v"(o0), "v"(o1));
+                    p[i >> 2][i & 3] = both;
                 } else {
+                    typedef __bf16 b2_t __attribute__((ext_vector_type(2)));
                     const float e0 = exp2_fast(fmaf(s[2 * i], scale2, -from)), e1 = exp2_fast(fmaf(s[2 * i + 1], scale2, -from));
                     sum += e0;
                     sum += e1;
-                    p[i >> 2][i & 3] = pack2<DT>(e0 * u[0], e1 * u[1]);
+                    const uint32_t both = pack2<DT>(e0 * u[0], e1 * u[1]);
+                    used = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(b2_t, both), __builtin_bit_cast(b2_t, over2), used, false);
+                    p[i >> 2][i & 3] = both;
                 }
             };
             constexpr int SLOTS = SLOTS_K * S::STEPS + SLOTS_V, LOAD_EVERY = SLOTS > S::LOADS ? SLOTS / S::LOADS : 1, LOADS_A_SLOT = (S::LOADS + SLOTS - 1) / SLOTS;
@@ -567,7 +595,10 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         const bool whole = t_first == 0 && n == sq.kv_tiles, mine = my_row < n_rows;  // (a part's rows behind the last: never looked at)
         const int in = my_row - row_tile * S::ROWS;
         float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);
-        float all = sum_halves(sum);
+        // In float16 a token whose power is far below the others' may keep nothing of a weight that counts, so where they
+        // differ by more than 2^6 the sum before the rounding is what divides.
+        if (DT == DT_F16 && most - least > 6) used = sum;
+        float all = sum_halves(sum), all_used = sum_halves(used);
         // the blocks of the output that this wave finishes: all, or with two sets its half
         constexpr int BLOCKS = S::BLOCKS, BLOCK_BYTES = S::BLOCK_BYTES;
         acc16_t fin[BLOCKS];
@@ -577,7 +608,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             wait_and_barrier<63>();  // the last tile has been read by all
         } else {
             // each set gives the other one's half through LDS, and all is brought to the common maximum
-            float *st = reinterpret_cast<float *>(ring + S::WAVES * BLOCKS * BLOCK_BYTES);  // maximum, sum [row waves][sets][32]
+            float *st = reinterpret_cast<float *>(ring + S::WAVES * BLOCKS * BLOCK_BYTES);  // maximum, sums [row waves][sets][32]
             char *give = ring + (row_wave * 2 + set) * BLOCKS * BLOCK_BYTES + l * 16, *take = ring + (row_wave * 2 + 1 - set) * BLOCKS * BLOCK_BYTES + l * 16;
             float *mine_st = st + (row_wave * 2 + set) * 96, *other_st = st + (row_wave * 2 + 1 - set) * 96;
             auto give_half = [&](auto from) {
@@ -593,6 +624,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             if (lh == 0) {
                 mine_st[l] = top;
                 mine_st[32 + l] = all;
+                mine_st[64 + l] = all_used;
             }
             if (set == 0) give_half(std::integral_constant<int, BLOCKS>{});
             else give_half(std::integral_constant<int, 0>{});
@@ -601,6 +633,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             // (no logit that is a number, -infinity: the sums are 0 or NaN)
             const float keep = to == -INFINITY ? 1.f : exp2_fast(top - to), add = to == -INFINITY ? 1.f : exp2_fast(other - to);
             all = all * keep + other_st[32 + (l & 31)] * add;
+            all_used = all_used * keep + other_st[64 + (l & 31)] * add;
             top = to;
             auto take_half = [&](auto from) {
 #pragma unroll
@@ -617,7 +650,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         }
         const int block0 = (S::SETS - 1) * set * BLOCKS;
         if (whole) {
-            const float inv = all == 0.f ? 0.f : 1.f / all;
+            const float inv = all_used == 0.f ? 0.f : 1.f / all_used;
             if (a.lse && set == 0 && lh == 0 && mine) a.lse[(int64_t)q0 * a.heads + my_row] = row_lse<DT>(top, all);
             // through LDS, to store whole rows: chunk c of row r at chunk c ^ (r % 16), in the wave's own place
             // (with two sets in what it has just read)
@@ -640,7 +673,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             if (lh == 0 && set == 0) {
                 part[S::ROWS * S::LATENT + in] = top;
                 part[S::ROWS * (S::LATENT + 1) + in] = all;
-                part[S::ROWS * (S::LATENT + 2) + in] = all;
+                part[S::ROWS * (S::LATENT + 2) + in] = all_used;
             }
             float *o = part + ((row_wave * S::DBLOCKS + block0) * 256 + l) * 4;
 #pragma unroll
