@@ -15,7 +15,8 @@ constexpr int AT_ONCE = 8;  // rows in flight
 // A thread takes the same 16 bytes of every row of a sequence, in one layer, and moves them in the order of
 // the kept tokens: `keep` rises, so what it reads was written by none of its own earlier moves (the source lies
 // at or behind the target, and in front of all later sources), and nobody else touches its bytes. AT_ONCE loads are
-// issued before their stores. Grid (layers x columns, sequences).
+// issued before their stores. Grid (layers x columns, sequences). 64 sequences, up to 8 rows of 656 bytes in 43 layers:
+// 5.0 us, 3.3 TB/s; one sequence and layer 2.6 us.
 __global__ __launch_bounds__(THREADS) void compact_kernel(CompactArgs a) {
     __shared__ int from[64], to[64];
     const int b = blockIdx.y, n = (int)a.N;
@@ -55,7 +56,8 @@ __global__ __launch_bounds__(THREADS) void compact_kernel(CompactArgs a) {
     }
 }
 
-// Grid (pieces of a page, layers, pairs); a workgroup a piece of COPY bytes.
+// Grid (pieces of a page, layers, pairs); a workgroup a piece of COPY bytes. 64 pages of 42 KB in 43 layers: 36 us, 6.4 TB/s
+// (part of what is read is still in the last cache).
 constexpr int COPY = THREADS * 16 * 4;
 __global__ __launch_bounds__(THREADS) void copy_kernel(Store s, int n, const int32_t *pairs) {
     const int64_t page_bytes = s.row_bytes << s.page_shift;
@@ -79,7 +81,9 @@ __global__ __launch_bounds__(THREADS) void copy_kernel(Store s, int n, const int
 
 // Two kernels: the first, one workgroup, finds what each item needs and the free pages in ascending order; the
 // second writes tables and counts, all items side by side. Counts change by whole-number atomics alone, in the
-// second kernel, so that results do not depend on an order.
+// second kernel, so that results do not depend on an order. 64 slots with up to 128 pages each, of 65536: 8.0 and
+// 3.3 us, chains of latencies. (Both in one kernel, a wave an item: 16 slots with 16 pages 7.2 for 8.4 us, 64 with 16
+// 11.3 for 9.1, 256 with 128 37 for 14.)
 constexpr int DECIDE = 1024, WAVES = DECIDE / 64;
 constexpr int SCAN = 16;  // pages a lane: 1024 a wave, 16384 a step of the workgroup
 

@@ -521,8 +521,11 @@ ds4hc_status ds4hc_latent_append8(const ds4hc_paged_cache *c, int64_t N, ds4hc_d
  * lengths, workspace and limits, with c_j = c8 * 2^(s - 127). Scale bytes outside 10..246 are
  * taken as the nearest of these, and 255 as a token that is NaN; a token with a NaN makes
  * the rows that see it not finite, in some of their elements at least.
- * Products are of 16-bit values (float16: as far as its range goes) and sums float32. The weight
- * times the token's power of 2 is rounded to 16 bits for the second product.
+ * Products are of 16-bit values (the cached ones exact in bfloat16, in float16 as far as its range
+ * goes: beyond 65504 infinite, below 2^-24 gone) and sums float32. A weight times its token's power of
+ * 2 is rounded to 16 bits for the second product, and the row divided by the sum of the weights as that
+ * leaves them (in float16 only where a row's powers lie within 2^6 of one another); the rest as for
+ * ds4hc_latent_attn.
  */
 ds4hc_status ds4hc_latent_attn8(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
                                 const void *q_latent, ds4hc_strides q_latent_strides,
