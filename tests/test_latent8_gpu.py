@@ -363,3 +363,140 @@ def test_attn8_in_a_graph_follows_the_lengths():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got.view(torch.int16), out.view(torch.int16)) and torch.equal(got_lse, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,latent,page,q_len,kv_len", [
+    (16, 512, 4, [2, 1], [333, 150]), (128, 512, 8, [1], [1000]), (64, 256, 8, [1, 3], [64, 129]), (16, 128, 2, [5], [400]),
+    (128, 512, 1, [2], [200])])
+def test_attn8_small_pages(dtype, heads, latent, page, q_len, kv_len):
+    """Pages of fewer than 16 tokens over several tiles, one of them missing."""
+    bt = Batch8(73, q_len, kv_len, page, latent, dtype)
+    ql, qr = bt.queries(heads)
+    table = bt.table.clone()
+    table[0, 70 // page] = -1
+    tree = random_tree(bt.g, q_len, 1)
+    for mask in (None, tree):
+        out, lse = run_attn8(bt, ql, qr, 0.07, mask, table=table)
+        check_attn8(bt, ql, qr, 0.07, out, lse, mask, holes=[(0, 70 // page)])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads", [1, 40, 128])
+def test_attn8_one_token_seen_gives_its_values(dtype, heads):
+    """A row that sees one token alone has its values, whatever its logit and power of 2 are: the rounded weight's product with
+    a value of 4 bits is exact, and the quotient by the same weight off by roundings of float32, which the rounding to 16 bits
+    takes back to the value."""
+    bt = Batch8(79, [1] * 9, [1] * 9, 16, 512, dtype, spread=3)
+    ql, qr = bt.queries(heads, 3.0)
+    out, lse = run_attn8(bt, ql, qr, 0.3)
+    for b in range(9):
+        want = bt.cache.view(-1, 576)[bt.rows(b, 1)[0], :512].to(dtype)
+        assert torch.equal(out[b].cpu(), want.expand(heads, 512))
+    check_attn8(bt, ql, qr, 0.3, out, lse)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads,kv_len", [(16, 300), (128, 300), (64, 6000)])
+def test_attn8_logits_of_minus_infinity(dtype, heads, kv_len):
+    """Tokens whose rotated key is infinite against the queries' sign weigh nothing, whole tiles and parts of them, too: as if
+    their pages were missing."""
+    bt = Batch8(83, [1], [kv_len], 64, 512, dtype)
+    ql, qr = bt.queries(heads)
+    qr[..., 5] = 1 + qr[..., 5].abs()
+    pages = [0, 1, 2, 4] if kv_len < 1000 else list(range(40)) + list(range(50, 60)) + [93]
+    for p in pages:
+        keys = bt.rows8[bt.table[0, p].long(), :, 512:640].view(dtype).clone()
+        keys[:, 5] = -math.inf
+        bt.rows8[bt.table[0, p].long(), :, 512:640] = keys.view(torch.uint8)
+    out, lse = run_attn8(bt, ql, qr, 0.07)
+    check_attn8(bt, ql, qr, 0.07, out, lse, holes=[(0, p) for p in pages])
+
+
+def test_attn8_results_of_more_than_2_to_the_31_elements():
+    """40000 sequences of one token, 128 heads: queries and results behind 2^31 elements, and 2^32 bytes."""
+    n, page = 40000, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = torch.zeros(n, page, 656, dtype=torch.uint8, device="cuda")
+    cache[:, 0, :512] = torch.randint(0, 120, (n, 512), generator=g, dtype=torch.uint8, device="cuda")
+    cache[:, 0, 640] = 127
+    q = torch.randn(n, 128, 512, generator=g, dtype=BF, device="cuda")
+    r = torch.randn(n, 128, 64, generator=g, dtype=BF, device="cuda")
+    assert q.numel() > 2 ** 31
+    table = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    out, _ = B.ds4hc_latent_attn8(q, r, cache, torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+                                  torch.ones(n, dtype=torch.int32, device="cuda"), table, scale=0.05)
+    for t in (0, 1, 20000, 32767, 32768, 39998, 39999):
+        want = cache[table[t, 0].item(), 0, :512].view(torch.float8_e4m3fn).to(BF)
+        assert torch.equal(out[t], want.expand(128, 512)), t
+
+
+def test_attn8_two_at_once():
+    """Calls side by side on two streams, each with the workspace that it was given: as one after another."""
+    both = []
+    for seed, heads in ((89, 16), (97, 128)):
+        bt = Batch8(seed, [1, 2], [3000, 900], 64, 512)
+        ql, qr = bt.queries(heads)
+        both.append([t.cuda() for t in (ql, qr, bt.rows8, bt.cu, bt.lens, bt.table)])
+    want = [B.ds4hc_latent_attn8(*a, scale=0.07, want_lse=True) for a in both]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [B.ds4hc_latent_attn8(*a, scale=0.07, want_lse=True, stream=s) for a, s in zip(both, streams)]
+        torch.cuda.synchronize()
+        for (o, l), (o2, l2) in zip(got, want):
+            assert torch.equal(o.view(torch.int16), o2.view(torch.int16)) and torch.equal(l, l2)
+
+
+def test_attn8_two_graphs_share_a_workspace():
+    """Two captured calls of unlike sizes with one workspace, replayed in turn on one stream with eager work between."""
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for seed, heads, kv in ((101, 16, 2000), (103, 128, 700)):
+        bt = Batch8(seed, [1, 2], [kv, 900], 64, 512)
+        ql, qr = bt.queries(heads)
+        a = [t.cuda() for t in (ql, qr, bt.rows8, bt.cu, bt.lens, bt.table)]
+        want = B.ds4hc_latent_attn8(*a, scale=0.07)[0]
+        out = torch.zeros_like(want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            B.ds4hc_latent_attn8(*a, scale=0.07, out=out, workspace=ws)
+        graphs.append((graph, out, want, a))
+    for _ in range(3):
+        for graph, out, want, a in graphs:
+            graph.replay()
+        for graph, out, want, a in graphs:
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+            out.zero_()
+            B.ds4hc_latent_attn8(*a, scale=0.07, workspace=ws)
+
+
+def test_refusals_of_the_binding():
+    bt = Batch8(107, [1, 1], [5, 9], 16, 512)
+    ql, qr = (t.cuda() for t in bt.queries(4))
+    cache, cu, lens, table = (t.cuda() for t in (bt.rows8, bt.cu, bt.lens, bt.table))
+    ok = dict(scale=0.1)
+    kv, pos, f = torch.zeros(2, 576, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda"), B.ds4hc_rope_frequencies(64)[0].cuda()
+    for call in (lambda: B.ds4hc_latent_attn8(ql.float(), qr.float(), cache, cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr.half(), cache, cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache.view(torch.int8), cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache, cu.long(), lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache, cu, lens, table, lse=torch.zeros(2, 4, device="cuda", dtype=BF), **ok),
+                 lambda: B.ds4hc_latent_append8(kv, pos, f, cache, cu, lens, table, dtype=F32),
+                 lambda: B.ds4hc_latent_append8(kv, pos.int(), f, cache, cu, lens, table)):
+        with pytest.raises((TypeError, ValueError)):
+            call()
+    for call in (lambda: B.ds4hc_latent_attn8(ql[..., :256], qr, cache, cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache[:, :, :640], cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache, cu, lens.cpu(), table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql.cpu(), qr, cache, cu, lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache, cu[:2], lens, table, **ok),
+                 lambda: B.ds4hc_latent_attn8(ql, qr, cache, cu, lens, table, tree_mask=torch.zeros(1, 1, dtype=torch.int64, device="cuda"), **ok),
+                 lambda: B.ds4hc_latent_append8(kv[:, :500], pos, f, cache, cu, lens, table),
+                 lambda: B.ds4hc_latent_append8(kv, pos, f, cache, cu, lens, table.t())):
+        with pytest.raises(ValueError):
+            call()
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        with pytest.raises(B.Ds4hcError):
+            B.ds4hc_latent_attn8(ql, qr, cache, cu, lens, table, scale=scale)

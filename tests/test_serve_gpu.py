@@ -402,6 +402,61 @@ def test_pages_and_verify_in_a_graph():
             assert torch.equal(a, b)
 
 
+def test_verify_two_at_once():
+    """Two calls side by side on two streams, each with a workspace of its own: as one after another."""
+    g = torch.Generator().manual_seed(3)
+    both = []
+    for q_len in ([5] * 20, [3, 9, 1]):
+        n = sum(q_len)
+        p, q = distributions(g, n, 9000)
+        both.append(((p.cuda(), torch.randint(0, 9000, (n,), generator=g).cuda(), i32(sums_of(q_len)), torch.rand(n, generator=g).cuda()),
+                     dict(draft=q.cuda())))
+    want = [B.ds4hc_draft_verify(*a, **kw) for a, kw in both]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = [B.ds4hc_draft_verify(*a, **kw, stream=s) for (a, kw), s in zip(both, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for one, other in zip(got, want) for x, y in zip(one, other))
+
+
+def test_refusals_of_the_binding():
+    dev = "cuda"
+    target, tokens, cu, u = torch.zeros(4, 9, device=dev), torch.zeros(4, dtype=torch.int64, device=dev), i32([0, 2, 4]), torch.zeros(4, device=dev)
+    small = torch.zeros(16, dtype=torch.uint8, device=dev)
+    for call in (lambda: B.ds4hc_draft_verify(target.half(), tokens, cu, u), lambda: B.ds4hc_draft_verify(target.t(), tokens, cu, u),
+                 lambda: B.ds4hc_draft_verify(target, tokens.int(), cu, u), lambda: B.ds4hc_draft_verify(target, tokens[:3], cu, u),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, draft=target, parents=i32([0] * 4)),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, draft=target[:, :8]),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, n_kept=i32([0])),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, workspace=small),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu.cpu(), u),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, path=tokens),
+                 lambda: B.ds4hc_draft_verify(target, tokens, cu, u, n_kept=cu[:2])):
+        with pytest.raises((TypeError, ValueError, B.Ds4hcError)):
+            call()
+    cache = torch.zeros(2, 8, 4, 32, device=dev)
+    table, lens, refs = i32([[-1, -1]] * 2), i32([0, 0]), i32([0] * 8)
+    for call in (lambda: B.ds4hc_cache_compact(cache[..., :30], cu, lens, table, tokens.int(), lens),
+                 lambda: B.ds4hc_cache_compact(cache[..., :3].contiguous(), cu, lens, table, tokens.int(), lens),
+                 lambda: B.ds4hc_cache_compact(cache[:, :, :3].contiguous(), cu, lens, table, tokens.int(), lens),
+                 lambda: B.ds4hc_cache_compact(cache[0, 0], cu, lens, table, tokens.int(), lens),
+                 lambda: B.ds4hc_cache_compact(cache, cu, lens, table, tokens, lens),
+                 lambda: B.ds4hc_cache_compact(cache[:0], cu, lens, table, tokens.int(), lens),
+                 lambda: B.ds4hc_pages_copy(cache, tokens.int()), lambda: B.ds4hc_pages_copy(cache, tokens.view(2, 2)),
+                 lambda: B.ds4hc_pages_copy(cache.transpose(1, 2), i32([[0, 1]])),
+                 lambda: B.ds4hc_pages_resize(table, lens, refs, 3, i32([0]), i32([1])),
+                 lambda: B.ds4hc_pages_resize(table, lens, refs, 4, i32([0]), i32([1, 2])),
+                 lambda: B.ds4hc_pages_resize(table, lens[:1], refs, 4, i32([0]), i32([1])),
+                 lambda: B.ds4hc_pages_resize(table, lens, refs, 4, i32([0]), lens[:1]),
+                 lambda: B.ds4hc_pages_resize(table, lens, refs, 4, i32([0]), i32([1]), workspace=small),
+                 lambda: B.ds4hc_pages_fork(table, lens, refs, 4, i32([0]), i32([1]).long()),
+                 lambda: B.ds4hc_pages_fork(table.t(), lens, refs, 4, i32([0]), i32([1]))):
+        with pytest.raises((TypeError, ValueError, B.Ds4hcError)):
+            call()
+    assert (lens == 0).all() and (refs == 0).all() and (table == -1).all()
+
+
 # ------------------------------------------------------------------ all of them
 
 @pytest.mark.parametrize("trees", [False, True])
