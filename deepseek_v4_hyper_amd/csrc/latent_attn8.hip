@@ -696,16 +696,24 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
     }
 }
 
-// How a call is run: tiles and clusters by the average rows of a sequence, as for the 16-bit cache.
+// How a call is run, by the average rows of a sequence. Up to 64: a tile of them each. More, with latents of 512: tiles of 64
+// rows in clusters of two, of which a cut leaves half the bytes of sums that it leaves of 128 rows; unless there are so many
+// rows that most tiles are cut little, where 128 rows keep the matrix unit better fed. Of 128 rows and of 64 (whole calls, us):
+// 8 trees of up to 40 tokens x 16 heads, float16, 78 and 68, 24 chains of 4 tokens x 128 heads 84 and 80, 32 over up to
+// 2048 88 and 69, one token over 131000 79 and 71, 64 x 128 heads 120 and 118; 64 x 4 x 128 228 and 236, 24 x 16 x 128 156 and
+// 162, 512 tokens over 4096 580 and 692. Smaller latents have smaller sums: 256 rather 128 rows (64 x 128 heads 72 and 81).
+// Clusters of four: 64 x 4 x 128 322 for one workgroup's 228, trees 84 for 78: they read the cache once, but all of it
+// waits for the slowest, and the caches serve the single ones as well.
 struct Plan8 {
     int rows, members;
 };
 
-Plan8 plan8(const Paged &c, int heads, int64_t N) {
-    const int64_t rows = (N * heads + c.n_seqs - 1) / c.n_seqs;
+Plan8 plan8(const Paged &c, int latent, int heads, int64_t N) {
+    const int64_t all = N * heads, rows = (all + c.n_seqs - 1) / c.n_seqs;
     if (rows <= 32) return {32, 1};
     if (rows <= 64) return {64, 1};
-    return {128, rows <= 128 ? 1 : rows <= 256 ? 2 : 4};
+    if (latent == 512 && all < WORKGROUPS * 128) return {64, 2};
+    return {128, 1};
 }
 
 template <int DT, class S> hipError_t run8(const AttnArgs &a, hipStream_t s) {
@@ -734,12 +742,12 @@ template <int DT> hipError_t run8_latent(const AttnArgs &a, int rows, hipStream_
 }  // namespace
 
 uint64_t attn8_workspace_bytes(const Paged &c, int latent, int heads, int64_t N) {
-    return sizeof(Header) + 2ull * WORKGROUPS * plan8(c, heads, N).rows * (latent + 3) * sizeof(float);
+    return sizeof(Header) + 2ull * WORKGROUPS * plan8(c, latent, heads, N).rows * (latent + 3) * sizeof(float);
 }
 
 hipError_t launch_attn8(const AttnArgs &args, hipStream_t s) {
     AttnArgs a = args;
-    const Plan8 p = plan8(a.c, a.heads, a.N);
+    const Plan8 p = plan8(a.c, a.latent, a.heads, a.N);
     a.members = p.members;
     return a.dt == DT_BF16 ? run8_latent<DT_BF16>(a, p.rows, s) : run8_latent<DT_F16>(a, p.rows, s);
 }
