@@ -46,7 +46,11 @@ template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape8 {
     static constexpr int BLOCKS = DBLOCKS / SETS, BLOCK_BYTES = 16 * 64 * 4;
     static constexpr int END_BYTES = SETS == 1 ? WAVES * 32 * BLOCKS * 64 : WAVES * (BLOCKS * BLOCK_BYTES + 384);
     static constexpr int RING_BYTES = BUFS * TILE_BYTES > END_BYTES ? BUFS * TILE_BYTES : END_BYTES;
+    // the queries, on their way to registers: behind the first tile, or (of 128 rows) where it will be
+    static constexpr int QUERY_BYTES = LATENT * 2, QUERY_AT = SETS == 1 ? 0 : TILE_BYTES, QUERY_ROWS = 1024 / QUERY_BYTES;
+    static constexpr int QUERY_LOADS = 32 / SETS / QUERY_ROWS;
     static_assert(GROUPS * 16 * WAVES == TOKENS && LOADS_LATENT * ROWS_A_LOAD == 16, "the waves load alike");
+    static_assert(QUERY_AT + ROWS * QUERY_BYTES <= RING_BYTES, "the queries' place");
 };
 
 // f(0) .. f(N - 1), each with its number as a constant.
@@ -191,22 +195,35 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         const int row0 = row_tile * S::ROWS + row_wave * 32;
         const int tok = min(row0 + (lane & 31), n_rows - 1) / a.heads;  // rows behind the last repeat it
         u32x4_t q[S::KLATENT];
-        u32x4_t rope[LATENT_ROPE / 16];
-        auto load_queries = [&]() {  // (they are there once the block table's entries are, before the first tile's loads)
-            const int head = min(row0 + (lane & 31), n_rows - 1) - tok * a.heads;
-            const elem_t<DT> *ql = static_cast<const elem_t<DT> *>(a.ql) + (int64_t)(q0 + tok) * a.ql_token + head * a.ql_head + (lane >> 5) * 16;
-            const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head + (lane >> 5) * 8;
+        // They come through LDS, by loads of whole lines: a lane's own 16 bytes of a row each, straight to registers, take the
+        // texture unit 4 us longer. Chunk c of 16 bytes of row r lies at chunk c ^ (r % 16).
+        const uint32_t ring_at = lds_address(ring);
+        auto load_queries = [&]() {
+            const int l = lane_here(), head = min(row0 + (l & 31), n_rows - 1) - tok * a.heads;
+            const int64_t o = (int64_t)(q0 + tok) * a.ql_token + head * a.ql_head;
+            const char *ql = static_cast<const char *>(a.ql);
+            constexpr int CHUNKS = S::QUERY_BYTES / 16;
+            const uint32_t first = S::SETS == 1 ? 0 : set * 16, to = (uint32_t)uniform((int)(ring_at + S::QUERY_AT + (row_wave * 32 + first) * S::QUERY_BYTES));
+            for_each<S::QUERY_LOADS>([&](auto nth) {
+                const uint32_t r = nth * S::QUERY_ROWS + l / CHUNKS, at = ((l % CHUNKS) ^ (r & 15)) << 4;
+                const int64_t row = (int64_t)(uint32_t)from_lane((int)(uint32_t)o, first + r) | (int64_t)from_lane((int)(o >> 32), first + r) << 32;
+                load_to_lds16(ql + row * 2 + at, to + nth * 1024, ~0ull);
+            });
+            const elem_t<DT> *qr = static_cast<const elem_t<DT> *>(a.qr) + (int64_t)(q0 + tok) * a.qr_token + head * a.qr_head + (l >> 5) * 8;
 #pragma unroll
-            for (int k = 0; k < S::KLATENT; ++k)
-                q[k] = *reinterpret_cast<const u32x4_t *>(ql + (k >> 1) * 32 + (k & 1) * 8);
-#pragma unroll
-            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope[k] = *reinterpret_cast<const u32x4_t *>(qr + k * 16);
+            for (int k = 0; k < LATENT_ROPE / 16; ++k)
+                load_to_lds16(reinterpret_cast<const char *>(qr + k * 16), (uint32_t)uniform((int)lds_address(rope_queries[wave][k])), ~0ull);
         };
-        auto queries_loaded = [&]() {
+        auto read_queries = [&]() {
+            const uint32_t l = lane_here(), x = ((l >> 5) * 2) ^ (l & 15);
+            const DS4HC_LDS char *row = (const DS4HC_LDS char *)(uintptr_t)(ring_at + S::QUERY_AT + (row_wave * 32 + (l & 31)) * S::QUERY_BYTES);
+#pragma unroll
+            for (int k = 0; k < S::KLATENT; ++k) {
+                const uint32_t c = (k >> 1) * 4 + (k & 1);  // (bit 1: the lane's half)
+                q[k] = lds_read16(row + ((x ^ (c & 15)) << 4) + (c >> 4) * 256);
+            }
 #pragma unroll
             for (int k = 0; k < S::KLATENT; ++k) loaded(q[k]);
-#pragma unroll
-            for (int k = 0; k < LATENT_ROPE / 16; ++k) rope_queries[wave][k][lane_here()] = rope[k];
         };
         float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
         float sum = 0.f, used = 0.f;        // of the weights, and of the weights as they were rounded
@@ -576,17 +593,25 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         // tile t - 1 when they meet at the barrier of tile t, so its buffer takes tile t + 2.
         static_assert(S::BUFS == 3, "two tiles on their way");
         wait_and_barrier<63>();  // the last part's reads of the ring
-        const uint32_t ring_at = lds_address(ring);
         load_queries();
         Where now = look_up(t_first), next = look_up(t_first + 1);
+        if constexpr (S::SETS == 1) {
+            wait_and_barrier<0>();
+            read_queries();
+            wait_and_barrier<63>();
+        }
         buffer_t buffers[S::GROUPS];
         buffers_of(now, true, buffers);
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i) load(i, now, buffers, place(ring_at));
+        if constexpr (S::SETS == 2) {
+            wait_and_barrier<S::LOADS>();  // the queries are there, of both sets
+            read_queries();
+            wait_and_barrier<63>();  // and read: their place is the second tile's
+        }
         buffers_of(next, n > 1, buffers);
 #pragma unroll
         for (int i = 0; i < S::LOADS; ++i) load(i, next, buffers, place(ring_at + S::TILE_BYTES));
-        queries_loaded();
         uint64_t ok = now.ok, ok_next = next.ok;
         uint32_t at = 0;
         for (int i = 0; i < n; ++i) {
