@@ -7,13 +7,13 @@
 // with its sums in its 256 accumulation registers. A wave widens what it reads to 16 bits, which is exact.
 // A token's power of 2 scales its whole latent, so it goes into the logit's operand, and for the
 // second product into the weight: out = sum_j p_j c8_j / sum_j p_j 2^(127 - s_j), p_j = w_j 2^(s_j - 127).
-// What bounds it: with up to 32 rows a sequence a tile takes 2.1 us of the 1.75 that its bytes need at 6 TB/s. With 128
-// rows it takes 4.1: 1700 instructions of the one wave a SIMD has registers for (512 of them widen), a third of which fit
-// beside its 136 products (4350 cycles). Beside the tiles a workgroup needs some 15 us: its work, the queries, the first
-// tile's way (7), the part of the sums behind the last (4).
-// Measured (latent 512, bf16, both kernels in a graph): 128 sequences of up to 8192 tokens x 16 heads 107 us (97 and
-// 10; 3.1 TB/s), 64 x 128 heads 118 us (94 and 24), 24 chains of 4 tokens over up to 4096 95 us, one token of 128
-// heads over 131000 79 us, 512 tokens over 4096 590 us. The 16-bit cache: 64 x 128 heads 140, chains 112.
+// What bounds it: a tile takes 2.1 us. With up to 32 rows a sequence its bytes need 1.75 of that at 6 TB/s; with 64 rows
+// it is instructions of the one wave a SIMD has registers for: in 64 tokens by 32 rows 1700 (512 of them widen), a third of
+// which fit beside its 136 products (4350 cycles of 9000). Beside the tiles a workgroup needs some 10 us: its work, the
+// queries, the first tile's way, the part of the sums behind the last.
+// Measured (latent 512, bf16, both kernels in a graph): 128 sequences of up to 8192 tokens x 16 heads 108 us (98 and
+// 10; 3.1 TB/s), 64 x 128 heads 114 us (99 and 15), 24 chains of 4 tokens over up to 4096 77 us, one token of 128
+// heads over 131000 68 us, 512 tokens over 4096 594 us. The 16-bit cache: 64 x 128 heads 140, chains 112.
 // Products of e4m3 values as they are (queries and weights as two such numbers) take the same time within 5 %: they need
 // no widening but have to split the weights, and of 64 products the matrix unit keeps what lies within 2^-13 of the
 // largest, which takes the error of lse from 1e-8 to 5e-6.
