@@ -382,6 +382,31 @@ def test_attn8_small_pages(dtype, heads, latent, page, q_len, kv_len):
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("page,q_len,kv_len,words", [(64, [200, 60, 1, 9], [260, 700, 65, 9], 0), (4, [256], [300], 4),
+                                                     (16, [64, 64, 64, 64, 2], [64, 1000, 129, 2000, 3000], 1)])
+def test_attn8_many_rows(dtype, page, q_len, kv_len, words):
+    """Calls of 32768 rows and more, which are run by tiles of 128 rows: written whole, and cut between workgroups; then with
+    a token that is NaN, which rows behind it see and others do not."""
+    bt = Batch8(109, q_len, kv_len, page, 512, dtype)
+    ql, qr = bt.queries(128)
+    assert bt.N * 128 >= 32768
+    tree = random_tree(bt.g, q_len, words) if words else None
+    out, lse = run_attn8(bt, ql, qr, 0.07, tree)
+    refs = bt.reference(ql, qr, 0.07, tree)
+    for t, (ref, n) in enumerate(refs):
+        assert_attention(out[t].cpu(), lse[t].cpu(), ref, n, dtype, f"token {t}")
+    bad = q_len[0] // 2
+    bt.rows8.view(-1, 656)[bt.rows(0, kv_len[0])[kv_len[0] - q_len[0] + bad], 77] = 0x7F
+    out, lse = run_attn8(bt, ql, qr, 0.07, tree)
+    for t, (ref, n) in enumerate(refs):
+        sees = t < q_len[0] and (t >= bad if tree is None else bool((int(tree[t, bad // 64]) >> (bad % 64)) & 1))
+        if sees:
+            assert not torch.isfinite(out[t].float()).all(-1).any()
+        else:
+            assert_attention(out[t].cpu(), lse[t].cpu(), ref, n, dtype, f"token {t}")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("heads", [1, 40, 128])
 def test_attn8_one_token_seen_gives_its_values(dtype, heads):
     """A row that sees one token alone has its values, whatever its logit and power of 2 are: the rounded weight's product with
