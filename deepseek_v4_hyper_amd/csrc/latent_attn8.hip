@@ -28,9 +28,8 @@ namespace {
 template <int LATENT_, int ROW_WAVES_, int SETS_> struct Shape8 {
     static constexpr int LATENT = LATENT_, ROW_WAVES = ROW_WAVES_, SETS = SETS_;
     static constexpr int TOKENS = 64, BUFS = 3, STEPS = TOKENS / SETS / 32;
-    // (EXTRA and the share that it may take: 8 and a quarter, 6 and a half, 8 and a half, all: 128 sequences of up to 8192 tokens
-    // x 16 heads 105, 106, 105, 105 us; 64 x 128 heads 122, 114, 114, 114; 24 chains over up to 4096 98, 91, 91, 93; trees
-    // 79, 73, 73, 72, float16 78, 80, 80, 84; latent 128 54.6, 56.8, 56.3, 56.0)
+    // (EXTRA and the share that it may take: 4 and a half, 5 and a half, 5 and all take 24 calls of 1 to 256 sequences of up to
+    // 8192 tokens, all tile shapes, 1.000, 0.997 and 1.006 of the time, single ones 0.96 to 1.05)
     static constexpr int EXTRA = 6, EXTRA_OF = 2;
     static constexpr int WAVES = ROW_WAVES * SETS, THREADS = WAVES * 64;
     static constexpr int ROWS = ROW_WAVES * 32;
