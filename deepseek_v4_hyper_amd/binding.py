@@ -675,7 +675,7 @@ def _append(eight, kv, positions, inv_freq, cache, cu_q, kv_len, block_table, no
     here = _device(stream)
     c = _paged(cache, cu_q, kv_len, block_table, here, eight)
     src = _any_code(kv, "kv")
-    N, D = kv.shape[0], c.d_latent + 64
+    N, D = kv.shape[0], cache.shape[2] if eight is None else cache.shape[2] - 80
     _rows(kv, (N, D), kv.dtype, "kv", here)
     _dense(positions, (N,), torch.int64, "positions", here)
     _dense(inv_freq, (32,), torch.float64, "inv_freq", here)
