@@ -77,6 +77,9 @@ template <int DT> __device__ __forceinline__ int scale_byte(uint32_t word) {
     return min(max((int)(word & 255), MIN), MAX);
 }
 __device__ __forceinline__ bool scale_is_nan(uint32_t word) { return (word & 255) == SCALE_NAN; }
+// In bfloat16 a weight times a power below 2^-63 may be rounded to few of its bits, or none: they end at 2^-133, and a latent
+// of zeros has 2^-117. Such a token adds next to nothing to a row's values, but its weight counts in what divides them.
+constexpr uint32_t SCALE_LOW = 64;
 template <int DT> __device__ __forceinline__ float scale_of(uint32_t word) {
     return scale_is_nan(word) ? NAN : __uint_as_float((uint32_t)scale_byte<DT>(word) << 23);
 }
@@ -227,6 +230,7 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         float top = -INFINITY, from = 0.f;  // running maximum less LIFT (what is subtracted: 0 if there is none)
         float sum = 0.f, used = 0.f;        // of the weights, and of the weights as they were rounded
         int least = 255, most = 0;          // float16: scale bytes so far
+        uint32_t low = 255;                 // bfloat16: the lowest of the lane's tokens
         acc16_t acc[S::DBLOCKS];
 #pragma unroll
         for (int d = 0; d < S::DBLOCKS; ++d) {
@@ -362,7 +366,10 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
             const int l = lane_here(), lr = l & 31, lh = l >> 5;
             const uint32_t own_scale = scale_of_token(l);
             units[wave][l] = scale_of<DT>(own_scale);
-            if constexpr (DT == DT_BF16) inverses[wave][l] = (uint16_t)((254 - scale_byte<DT>(own_scale)) << 7);
+            if constexpr (DT == DT_BF16) {
+                low = min(low, own_scale & 255);
+                inverses[wave][l] = (uint16_t)((254 - scale_byte<DT>(own_scale)) << 7);
+            }
             if constexpr (DT == DT_F16) {
                 powers[wave][l] = scale_is_nan(own_scale) ? NAN : (float)(scale_byte<DT>(own_scale) - 127);
                 const int byte = scale_byte<DT>(own_scale);
@@ -630,9 +637,11 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
         const bool whole = t_first == 0 && n == sq.kv_tiles, mine = my_row < n_rows;  // (a part's rows behind the last: never looked at)
         const int in = my_row - row_tile * S::ROWS;
         float *part = part_at<S>(a, cluster, part_of_first ? 0 : 1, member);
-        // In float16 a token whose power is far below the others' may keep nothing of a weight that counts, so where they
-        // differ by more than 2^6 the sum before the rounding is what divides.
-        if (DT == DT_F16 && most - least > 6) used = sum;
+        // A token whose power is far below the others' (float16), or far below 1 (bfloat16), may keep nothing of a weight that
+        // counts, so where they differ by more than 2^6, or one is below SCALE_LOW, the sum before the rounding is what divides.
+        // (In bfloat16 leaving such tokens alone out of the rounded sum takes a second branch beside a tile's products, up to 1.4 %
+        // of a call for up to 0.5.)
+        if (DT == DT_F16 ? most - least > 6 : __any(low < SCALE_LOW)) used = sum;
         float all = sum_halves(sum), all_used = sum_halves(used);
         // the blocks of the output that this wave finishes: all, or with two sets its half
         constexpr int BLOCKS = S::BLOCKS, BLOCK_BYTES = S::BLOCK_BYTES;

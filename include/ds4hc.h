@@ -524,8 +524,9 @@ ds4hc_status ds4hc_latent_append8(const ds4hc_paged_cache *c, int64_t N, ds4hc_d
  * Products are of 16-bit values (the cached ones exact in bfloat16, in float16 as far as its range
  * goes: beyond 65504 infinite, below 2^-24 gone) and sums float32. A weight times its token's power of
  * 2 is rounded to 16 bits for the second product, and the row divided by the sum of the weights as that
- * leaves them (in float16 only where a row's powers lie within 2^6 of one another); the rest as for
- * ds4hc_latent_attn.
+ * leaves them, or, where these would not count in full, by the sum before the rounding: in float16 where
+ * the powers that a workgroup meets lie more than 2^6 apart, in bfloat16 where one is below 2^-63 (that of
+ * a latent of zeros is 2^-117). The rest as for ds4hc_latent_attn.
  */
 ds4hc_status ds4hc_latent_attn8(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
                                 const void *q_latent, ds4hc_strides q_latent_strides,
