@@ -69,11 +69,11 @@ template <int CHUNKS> __device__ __forceinline__ int swz8(int r) {
 __device__ __forceinline__ int swz8_rope(int r) { return (r >> 1) & 7; }
 
 // Scale bytes that the append writes; others but 255, which marks a token that is not finite, are taken
-// as the nearest of these. With float16 operands all values are below its smallest number at 87 (448 x 2^-40),
-// and half of the codes beyond its largest at 143.
+// as the nearest of these. With float16 operands the ends may lie nearer: at 87 all values are below its smallest
+// number (448 x 2^-40), at 152 all but zeros beyond its largest (2^-9 x 2^25).
 constexpr int SCALE_NAN = 255;
 template <int DT> __device__ __forceinline__ int scale_byte(uint32_t word) {
-    constexpr int MIN = DT == DT_F16 ? 87 : 10, MAX = DT == DT_F16 ? 143 : 246;
+    constexpr int MIN = DT == DT_F16 ? 87 : 10, MAX = DT == DT_F16 ? 152 : 246;
     return min(max((int)(word & 255), MIN), MAX);
 }
 __device__ __forceinline__ bool scale_is_nan(uint32_t word) { return (word & 255) == SCALE_NAN; }

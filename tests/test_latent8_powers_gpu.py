@@ -7,7 +7,7 @@ import torch
 
 from deepseek_v4_hyper_amd import binding as B
 from hc_testlib import say
-from site_testlib import E32, assert_attention
+from site_testlib import E32, assert_attention, attend64
 
 pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
@@ -69,3 +69,36 @@ def test_attn8_tokens_that_weigh_but_add_nothing(dtype, kind, power, seqs, heads
     ref = [t.cpu() for t in (want, x + torch.log1p(rest), want.abs(), (latent + 72) * E32 * x)]
     for b in range(0, seqs, 17):
         assert_attention(out[b].cpu(), lse[b].cpu(), ref, [n + 1] * heads, dtype, f"sequence {b}")
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_attn8_every_scale_byte(dtype, heads):
+    """A sequence for each scale byte, of one token with values of +-2^-9 times its power, the smallest there are: bytes outside
+    10..246 are taken as the nearest of these, values are exact, in float16 infinite beyond 65504, and 255 is a NaN. (Queries are
+    zeros where the values are beyond 2^16: logits beyond 2^30 are not promised.)"""
+    say(f"[gpu] attn8 scale bytes {dtype} heads={heads}")
+    page, d, n = 16, 128, 256
+    cache = torch.full((n, page, d + 144), 0x7F, dtype=torch.uint8)
+    cache[:, 0] = 0
+    cache[:, 0, 0:d:3], cache[:, 0, 1:d:3] = 0x01, 0x81
+    cache[:, 0, d + 128] = torch.arange(n).to(torch.uint8)
+    cache[:, 1:, d + 128] = 255
+    ql, qr = torch.zeros(n, heads, d, dtype=dtype), torch.zeros(n, heads, 64, dtype=dtype)
+    ql[:153, :, 0] = 2.0 ** -12 * torch.linspace(0.5, 1.0, heads)
+    out, lse = B.ds4hc_latent_attn8(ql.cuda(), qr.cuda(), cache.cuda(), torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+                                    i32([1] * n), torch.arange(n, dtype=torch.int32, device="cuda")[:, None].contiguous(), scale=1.0,
+                                    want_lse=True)
+    out, lse = out.cpu(), lse.cpu()
+    for b in range(n):
+        value = 2.0 ** -9 * 2.0 ** (min(max(b, 10), 246) - 127)
+        if b == 255 or dtype == HF and value > 65504:
+            assert not torch.isfinite(out[b].float()).all(-1).any(), b
+            continue
+        key = torch.zeros(1, d + 64, dtype=torch.float64)
+        key[0, 0:d:3], key[0, 1:d:3] = value, -value
+        ref = attend64(torch.cat((ql[b], qr[b]), -1), key, key[:, :d], torch.ones(heads, 1, dtype=torch.bool), 1.0)
+        # (half of float16's smallest number, where values and results are multiples of that)
+        small = 2.0 ** -25 if dtype == HF else 0.0
+        keep = (out[b].double() - ref[0]).abs() > small
+        assert_attention(torch.where(keep, out[b].double(), ref[0]), lse[b], ref, [1] * heads, dtype, f"scale byte {b}")
