@@ -984,7 +984,9 @@ def ds4hc_pages_resize(block_table, kv_len, refs, page_size, slots, lengths, *, 
                        stream=None):
     """New lengths for the given slots: takes free pages, or gives pages back. block_table [slots, max_pages], kv_len
     [slots] and refs [pages] int32 are changed in place; slots [n] and lengths [n] int32. Returns (copies [n, 2] int32 for
-    ds4hc_pages_copy, to be run before anything else is written to the pages; status [n] int32: DS4HC_PAGES_*)."""
+    ds4hc_pages_copy, to be run before anything else is written to the pages; status [n] int32: DS4HC_PAGES_*). A slot whose
+    status is not DS4HC_PAGES_DONE keeps its length and has no room: until it has, the operators of the step are given 0 as
+    its kv_len, torch.where(status == DS4HC_PAGES_DONE, kv_len, 0), which leaves its context and pages as they are."""
     torch = _torch()
     if not getattr(block_table, "is_cuda", False):
         _tensors(block_table=block_table)

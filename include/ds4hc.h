@@ -542,9 +542,14 @@ size_t ds4hc_latent_attn8_workspace_bytes(const ds4hc_paged_cache *c, int64_t N,
  * pages that hold them. One step of a serving program with drafts is
  *   ds4hc_pages_resize (room for the drafts), per layer an append and an attention,
  *   ds4hc_draft_verify, ds4hc_cache_compact (trees), ds4hc_pages_resize (what was accepted),
- * all on one stream and without a look at the results on the host. What device arrays hold
- * is checked in the kernels, as above: no value in them makes a kernel read or write outside
- * the arrays given.
+ * all on one stream and without a look at the results on the host. A sequence whose item of the first
+ * resize is not DS4HC_PAGES_DONE has its old length and no room for its drafts: appended all the same they would
+ * be written over the last tokens of its context. The operators between the two resizes are given 0 as
+ * the kv_len of such a sequence (kv_len where status is DS4HC_PAGES_DONE, else 0: computed on the device). Then the
+ * append and the compaction pass its tokens over, the attention gives zeros, what the verification
+ * says of it is to be left aside, and the last resize is given the length that it has.
+ * What device arrays hold is checked in the kernels, as above: no value in them makes a kernel read
+ * or write outside the arrays given.
  * ---------------------------------------------------------------------------
  */
 
@@ -608,8 +613,8 @@ typedef struct {
  * ds4hc_cache_compact -- moves accepted tokens to their places: in every layer, for sequence b
  * and i < n_keep[b], the row of the call's token keep[cu_q[b] + i] of b goes to the place of the
  * call's token i of b (token i of the call's q_len for b is token kv_len[b] - q_len + i of b).
- * keep[cu_q[b]] .. must rise strictly; entries outside [0, q_len) and places that are not in the
- * cache are passed over. Sequences whose pages are written may share none of them.
+ * keep[cu_q[b]] .. must rise strictly; entries outside [0, q_len), and places before token 0 of a
+ * sequence (q_len > kv_len) or not in the cache, are passed over. Sequences whose pages are written may share none of them.
  *   cu_q [n_seqs + 1], kv_len [n_seqs], block_table [n_seqs, max_pages], keep [N],
  *   n_keep [n_seqs] int32 (read). N <= 2^24, n_seqs <= 65535, max_pages as for ds4hc_paged_cache.
  */
@@ -642,8 +647,8 @@ typedef struct {
 
 /* What became of an item: */
 #define DS4HC_PAGES_DONE 0
-#define DS4HC_PAGES_SHORT 1   /* too few free pages: left as it was */
-#define DS4HC_PAGES_INVALID 2 /* left as it was: see there */
+#define DS4HC_PAGES_SHORT 1   /* too few free pages: the slot is left as it was, its kv_len too */
+#define DS4HC_PAGES_INVALID 2 /* left as it was, too: see there */
 
 /*
  * ds4hc_pages_resize -- new lengths for n of the slots. A slot that needs fewer pages gives those
