@@ -13,8 +13,8 @@ constexpr int THREADS = 256;
 constexpr int AT_ONCE = 8;  // rows in flight
 
 // A thread takes the same 16 bytes of every row of a sequence, in one layer, and moves them in the order of
-// the kept tokens: `keep` rises, so what it reads was written by none of its own earlier moves (the source lies
-// at or behind the target, and in front of all later sources), and nobody else touches its bytes. AT_ONCE loads are
+// the kept tokens: `keep` rises and entries that do not lie behind their targets are passed over, so what it reads was
+// written by none of its own earlier moves, and nobody else touches its bytes. AT_ONCE loads are
 // issued before their stores. Grid (layers x columns, sequences). 64 sequences, up to 8 rows of 656 bytes in 43 layers:
 // 5.0 us, 3.3 TB/s; one sequence and layer 2.6 us.
 __global__ __launch_bounds__(THREADS) void compact_kernel(CompactArgs a) {
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(THREADS) void compact_kernel(CompactArgs a) {
             int source = -1, target = -1;
             if (i < kept) {
                 const int k = a.keep[t0 + i];
-                if (k >= 0 && k < few && k != i) {
+                if (k > i && k < few) {
                     source = place(k);
                     target = place(i);
                 }

@@ -613,8 +613,8 @@ typedef struct {
  * ds4hc_cache_compact -- moves accepted tokens to their places: in every layer, for sequence b
  * and i < n_keep[b], the row of the call's token keep[cu_q[b] + i] of b goes to the place of the
  * call's token i of b (token i of the call's q_len for b is token kv_len[b] - q_len + i of b).
- * keep[cu_q[b]] .. must rise strictly; entries outside [0, q_len), and places before token 0 of a
- * sequence (q_len > kv_len) or not in the cache, are passed over. Sequences whose pages are written may share none of them.
+ * keep[cu_q[b]] .. must rise strictly; entries outside [i, q_len) (no token moves to a later place), and
+ * places before token 0 of a sequence (q_len > kv_len) or not in the cache, are passed over. Sequences whose pages are written may share none of them.
  *   cu_q [n_seqs + 1], kv_len [n_seqs], block_table [n_seqs, max_pages], keep [N],
  *   n_keep [n_seqs] int32 (read). N <= 2^24, n_seqs <= 65535, max_pages as for ds4hc_paged_cache.
  */

@@ -236,6 +236,22 @@ def test_compact_passes_over_what_is_not_there():
     assert torch.equal(dev, before)
 
 
+def test_compact_moves_no_row_up():
+    """A list that rises from an entry below 0 has entries smaller than their places: no row goes to a later place, where it
+    would meet rows that are still to be moved, and those that follow are moved as ever."""
+    page, few = 16, 40
+    cache = torch.arange(4 * page * 16).remainder(251).to(torch.uint8).view(1, 4, page, 16)
+    for keep, moves in ((list(range(-1, few - 1)), []), (list(range(-20, few - 20)), []),
+                        ([-3, -2, -1, 0, 1, 5, 6, 9] + list(range(20, 40)), [(6, 6), (7, 9)] + [(8 + i, 20 + i) for i in range(20)])):
+        ref = cache.clone().view(-1, 16)
+        for to, source in moves:
+            ref[10 + to] = cache.view(-1, 16)[10 + source]
+        dev = cache.cuda()
+        B.ds4hc_cache_compact(dev, i32([0, few]), i32([few + 10]), i32([[0, 1, 2, 3]]), i32(keep + [0] * (few - len(keep))),
+                              i32([len(keep)]))
+        assert torch.equal(dev.cpu().view(-1, 16), ref)
+
+
 def test_compact_offsets_past_32_bits():
     """Layers far apart (their strides pass 2^32 bytes) and rows past 2^32 bytes within one."""
     n_pages, page = 60000, 64
