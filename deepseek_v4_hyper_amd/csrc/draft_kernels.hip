@@ -4,6 +4,8 @@
 // token kept: whether a token is accepted takes single elements. Everything is in 64 bits: the sums of
 // a vocabulary's float32 weights decide between neighbours whose borders lie 1e-5 of the total apart and less,
 // and one in a hundred of 32-bit sums would choose another.
+#include "ds4hc.h"
+
 #include "latent_device.hpp"
 #include "serve_launch.hpp"
 
@@ -11,7 +13,7 @@ namespace ds4hc {
 
 namespace {
 
-constexpr int NODES = 1024;  // tokens of a sequence that are looked at
+constexpr int NODES = DS4HC_VERIFY_MAX_TOKENS;  // of a sequence
 constexpr int WIDE = 256, WAVES = WIDE / 64, LAST = 1024;  // threads of a workgroup: of the sums, of the choice
 constexpr int CHUNK_STEP = 1024, CHUNK_MOST = 16384;       // elements of a workgroup, a quarter of them a wave
 constexpr int GOAL = 1024;   // workgroups that sum

@@ -1,5 +1,7 @@
 // page_kernels.hip -- pages of paged caches: who has which (taking, sharing and giving back), and the
 // moves of whole pages and of single rows.
+#include "ds4hc.h"
+
 #include "latent_device.hpp"
 #include "serve_launch.hpp"
 
@@ -242,9 +244,10 @@ __global__ __launch_bounds__(THREADS) void resize_apply_kernel(PoolArgs a) {
     const Space ws = space(a);
     const Item item = ws.items[i];
     const int grows = max(item.has - item.had, 0);
-    const int state = item.has < 0 ? 2 : (int64_t)item.first + grows + item.own > *ws.found && grows + item.own > 0 ? 1 : 0;
+    const bool too_few = (int64_t)item.first + grows + item.own > *ws.found && grows + item.own > 0;
+    const int state = item.has < 0 ? DS4HC_PAGES_INVALID : too_few ? DS4HC_PAGES_SHORT : DS4HC_PAGES_DONE;
     int from = -1, to = -1;
-    if (state == 0) {
+    if (state == DS4HC_PAGES_DONE) {
         const int slot = a.slots[i];
         int32_t *row = a.block_table + (int64_t)slot * a.max_pages;
         if (at == 0) {
@@ -304,7 +307,7 @@ __global__ __launch_bounds__(THREADS) void fork_apply_kernel(PoolArgs a) {
         }
         if (at == 0) a.kv_len[a.slots[i]] = item.had;
     }
-    if (at == 0) a.status[i] = item.has < 0 ? 2 : 0;
+    if (at == 0) a.status[i] = item.has < 0 ? DS4HC_PAGES_INVALID : DS4HC_PAGES_DONE;
 }
 
 // Workgroups a row of the table.

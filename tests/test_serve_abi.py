@@ -3,6 +3,8 @@ everything that needs no GPU. Rejected calls enqueue nothing; the fake device ad
 dereferenced, so these run only where no GPU is visible."""
 import ctypes
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -223,3 +225,11 @@ def test_binding_refuses_host_tensors():
     for call in calls:
         with pytest.raises(ValueError, match="device tensor"):
             call()
+
+
+@pytest.mark.parametrize("name", ["VERIFY_MAX_TOKENS", "PAGES_DONE", "PAGES_SHORT", "PAGES_INVALID"])
+def test_binding_has_the_headers_numbers(name):
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "ds4hc.h")
+    with open(header) as f:
+        said = re.search(rf"#define DS4HC_{name} (\d+)\b", f.read())
+    assert int(said.group(1)) == getattr(B, "DS4HC_" + name)
