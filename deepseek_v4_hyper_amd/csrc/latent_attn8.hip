@@ -7,13 +7,15 @@
 // with its sums in its 256 accumulation registers. A wave widens what it reads to 16 bits, which is exact.
 // A token's power of 2 scales its whole latent, so it goes into the logit's operand, and for the
 // second product into the weight: out = sum_j p_j c8_j / sum_j p_j 2^(127 - s_j), p_j = w_j 2^(s_j - 127).
-// What bounds it: a tile takes 2.1 us. With up to 32 rows a sequence its bytes need 1.75 of that at 6 TB/s; with 64 rows
-// it is instructions of the one wave a SIMD has registers for: in 64 tokens by 32 rows 1700 (512 of them widen), a third of
-// which fit beside its 136 products (4350 cycles of 9000). Beside the tiles a workgroup needs some 10 us: its work, the
-// queries, the first tile's way, the part of the sums behind the last.
-// Measured (latent 512, bf16, both kernels in a graph): 128 sequences of up to 8192 tokens x 16 heads 108 us (98 and
-// 10; 3.1 TB/s), 64 x 128 heads 114 us (99 and 15), 24 chains of 4 tokens over up to 4096 77 us, one token of 128
-// heads over 131000 68 us, 512 tokens over 4096 594 us. The 16-bit cache: 64 x 128 heads 140, chains 112.
+// What bounds it (by clock readings in a copy of the kernel): with all workgroups at work a tile takes 2.5 us with up to 32 rows
+// a sequence, of which its bytes need 1.75 at 6 TB/s; with 64 rows 2.7, in float16 3.1, with 128 rows 4.5: instructions of the one
+// wave a SIMD has registers for, in 64 tokens by 32 rows 1700 (512 of them widen), a third of which fit beside its 136
+// products (4350 cycles of 9000). Beside its tiles a workgroup needs 12 to 13 us for a part of the sums: 1.5 to 2.4 to find its work,
+// 1.3 to 1.9 to take it up, 3 to 3.4 for queries and the first page numbers, 0.6 to 2 until the first tile is there, 3.4 to 4.4
+// to store the results. A second part (a third of the workgroups has one) costs 8 to 10 again: nothing of it runs beside tiles.
+// Measured (latent 512, bf16, both kernels in a graph): 128 sequences of up to 8192 tokens x 16 heads 108 us (3.1 TB/s),
+// 64 x 128 heads 113 us, 24 chains of 4 tokens over up to 4096 77 us, one token of 128
+// heads over 131000 68 us, 512 tokens over 4096 594 us. The 16-bit cache: 64 x 128 heads 129, chains 103.
 // Products of e4m3 values as they are (queries and weights as two such numbers) take the same time within 5 %: they need
 // no widening but have to split the weights, and of 64 products the matrix unit keeps what lies within 2^-13 of the
 // largest, which takes the error of lse from 1e-8 to 5e-6.
@@ -731,12 +733,12 @@ __global__ __launch_bounds__(S::THREADS, 1) void attn8_kernel(AttnArgs a) {
 
 // How a call is run, by the average rows of a sequence. Up to 64: a tile of them each. More, with latents of 512: tiles of 64
 // rows in clusters of two, of which a cut leaves half the bytes of sums that it leaves of 128 rows; unless there are so many
-// rows that most tiles are cut little, where 128 rows keep the matrix unit better fed. Of 128 rows and of 64 (whole calls, us):
-// 8 trees of up to 40 tokens x 16 heads, float16, 78 and 68, 24 chains of 4 tokens x 128 heads 84 and 80, 32 over up to
-// 2048 88 and 69, one token over 131000 79 and 71, 64 x 128 heads 120 and 118; 64 x 4 x 128 228 and 236, 24 x 16 x 128 156 and
-// 162, 512 tokens over 4096 580 and 692. Smaller latents have smaller sums: 256 rather 128 rows (64 x 128 heads 72 and 81).
-// Clusters of four: 64 x 4 x 128 322 for one workgroup's 228, trees 84 for 78: they read the cache once, but all of it
-// waits for the slowest, and the caches serve the single ones as well.
+// rows that most tiles are cut little, where 128 rows keep the matrix unit better fed. Of 128 rows, of 64, and of 64 in clusters
+// of four (whole calls in a graph, us; 128 heads unless said): 8 trees of up to 40 tokens x 16 heads, float16, 76, 66 and 68, 24
+// chains of up to 4 tokens 82, 77 and 82, 32 over up to 2048 83, 64 and 70, one token over 131000 78, 68 and 99, 64 x 1 over up to
+// 8192 121, 113 and 186, 64 chains of up to 4 228, 235 and 263, 24 x up to 16 157, 157 and 166, 512 tokens over 4096 594, 680 and 682.
+// Smaller latents have smaller sums: 256 rather 128 rows (64 x 1 72, 80 and 132; 24 chains 53, 57 and 63).
+// Clusters of four read the cache once, but all of it waits for the slowest, and the caches serve the single ones as well.
 struct Plan8 {
     int rows, members;
 };

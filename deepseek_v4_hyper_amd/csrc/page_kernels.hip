@@ -83,8 +83,10 @@ __global__ __launch_bounds__(THREADS) void copy_kernel(Store s, int n, const int
 
 // Two kernels: the first, one workgroup, finds what each item needs and the free pages in ascending order; the
 // second writes tables and counts, all items side by side. Counts change by whole-number atomics alone, in the
-// second kernel, so that results do not depend on an order. 64 slots with up to 128 pages each, of 65536: 8.0 and
-// 3.3 us, chains of latencies. (Both in one kernel, a wave an item: 16 slots with 16 pages 7.2 for 8.4 us, 64 with 16
+// second kernel, so that results do not depend on an order. 64 slots with up to 128 pages each, of 65536: 12.0 and
+// 4.0 us where pages are taken, 3.5 and 3.1 where none are: chains of latencies, and the counts, which one workgroup reads from the
+// first page on until it has found as many free ones as are needed (a call that takes one behind 2^14 used pages 12 us, 2^16 26,
+// 2^18 81, 2^20 318; none 4.9 whatever the pool). (Both in one kernel, a wave an item: 16 slots with 16 pages 7.2 for 8.4 us, 64 with 16
 // 11.3 for 9.1, 256 with 128 37 for 14.)
 constexpr int DECIDE = 1024, WAVES = DECIDE / 64;
 constexpr int SCAN = 16;  // pages a lane: 1024 a wave, 16384 a step of the workgroup

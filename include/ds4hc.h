@@ -526,7 +526,8 @@ ds4hc_status ds4hc_latent_append8(const ds4hc_paged_cache *c, int64_t N, ds4hc_d
  * 2 is rounded to 16 bits for the second product, and the row divided by the sum of the weights as that
  * leaves them, or, where these would not count in full, by the sum before the rounding: in float16 where
  * the powers that a workgroup meets lie more than 2^6 apart, in bfloat16 where one is below 2^-63 (that of
- * a latent of zeros is 2^-117). The rest as for ds4hc_latent_attn.
+ * a latent of zeros is 2^-117). The ends that float16 has for small weights are those of weights times
+ * powers. The rest as for ds4hc_latent_attn.
  */
 ds4hc_status ds4hc_latent_attn8(const ds4hc_paged_cache *c, int64_t N, int32_t heads, float scale,
                                 const void *q_latent, ds4hc_strides q_latent_strides,
