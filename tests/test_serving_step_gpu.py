@@ -111,3 +111,64 @@ def test_a_step_that_finds_too_few_pages(trees, eight):
                 known[b] = torch.cat((known[b], now[b][:, [context[b] + w for w in way]]), 1)
             context[b] = pool.lens[b]
             assert torch.equal(rows_of(b, context[b]), known[b]), (turn, b)
+
+
+def test_a_captured_step_that_finds_too_few_pages():
+    """The step of a chain of 4 for each of three sequences, captured whole: replays that find pages for all, for some and for
+    none, with eager work between them, leave what the eager step leaves."""
+    g = torch.Generator().manual_seed(23)
+    layers, page, seqs, few, heads, vocab, d, pages = 2, 16, 3, 4, 16, 200, 128, 6
+    table, lens, refs = Pool(seqs, 4, pages, page).tensors("cuda")
+    caches = torch.randint(0, 120, (layers, pages, page, d + 144), generator=g, dtype=torch.uint8).cuda()
+    caches[..., d:] = 0
+    caches[..., d + 128] = 120
+    f, cu, slots = B.ds4hc_rope_frequencies(64)[0].cuda(), i32([few * b for b in range(seqs + 1)]), i32(list(range(seqs)))
+    new = torch.randn(layers, seqs * few, d + 64, generator=g).to(BF).cuda()
+    pos = torch.arange(seqs * few).cuda()
+    ql = torch.randn(seqs * few, heads, d, generator=g).to(BF).cuda()
+    qr = torch.randn(seqs * few, heads, 64, generator=g).to(BF).cuda()
+    target, draft = (t.cuda() for t in distributions(g, seqs * few, vocab))
+    tokens, uniform = target.argmax(-1).roll(1), torch.zeros(seqs * few, device="cuda")
+    copies, status, status2 = i32([[0, 0]] * seqs), i32([0] * seqs), i32([0] * seqs)
+    out = torch.zeros(layers, seqs * few, heads, d, dtype=BF, device="cuda")
+    path, kept, following = i32([0] * seqs * few), i32([0] * seqs), torch.zeros(seqs, dtype=torch.int64, device="cuda")
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+
+    def step():
+        B.ds4hc_pages_resize(table, lens, refs, page, slots, lens + few, copies=copies, status=status, workspace=ws)
+        B.ds4hc_pages_copy(caches, copies)
+        done = status == B.DS4HC_PAGES_DONE
+        live = torch.where(done, lens, 0)
+        for layer in range(layers):
+            B.ds4hc_latent_append8(new[layer], pos, f, caches[layer], cu, live, table)
+            B.ds4hc_latent_attn8(ql, qr, caches[layer], cu, live, table, scale=0.1, out=out[layer], workspace=ws)
+        B.ds4hc_draft_verify(target, tokens, cu, uniform, draft=draft, path=path, n_kept=kept, next_token=following, workspace=ws)
+        B.ds4hc_cache_compact(caches, cu, live, table, path, kept)
+        B.ds4hc_pages_resize(table, lens, refs, page, slots, torch.where(done, lens - few + kept, lens), copies=copies,
+                             status=status2, workspace=ws)
+
+    state = (table, lens, refs, caches, out, path, kept, following, status, status2)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    seen = set()
+    for want in ([15, 30, 2], [31, 30, 30], [32, 16, 32], [32, 32, 32], [64, 1, 0]):
+        B.ds4hc_pages_resize(table, lens, refs, page, slots, i32([0] * seqs))
+        _, what = B.ds4hc_pages_resize(table, lens, refs, page, slots, i32(want))
+        assert (what == 0).all() and lens.tolist() == want
+        saved = [t.clone() for t in state]
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [t.clone() for t in state]
+        for t, old in zip(state, saved):
+            t.copy_(old)
+        step()
+        torch.cuda.synchronize()
+        for a, b in zip(state, replayed):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        seen.add(tuple(status.tolist()))
+        for b, was in enumerate(want):
+            assert lens[b].item() == (was + kept[b].item() if status[b].item() == 0 else was)
+    assert {(0, 0, 0), (1, 1, 1)} < seen and len(seen) >= 3
